@@ -65,6 +65,12 @@ extern "C" {
 #define FLIDE_BF16 1
 #define FLIDE_E4M3 2 /* 8-bit e4m3 codes (flide_fork_attn_fp8, flide_quantize_e4m3) */
 
+/* ---- frequency scaling for flide_rope_freqs ----------------------------- */
+#define FLIDE_ROPE_NONE 0
+#define FLIDE_ROPE_LINEAR 1 /* every frequency divided by the factor              */
+#define FLIDE_ROPE_NTK 2    /* the base raised: fast pairs hardly change           */
+#define FLIDE_ROPE_YARN 3   /* pairs that turn often kept, slow ones divided       */
+
 /* ---- flags for flide_fork_attn / flide_fork_gdn ------------------------ */
 #define FLIDE_FLAG_PORTABLE 1 /* force the portable SIMT kernels (any d, any dtype) */
 
@@ -445,6 +451,10 @@ int flide_pool_append_batch(flide_pool *pool, int32_t n, const int32_t *slots,
 /* Returns all blocks of request `slot` to the free list; its length becomes 0.
  * FLIDE_ERR_INVALID for a bad slot. */
 int flide_pool_release(flide_pool *pool, int32_t slot);
+/* Cuts request `slot`'s history to its first `rows` rows (what
+ * flide_history_evict leaves) and returns the blocks past them to the free
+ * list.  FLIDE_ERR_INVALID for a bad slot or rows outside [0, length]. */
+int flide_pool_truncate(flide_pool *pool, int32_t slot, int32_t rows);
 /* History rows held by `slot`; -FLIDE_ERR_INVALID for a bad slot. */
 int32_t flide_pool_length(const flide_pool *pool, int32_t slot);
 /* Blocks on the free list (0 for a NULL pool). */
@@ -487,6 +497,185 @@ int flide_history_gather(int32_t R, const int32_t *req_slot, int32_t max_request
                          int32_t d, int32_t dtype, const float *pool_S, int32_t H, int32_t dk,
                          int32_t dv, int32_t *past_len, void *past_k, void *past_v,
                          int32_t past_rows, float *state_in, int32_t *status, flide_stream stream);
+
+/* ---- speculative decoding over a history ---------------------------------
+ * A step continues each request's history with a root (the tokens committed
+ * since the last step) and drafted tokens below it, as one request tree.  The
+ * calls below are such a step next to fork attention and decision scoring: the
+ * tree's rotary positions, attention of its few tokens over the long history,
+ * verification of the drafted tokens, and a bound on the history's growth.
+ * (The pages keep growing histories -- kongchang.com, closing section;
+ * techfi24.com, "Exact State Forking"; these operators are this library's.)
+ *
+ * Rotation frequencies, host only: freqs[i] (host double[rot_dim / 2]) =
+ * base^(-2 i / rot_dim) radians a position, scaled for contexts of `factor`
+ * times the trained length:
+ *   FLIDE_ROPE_NONE    as they are (factor and what follows ignored)
+ *   FLIDE_ROPE_LINEAR  divided by factor
+ *   FLIDE_ROPE_NTK     base * factor^(rot_dim / (rot_dim - 2)) as the base
+ *   FLIDE_ROPE_YARN    by parts (Peng et al., "YaRN"): a pair that makes at
+ *                      least `fast` turns over orig_len positions is kept, one
+ *                      of at most `slow` turns divided by factor, linearly in
+ *                      between; *mscale = 0.1 ln(factor) + 1
+ * *mscale (host) is 1 otherwise.  2 <= rot_dim <= 1024, even, else
+ * FLIDE_ERR_SHAPE (also for an unknown scaling or a NULL argument); base <= 0,
+ * factor < 1, for YARN orig_len <= 0, slow < 0 or fast <= slow, or a value that
+ * is not finite: FLIDE_ERR_INVALID. */
+int flide_rope_freqs(int32_t rot_dim, double base, int32_t scaling, double factor,
+                     double orig_len, double fast, double slow, double *freqs, float *mscale);
+
+/* Rotary positions: the first rot_dim elements of every head of stream token t
+ * turn pairwise by the angle p freqs[i], p = token_pos[t] + pos_offset[request]:
+ *   a' = mscale (a cos - b sin),  b' = mscale (a sin + b cos)
+ * with (a, b) = elements (i, i + rot_dim / 2), or (2i, 2i + 1) when
+ * `interleaved`; with `transpose` the angles are negated (the rotation's
+ * gradient; its inverse when mscale is 1).  Elements from rot_dim on are copied.
+ *   pos_offset   device int32 [idx->R], may be NULL (zeros): for histories whose
+ *                rows are fewer than their positions (flide_history_evict)
+ *   freqs        device double [rot_dim / 2]
+ *   q, q_out [T, Hq, d], k, k_out [T, Hkv, d] dtype (FLIDE_F32 or FLIDE_BF16);
+ *                q and q_out, or k and k_out, may both be NULL; an output may be
+ *                its input (in place), other overlaps are not allowed
+ * Angles are formed in 64 bits.  Rows past the stream's last token are left as
+ * they were.  rot_dim even, 2 <= rot_dim <= min(d, 1024).  Host errors:
+ * FLIDE_ERR_SHAPE, FLIDE_ERR_CAPACITY (a row of 2^30 elements or more),
+ * FLIDE_ERR_CUDA. */
+int flide_rope(const flide_tree_index *idx, const int32_t *pos_offset, const double *freqs,
+               const void *q, const void *k, void *q_out, void *k_out, int32_t Hq, int32_t Hkv,
+               int32_t d, int32_t rot_dim, int32_t interleaved, int32_t transpose, float mscale,
+               int32_t dtype, flide_stream stream);
+
+/* Bytes of `workspace` that flide_draft_attn needs for an index of these
+ * capacities; 0 for bad arguments. */
+size_t flide_draft_attn_workspace_bytes(int32_t R, int32_t T, int32_t Hq, int32_t Hkv, int32_t d);
+
+/* Attention of a few tokens per request over a long past: the same keys, GQA
+ * and result as flide_fork_attn, with the past cut along its length over the
+ * whole GPU and the pieces joined, where fork attention streams a request's
+ * past through one block per query tile.  Made for requests of up to some
+ * hundred stream tokens (a root and its drafted tree); right for any, but a
+ * token's stream keys are taken one by one, so long roots belong to
+ * flide_fork_attn.
+ *   q [T, Hq, d], k, v [T, Hkv, d], past_k, past_v [past_rows, Hkv, d], out as
+ *          in flide_fork_attn: dtype FLIDE_F32 or FLIDE_BF16, d a multiple of
+ *          32, <= 256; or FLIDE_E4M3 codes with descale (device float[3]) and
+ *          bf16 out as in flide_fork_attn_fp8, d == 128
+ *   lse    float [T, Hq], may be NULL: natural logarithm of the sum of
+ *          exp(scale * score) over the token's keys
+ *   workspace  device, 256-byte aligned, flide_draft_attn_workspace_bytes(idx->R,
+ *          idx->T, Hq, Hkv, d) bytes; one call at a time
+ * Rows past the stream's last token are left as they were.  A key that a row
+ * does not see takes no part in its result, whatever its value.  q, k, v and
+ * the past 16-byte aligned.  The softmax weights are rounded to the input's
+ * precision (e4m3: to half) before they multiply v; their sum is not.
+ * Host errors: FLIDE_ERR_SHAPE, FLIDE_ERR_CAPACITY (workspace too small, more
+ * than 4096 requests, T * Hq past 2^30), FLIDE_ERR_CUDA; device errors as
+ * flide_fork_attn. */
+int flide_draft_attn(const void *q, const void *k, const void *v, const void *past_k,
+                     const void *past_v, int32_t past_rows, const flide_tree_index *idx, int32_t Hq,
+                     int32_t Hkv, int32_t d, int32_t dtype, const float *descale, float scale,
+                     void *out, float *lse, void *workspace, size_t workspace_bytes,
+                     flide_stream stream);
+
+/* The same with the past rows read in place from a block-paged pool, laid out
+ * as for flide_fork_attn_paged but with blocks of any multiple of 16 rows.
+ * Device errors: FLIDE_ERR_INVALID as there. */
+int flide_draft_attn_paged(const void *q, const void *k, const void *v, const void *pool_k,
+                           const void *pool_v, int32_t n_blocks, int32_t block_rows,
+                           const int32_t *block_table, int32_t max_blocks, const int32_t *req_slot,
+                           int32_t n_slots, const flide_tree_index *idx, int32_t Hq, int32_t Hkv,
+                           int32_t d, int32_t dtype, const float *descale, float scale, void *out,
+                           float *lse, void *workspace, size_t workspace_bytes, flide_stream stream);
+
+/* Verification of the drafted tokens, with the random numbers given.  From the
+ * last token of request r's root the drafted continuations of the current
+ * token (the next token of its node, or its children's first tokens in node
+ * order) are tried in turn; the first accepted one becomes the current token.
+ * With p = target row, q = draft row of the current token (the distribution
+ * its continuations were drawn from, independently), after i rejections at it,
+ * continuation x with random number u is accepted when
+ *   u q(x) D_i < p(x) - c_i q(x),  c_0 = 0, D_0 = 1, c_i = c_{i-1} + D_{i-1},
+ *   D_i = sum_v max(p(v) - c_i q(v), 0):
+ * the residual rejection rule, under which the accepted tokens and the next one
+ * are distributed as the target's.  With draft == NULL the continuations are
+ * point masses (the draft's best tokens, distinct among siblings): accepted
+ * when u D < p(x), D = 1 - the sum of the rejected siblings' p; a token that
+ * was already rejected there never is.  Where none is left, the next token is
+ * the first v whose cumulative residual (max(p - c q, 0); point masses: p with
+ * the rejected tokens' entries 0) passes u_next[r] times its sum; p itself if
+ * the residual is empty.
+ *   tokens [T] int32   the stream's token ids (read for branch tokens)
+ *   target, draft [T, V] dtype (FLIDE_F32 or FLIDE_BF16): row t = distribution
+ *                      after stream token t; entries that are not positive
+ *                      numbers count as 0; rows the walk does not reach are not
+ *                      read
+ *   u [T], u_next [R]  float in [0, 1)
+ *   n_accept [R], next_token [R] int32 out; path [T] int32 out: at a request's
+ *                      stream rows, its accepted tokens' stream rows in order,
+ *                      then -1 (rows past the stream's last token are left)
+ * A request without a root token gets 0 and -1.  All arithmetic is in 64 bits.
+ * Device errors in idx->status: FLIDE_ERR_INVALID for a token outside [0, V)
+ * (never accepted), FLIDE_ERR_CAPACITY for more than 4096 nodes in a request
+ * (0 and -1) or 1024 continuations of a token (the rest are not tried).  Host
+ * errors: FLIDE_ERR_SHAPE (also V > 2^26), FLIDE_ERR_CAPACITY (R > 2^24),
+ * FLIDE_ERR_CUDA. */
+int flide_verify_draft(const flide_tree_index *idx, const int32_t *tokens, const void *target,
+                       const void *draft, const float *u, const float *u_next, int32_t V,
+                       int32_t dtype, int32_t *n_accept, int32_t *next_token, int32_t *path,
+                       flide_stream stream);
+
+/* Attention weight of the history rows.  For request r with slot s =
+ * req_slot[r] >= 0, past length P and n root tokens:
+ *   mass_out[s][i] = mass[s][i] + sum_t sum_h exp(scale q_th . k_i - lse[t][h]),
+ *     i < P, over the root's tokens t and all query heads h;
+ *   mass_out[s][P + j] = the same sum for root row j, over the root tokens
+ *     t >= j (the rows flide_history_append gives the history after the step).
+ * Only root tokens count: drafted ones may be rejected, and an accepted token
+ * is a root token of a later step, so each token counts once.
+ *   q [T, Hq, d], k [T, Hkv, d], pool_k, block_table, req_slot, idx and descale
+ *     as given to flide_draft_attn_paged, lse as written by it
+ *   mass, mass_out float [n_slots][max_blocks * block_rows]; mass_out may be
+ *     mass (in place), else entries not named above are left as they were.
+ * Each slot at most once per call (two requests would race for its sums).
+ * Device errors: FLIDE_ERR_INVALID for a bad slot or block,
+ * FLIDE_ERR_CAPACITY where P + n passes max_blocks * block_rows (that request
+ * is skipped).  Host errors as flide_draft_attn_paged. */
+int flide_history_mass(const void *q, const void *k, const float *lse, const void *pool_k,
+                       int32_t n_blocks, int32_t block_rows, const int32_t *block_table,
+                       int32_t max_blocks, const int32_t *req_slot, int32_t n_slots,
+                       const flide_tree_index *idx, int32_t Hq, int32_t Hkv, int32_t d, int32_t dtype,
+                       const float *descale, float scale, const float *mass, float *mass_out,
+                       flide_stream stream);
+
+/* Eviction: cuts every history req_slot[r] (-1: none) that is longer than
+ * `budget` down to that many rows: its first `sinks`, its last `recent`, and of
+ * the rows between them those of largest mass (of equal ones the lowest row; a
+ * NaN counts as the lowest mass).  The kept rows and their masses move, in
+ * order, to history rows 0 .. min(length, budget) - 1 of the same slot in the
+ * destination: dst_k, dst_v through dst_table, and mass_out.
+ *   hist_len  device int32 [n_slots] (not changed; the new lengths are
+ *             min(length, budget): flide_pool_truncate)
+ *   block_table, dst_table  device int32 [n_slots * max_blocks]
+ *   pool_k, pool_v [n_blocks * block_rows, Hkv, d], dst_k, dst_v [dst_blocks *
+ *             block_rows, Hkv, d] dtype; row bytes a multiple of 16 and at most
+ *             2^20
+ *   mass, mass_out float [n_slots][max_blocks * block_rows]
+ *   kept      int32 [R][budget]: the rows kept, ascending, then -1
+ * In place (dst_k == pool_k, dst_v == pool_v, dst_table == block_table,
+ * mass_out == mass), or into blocks that hold none of the histories' rows (of
+ * the same pool or another): any other overlap is not allowed.
+ * Device errors to *status (device int32): FLIDE_ERR_INVALID for a slot >=
+ * n_slots or listed twice, a length outside [0, max_blocks * block_rows] (those
+ * requests are left as they are) or a row without a block.  Host errors:
+ * FLIDE_ERR_SHAPE (also budget <= 0, sinks + recent > budget),
+ * FLIDE_ERR_CAPACITY (more than 4096 requests), FLIDE_ERR_CUDA. */
+int flide_history_evict(int32_t R, const int32_t *req_slot, int32_t n_slots, const int32_t *hist_len,
+                        const int32_t *block_table, int32_t max_blocks, int32_t block_rows,
+                        const void *pool_k, const void *pool_v, int32_t n_blocks, int32_t Hkv,
+                        int32_t d, int32_t dtype, const float *mass, int32_t budget, int32_t sinks,
+                        int32_t recent, void *dst_k, void *dst_v, const int32_t *dst_table,
+                        int32_t dst_blocks, float *mass_out, int32_t *kept, int32_t *status,
+                        flide_stream stream);
 
 /* ---- memory-bounded GDN scheduling ---------------------------------------
  * Memory for cloned states is what limits how many options one call can hold

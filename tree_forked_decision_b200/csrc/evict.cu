@@ -1,0 +1,421 @@
+// evict.cu -- which history rows were looked at, and dropping those that were
+// not.
+//
+// flide_history_mass adds, for every history row i of a request, the attention
+// weight that the step's root tokens (the tokens the step commits; drafted
+// ones may still be rejected) gave it over all query heads:
+//   mass_i += sum_{t in root} sum_h exp(scale q_th . k_i - lse_th),
+// with lse as the step's attention wrote it, so the weights are final and no
+// second softmax is needed.  The root's own rows, which enter the history with
+// this step, start from what they received in it.  A block takes whole rows
+// (all heads), so each sum has one writer and one order.
+//
+// flide_history_evict keeps `budget` rows of each longer history: the first
+// `sinks`, the last `recent`, and the rows of largest mass between them (of
+// equal ones the lowest index).  The kept rows stay in order and move to the
+// front of the destination's blocks, in place if they are the source's.
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+#include "sm100.cuh"
+#include "worklist.cuh"
+
+namespace flide {
+namespace {
+
+constexpr float kLog2eM = 1.4426950408889634f;
+
+struct MassParams {
+  flide_tree_index x;
+  HistoryView hist;
+  const void *q, *k, *pool_k;
+  const float *lse, *mass, *descale;
+  float *mass_out;
+  int Hq, Hkv, G, d;
+  float scale;
+};
+
+template <typename T>
+__device__ __forceinline__ float element(const T *p) { return load_f(p); }
+template <>
+__device__ __forceinline__ float element<uint8_t>(const uint8_t *p) {
+  __nv_fp8_e4m3 c;
+  c.__x = *p;
+  return (float)c;
+}
+
+// Units of a request: its history rows and its root's rows, kMKeys at a time
+// each.  Requests without a slot have no history and take no part.
+constexpr int kMKeys = 32;
+constexpr int kMThreads = 128;
+
+__device__ __forceinline__ int root_tokens(const flide_tree_index &x, int r, int *t0) {
+  const int n0 = x.req_node[r], n1 = x.req_node[r + 1];
+  *t0 = n1 > n0 ? x.node_start[n0] : 0;
+  return n1 > n0 ? x.node_start[n0 + 1] - *t0 : 0;
+}
+
+__device__ __forceinline__ long long mass_units(const MassParams &p, int r, bool report) {
+  const flide_tree_index &x = p.x;
+  const int slot = p.hist.req_slot[r];
+  if (slot < 0) return 0;
+  int t0;
+  long long base;
+  const int root = root_tokens(x, r, &t0);
+  const int n = history_rows(x, p.hist, r, report, &base);
+  if (root == 0) return 0;
+  if (slot >= p.hist.n_slots || n + (long long)root > (long long)p.hist.max_blocks * p.hist.block_rows) {
+    if (report) set_status(x.status, slot >= p.hist.n_slots ? FLIDE_ERR_INVALID : FLIDE_ERR_CAPACITY);
+    return 0;
+  }
+  return (n + kMKeys - 1) / kMKeys + (root + kMKeys - 1) / kMKeys;
+}
+
+// Any element type and head size: a lane per key, the heads and tokens split
+// over the warps.
+template <typename T>
+__global__ void __launch_bounds__(kMThreads) mass_kernel_portable(const MassParams p) {
+  extern __shared__ float smem[];
+  __shared__ long long part[32];
+  __shared__ float sums[kMThreads / 32][kMKeys];
+  const flide_tree_index &x = p.x;
+  if (failed(x.status)) return;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, R = x.R, d = p.d, ld = d + 1;
+  long long *unit0 = reinterpret_cast<long long *>(smem);
+  float *sk = smem + 2 * (R + 1);
+  request_prefix(R, [&](int r) { return mass_units(p, r, blockIdx.x == 0); }, unit0, part);
+  const T *Q = static_cast<const T *>(p.q), *K = static_cast<const T *>(p.k),
+          *Pk = static_cast<const T *>(p.pool_k);
+  const float qk_scale = p.scale * (p.descale ? p.descale[0] * p.descale[1] : 1.f);
+  for (long long u = blockIdx.x; u < unit0[R]; u += gridDim.x) {
+    const int r = request_of(unit0, R, u);
+    int t0;
+    long long slot;
+    const int root = root_tokens(x, r, &t0);
+    const int n = history_rows(x, p.hist, r, false, &slot);
+    slot = p.hist.req_slot[r];
+    const int past_units = (n + kMKeys - 1) / kMKeys;
+    const int c = (int)(u - unit0[r]);
+    const bool fresh = c >= past_units;
+    const int k0 = (fresh ? c - past_units : c) * kMKeys;
+    const int left = min(kMKeys, (fresh ? root : n) - k0);
+    float acc = 0.f;
+    for (int hk = 0; hk < p.Hkv; ++hk) {
+      __syncthreads();
+      for (int kr = warp; kr < left; kr += kMThreads / 32) {
+        const long long row = fresh ? t0 + k0 + kr : history_row(x, p.hist, slot, k0 + kr);
+        const T *src = (fresh ? K : Pk) + ((size_t)max(row, 0ll) * p.Hkv + hk) * d;
+        for (int i = lane; i < d; i += 32) sk[kr * ld + i] = row >= 0 ? element(src + i) : 0.f;
+      }
+      __syncthreads();
+      for (int j = warp; j < root * p.G; j += kMThreads / 32) {
+        const int t = t0 + j / p.G, h = hk * p.G + j % p.G;
+        const T *qr = Q + ((size_t)t * p.Hq + h) * d;
+        float s = 0.f;
+        if (lane < left)
+          for (int i = 0; i < d; ++i) s = fmaf(element(qr + i), sk[lane * ld + i], s);
+        if (lane < left && (!fresh || t0 + k0 + lane <= t))
+          acc += exp2f((s * qk_scale - p.lse[(size_t)t * p.Hq + h]) * kLog2eM);
+      }
+    }
+    sums[warp][lane] = acc;
+    __syncthreads();
+    if (tid < left) {
+      float all = 0.f;
+#pragma unroll
+      for (int w = 0; w < kMThreads / 32; ++w) all += sums[w][tid];
+      const size_t at = (size_t)slot * p.hist.max_blocks * p.hist.block_rows + (fresh ? n : 0) + k0 + tid;
+      p.mass_out[at] = fresh ? all : p.mass[at] + all;
+    }
+  }
+}
+
+template <typename T>
+int mass_launch(const MassParams &p, int sms, cudaStream_t s) {
+  const size_t smem = (size_t)(p.x.R + 1) * 8 + sizeof(float) * kMKeys * (p.d + 1);
+  if (cudaFuncSetAttribute(mass_kernel_portable<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)smem) != cudaSuccess)
+    return FLIDE_ERR_CUDA;
+  mass_kernel_portable<T><<<8 * sms, kMThreads, smem, s>>>(p);
+  FLIDE_LAUNCH_CHECK();
+  return FLIDE_OK;
+}
+
+// ---- eviction ------------------------------------------------------------------
+
+struct EvictParams {
+  int R, n_slots, n_blocks, dst_blocks, max_blocks, block_rows, budget, sinks, recent;
+  const int32_t *req_slot, *hist_len, *table, *dst_table;
+  const char *pool_k, *pool_v;
+  char *dst_k, *dst_v;
+  const float *mass;
+  float *mass_out;
+  int32_t *kept, *status;
+  int row_bytes;
+};
+
+// Order-preserving code of a mass: NaN counts as the lowest, -0 as 0.
+__device__ __forceinline__ uint32_t mass_code(float v) {
+  if (!(v == v)) return 0u;
+  const uint32_t b = __float_as_uint(v + 0.f);
+  return (b & 0x80000000u) ? ~b : b | 0x80000000u;
+}
+
+// Rows of the history that request r has to be cut from, or -1 where the
+// request is skipped (no slot) or refused (status set).
+__device__ __forceinline__ int evict_length(const EvictParams &p, int r, bool report) {
+  const int slot = p.req_slot[r];
+  if (slot < 0) return -1;
+  const int len = slot < p.n_slots ? p.hist_len[slot] : -1;
+  if (len < 0 || len > (long long)p.max_blocks * p.block_rows) {
+    if (report) set_status(p.status, FLIDE_ERR_INVALID);
+    return -1;
+  }
+  return len;
+}
+
+constexpr int kSelThreads = 1024;
+constexpr int kBits = 11;  // 3 passes over 32-bit codes
+constexpr int kBins = 1 << kBits;
+
+// One block per request: the code of the smallest kept mass by radix selection
+// over the rows between sinks and recent, then the kept rows in order.
+__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictParams p) {
+  __shared__ int hist[kBins];
+  __shared__ int scratch[40];
+  __shared__ int s_dup, s_bin, s_left;
+  const int r = blockIdx.x, tid = threadIdx.x;
+  const int len = evict_length(p, r, tid == 0);
+  int32_t *kept = p.kept + (size_t)r * p.budget;
+  if (tid == 0) s_dup = 0;
+  __syncthreads();
+  if (len >= 0) {  // a slot twice in one call would be moved twice
+    for (int i = tid; i < p.R; i += kSelThreads)
+      if (i != r && p.req_slot[i] == p.req_slot[r]) s_dup = 1;
+  }
+  __syncthreads();
+  if (len < 0 || s_dup) {
+    if (s_dup && tid == 0) set_status(p.status, FLIDE_ERR_INVALID);
+    for (int j = tid; j < p.budget; j += kSelThreads) kept[j] = -1;
+    return;
+  }
+  const size_t at = (size_t)p.req_slot[r] * p.max_blocks * p.block_rows;
+  const float *mass = p.mass + at;
+  float *mass_out = p.mass_out + at;
+  const bool all = len <= p.budget;
+  const int lo = all ? 0 : p.sinks, hi = all ? 0 : len - p.recent;  // candidates
+  int want = all ? 0 : p.budget - p.sinks - p.recent;
+  uint32_t prefix = 0, mask = 0;  // codes still in question: (code & mask) == prefix
+  if (want > 0) {
+    for (int shift = 32 - kBits; ; shift = max(0, shift - kBits)) {
+      const uint32_t bins = mask == 0 || shift > 0 ? kBins : 1u << (32 - 2 * kBits);
+      for (int b = tid; b < kBins; b += kSelThreads) hist[b] = 0;
+      __syncthreads();
+      for (int i = lo + tid; i < hi; i += kSelThreads) {
+        const uint32_t c = mass_code(mass[i]);
+        if ((c & mask) == prefix) atomicAdd(&hist[(c >> shift) & (bins - 1)], 1);
+      }
+      __syncthreads();
+      // bins from the top: thread b holds bins kBins-1-2b and kBins-2-2b
+      const int b0 = kBins - 1 - 2 * tid, h0 = hist[b0], h1 = hist[b0 - 1];
+      int tot;
+      const int before = block_excl_scan(h0 + h1, scratch, &tot);
+      if (before < want && before + h0 >= want) {
+        s_bin = b0;
+        s_left = want - before;
+      } else if (before + h0 < want && before + h0 + h1 >= want) {
+        s_bin = b0 - 1;
+        s_left = want - before - h0;
+      }
+      __syncthreads();
+      want = s_left;  // of the chosen bin's rows
+      prefix |= (uint32_t)s_bin << shift;
+      mask |= (bins - 1) << shift;
+      __syncthreads();
+      if (shift == 0) break;
+    }
+  }
+  // rows above the threshold, the first `want` at it, and the fixed ones.  The
+  // mass of a chunk is read before the chunk's scan and written after it, to
+  // places that are not past the chunk: safe in place.
+  int out = 0, ties = 0;
+  for (int i0 = 0; i0 < len; i0 += kSelThreads) {
+    const int i = i0 + tid;
+    const float v = i < len ? mass[i] : 0.f;
+    bool keep = all || i < lo || i >= hi;
+    int tie = 0;
+    if (!keep && p.budget > p.sinks + p.recent) {
+      const uint32_t c = mass_code(v);
+      keep = c > prefix;
+      tie = c == prefix;
+    }
+    int n_tie = 0, n_keep;
+    const int before = block_excl_scan(tie, scratch, &n_tie);
+    if (tie) keep = ties + before < want;
+    ties += n_tie;
+    keep = keep && i < len;
+    const int j = out + block_excl_scan(keep ? 1 : 0, scratch, &n_keep);
+    if (keep) {
+      kept[j] = i;
+      mass_out[j] = v;
+    }
+    out += n_keep;
+  }
+  for (int j = out + tid; j < p.budget; j += kSelThreads) kept[j] = -1;
+}
+
+constexpr int kMoveThreads = 256;
+constexpr int kSlice = 64;       // bytes of a row that one block moves
+constexpr int kUnroll = 8;       // rows in flight per thread
+
+// Block (slice, request): the slice of every kept row, front to back.  A row
+// never moves backwards past one that is still to be read (kept[j] >= j and
+// ascending), so in one block order is all that in-place movement needs: a
+// chunk is loaded whole before it is stored.
+__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictParams p) {
+  const int r = blockIdx.y, tid = threadIdx.x;
+  const int len = evict_length(p, r, false);
+  if (len < 0) return;
+  const int32_t *kept = p.kept + (size_t)r * p.budget;
+  const int n = min(len, p.budget);
+  const int slices = (p.row_bytes + kSlice - 1) / kSlice;
+  const bool is_v = (int)blockIdx.x >= slices;
+  const int off = (is_v ? blockIdx.x - slices : blockIdx.x) * kSlice + (tid % (kSlice / 16)) * 16;
+  const char *src = is_v ? p.pool_v : p.pool_k;
+  char *dst = is_v ? p.dst_v : p.dst_k;
+  const size_t slot = p.req_slot[r];
+  const int32_t *st = p.table + slot * p.max_blocks, *dt = p.dst_table + slot * p.max_blocks;
+  constexpr int kPer = kMoveThreads / (kSlice / 16);  // rows a step
+  const bool mine = off < p.row_bytes;
+  if (n > 0 && kept[0] < 0) return;  // refused by the selection (a slot twice)
+  for (int j0 = 0; j0 < n; j0 += kPer * kUnroll) {
+    uint4 v[kUnroll];
+    char *to[kUnroll];
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k) {
+      const int j = j0 + k * kPer + tid / (kSlice / 16);
+      to[k] = nullptr;
+      if (j >= n || !mine) continue;
+      const int i = kept[j];
+      const int sb = st[i / p.block_rows], db = dt[j / p.block_rows];
+      if (sb < 0 || sb >= p.n_blocks || db < 0 || db >= p.dst_blocks) {
+        set_status(p.status, FLIDE_ERR_INVALID);
+        continue;
+      }
+      const char *from = src + ((size_t)sb * p.block_rows + i % p.block_rows) * p.row_bytes + off;
+      to[k] = dst + ((size_t)db * p.block_rows + j % p.block_rows) * p.row_bytes + off;
+      if (from == to[k]) {
+        to[k] = nullptr;
+        continue;
+      }
+      v[k] = *reinterpret_cast<const uint4 *>(from);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k)
+      if (to[k]) *reinterpret_cast<uint4 *>(to[k]) = v[k];
+    __syncthreads();
+  }
+}
+
+}  // namespace
+}  // namespace flide
+
+extern "C" {
+
+int flide_history_mass(const void *q, const void *k, const float *lse, const void *pool_k,
+                       int32_t n_blocks, int32_t block_rows, const int32_t *block_table,
+                       int32_t max_blocks, const int32_t *req_slot, int32_t n_slots,
+                       const flide_tree_index *idx, int32_t Hq, int32_t Hkv, int32_t d, int32_t dtype,
+                       const float *descale, float scale, const float *mass, float *mass_out,
+                       flide_stream stream) {
+  using namespace flide;
+  if (!idx || !q || !k || !lse || !pool_k || !block_table || !req_slot || !mass || !mass_out)
+    return FLIDE_ERR_SHAPE;
+  if (n_blocks <= 0 || max_blocks <= 0 || n_slots <= 0 || block_rows <= 0 || block_rows % 16)
+    return FLIDE_ERR_SHAPE;
+  if (Hq <= 0 || Hkv <= 0 || Hq % Hkv || d < 32 || d % 32 || d > 256) return FLIDE_ERR_SHAPE;
+  if (dtype != FLIDE_F32 && dtype != FLIDE_BF16 && dtype != FLIDE_E4M3) return FLIDE_ERR_SHAPE;
+  if (dtype == FLIDE_E4M3 && (!descale || d != 128)) return FLIDE_ERR_SHAPE;
+  if (idx->R < 0 || idx->T < 0) return FLIDE_ERR_SHAPE;
+  if (idx->R > kMaxListR) return FLIDE_ERR_CAPACITY;
+  if (idx->R == 0 || idx->T == 0) return FLIDE_OK;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return FLIDE_ERR_CUDA;
+  MassParams p;
+  p.x = *idx;
+  p.hist = HistoryView{block_table, req_slot, max_blocks, block_rows, n_blocks, n_slots, 0};
+  p.q = q;
+  p.k = k;
+  p.pool_k = pool_k;
+  p.lse = lse;
+  p.mass = mass;
+  p.mass_out = mass_out;
+  p.descale = dtype == FLIDE_E4M3 ? descale : nullptr;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.G = Hq / Hkv;
+  p.d = d;
+  p.scale = scale;
+  cudaStream_t s = (cudaStream_t)stream;
+  if (dtype == FLIDE_F32) return mass_launch<float>(p, sms, s);
+  if (dtype == FLIDE_BF16) return mass_launch<__nv_bfloat16>(p, sms, s);
+  return mass_launch<uint8_t>(p, sms, s);
+}
+
+int flide_history_evict(int32_t R, const int32_t *req_slot, int32_t n_slots, const int32_t *hist_len,
+                        const int32_t *block_table, int32_t max_blocks, int32_t block_rows,
+                        const void *pool_k, const void *pool_v, int32_t n_blocks, int32_t Hkv,
+                        int32_t d, int32_t dtype, const float *mass, int32_t budget, int32_t sinks,
+                        int32_t recent, void *dst_k, void *dst_v, const int32_t *dst_table,
+                        int32_t dst_blocks, float *mass_out, int32_t *kept, int32_t *status,
+                        flide_stream stream) {
+  using namespace flide;
+  if (!req_slot || !hist_len || !block_table || !pool_k || !pool_v || !mass || !dst_k || !dst_v ||
+      !dst_table || !mass_out || !kept || !status)
+    return FLIDE_ERR_SHAPE;
+  if (R < 0 || n_slots <= 0 || max_blocks <= 0 || block_rows <= 0 || n_blocks <= 0 || dst_blocks <= 0 ||
+      Hkv <= 0 || d <= 0)
+    return FLIDE_ERR_SHAPE;
+  if (budget <= 0 || sinks < 0 || recent < 0 || (int64_t)sinks + recent > budget) return FLIDE_ERR_SHAPE;
+  const int es = dtype == FLIDE_BF16 ? 2 : dtype == FLIDE_F32 ? 4 : dtype == FLIDE_E4M3 ? 1 : 0;
+  if (!es) return FLIDE_ERR_SHAPE;
+  const int64_t row_bytes = (int64_t)Hkv * d * es;
+  if (row_bytes % 16 || row_bytes > (1 << 20)) return FLIDE_ERR_SHAPE;
+  if (R > kMaxListR || (int64_t)max_blocks * block_rows > INT32_MAX) return FLIDE_ERR_CAPACITY;
+  if (R == 0) return FLIDE_OK;
+  EvictParams p;
+  p.R = R;
+  p.n_slots = n_slots;
+  p.n_blocks = n_blocks;
+  p.dst_blocks = dst_blocks;
+  p.max_blocks = max_blocks;
+  p.block_rows = block_rows;
+  p.budget = budget;
+  p.sinks = sinks;
+  p.recent = recent;
+  p.req_slot = req_slot;
+  p.hist_len = hist_len;
+  p.table = block_table;
+  p.dst_table = dst_table;
+  p.pool_k = static_cast<const char *>(pool_k);
+  p.pool_v = static_cast<const char *>(pool_v);
+  p.dst_k = static_cast<char *>(dst_k);
+  p.dst_v = static_cast<char *>(dst_v);
+  p.mass = mass;
+  p.mass_out = mass_out;
+  p.kept = kept;
+  p.status = status;
+  p.row_bytes = (int)row_bytes;
+  cudaStream_t s = (cudaStream_t)stream;
+  evict_select_kernel<<<R, kSelThreads, 0, s>>>(p);
+  FLIDE_LAUNCH_CHECK();
+  const int slices = (int)((row_bytes + kSlice - 1) / kSlice);
+  evict_move_kernel<<<dim3(2 * slices, R), kMoveThreads, 0, s>>>(p);
+  FLIDE_LAUNCH_CHECK();
+  return FLIDE_OK;
+}
+
+}  // extern "C"

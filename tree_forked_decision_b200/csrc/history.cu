@@ -246,13 +246,20 @@ int flide_pool_append_batch(flide_pool *p, int32_t n, const int32_t *slots, cons
 
 int flide_pool_release(flide_pool *p, int32_t slot) {
   if (!p || slot < 0 || slot >= p->max_requests) return FLIDE_ERR_INVALID;
-  for (int32_t i = p->nblocks[slot] - 1; i >= 0; --i) {
+  return flide_pool_truncate(p, slot, 0);
+}
+
+int flide_pool_truncate(flide_pool *p, int32_t slot, int32_t rows) {
+  if (!p || slot < 0 || slot >= p->max_requests || rows < 0 || rows > p->length[slot])
+    return FLIDE_ERR_INVALID;
+  const int32_t keep = (int32_t)(((int64_t)rows + p->block_rows - 1) / p->block_rows);
+  for (int32_t i = p->nblocks[slot] - 1; i >= keep; --i) {
     int32_t &e = p->table[(size_t)slot * p->max_blocks + i];
-    p->free_list.push_back(e);
+    p->free_list.push_back(e);  // capacity n_blocks since creation: cannot throw
     e = -1;
   }
-  p->nblocks[slot] = 0;
-  p->length[slot] = 0;
+  p->nblocks[slot] = keep;
+  p->length[slot] = rows;
   return FLIDE_OK;
 }
 

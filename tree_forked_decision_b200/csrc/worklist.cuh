@@ -1,0 +1,97 @@
+// worklist.cuh -- work lists over a batch's requests, built by each block from
+// the tree index: no list is kept between calls and no kernel prepares one.
+#pragma once
+
+#include "common.cuh"
+
+namespace flide {
+
+constexpr int kMaxListR = 4096;  // requests of a work list
+
+// pref[r] = sum of count(0 .. r-1), pref[R] = the total; 64 bits, because a
+// long history's units times its heads pass 2^31.  `part` holds a block's
+// thread sums (blockDim.x <= 1024 entries); ends with a barrier.
+template <typename F>
+__device__ __forceinline__ void request_prefix(int R, F count, long long *pref, long long *part) {
+  const int nt = blockDim.x, per = (R + nt - 1) / nt, tid = threadIdx.x;
+  const int lo = min(R, tid * per), hi = min(R, lo + per);
+  long long sum = 0;
+  for (int r = lo; r < hi; ++r) {
+    const long long c = count(r);
+    pref[r] = c;
+    sum += c;
+  }
+  const int lane = tid & 31, warp = tid >> 5;
+  long long incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) part[warp] = incl;
+  __syncthreads();
+  long long base = incl - sum;
+  for (int w = 0; w < warp; ++w) base += part[w];
+  for (int r = lo; r < hi; ++r) {
+    const long long c = pref[r];
+    pref[r] = base;
+    base += c;
+  }
+  if (tid == nt - 1) pref[R] = base;
+  __syncthreads();
+}
+
+// the request r with pref[r] <= u < pref[r + 1]
+__device__ __forceinline__ int request_of(const long long *pref, int R, long long u) {
+  int lo = 0, hi = R;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (pref[mid + 1] > u) hi = mid; else lo = mid + 1;
+  }
+  return lo;
+}
+
+// A request's history rows: packed rows [base, base + len), or rows of pool
+// slot `slot` through its block table.
+struct HistoryView {
+  const int32_t *block_table, *req_slot;  // NULL table: packed
+  int max_blocks, block_rows, n_blocks, n_slots;
+  long long rows;  // rows of the packed arrays
+};
+
+// History rows of request r that can be read (0 with the status set where the
+// slot or the lengths are bad); first packed row or slot in *base.
+__device__ __forceinline__ int history_rows(const flide_tree_index &x, const HistoryView &h, int r,
+                                            bool report, long long *base) {
+  const int p0 = x.past_start[r], len = x.past_start[r + 1] - p0;
+  *base = p0;
+  if (len <= 0) return 0;
+  if (h.block_table) {
+    const int slot = h.req_slot[r];
+    if (slot < 0 || slot >= h.n_slots || len > (long long)h.max_blocks * h.block_rows) {
+      if (report) set_status(x.status, FLIDE_ERR_INVALID);
+      return 0;
+    }
+    *base = slot;
+  } else if (p0 < 0 || (long long)p0 + len > h.rows) {
+    if (report) set_status(x.status, h.rows ? FLIDE_ERR_CAPACITY : FLIDE_ERR_SHAPE);
+    return 0;
+  }
+  return len;
+}
+
+// Row of the K/V arrays that holds history row i, or -1 (status set) where the
+// table has no valid block.
+__device__ __forceinline__ long long history_row(const flide_tree_index &x, const HistoryView &h,
+                                                 long long base, int i) {
+  if (!h.block_table) return base + i;
+  const int b = i / h.block_rows;
+  const int blk = h.block_table[base * h.max_blocks + b];
+  if (blk < 0 || blk >= h.n_blocks) {
+    set_status(x.status, FLIDE_ERR_INVALID);
+    return -1;
+  }
+  return (long long)blk * h.block_rows + (i - b * h.block_rows);
+}
+
+}  // namespace flide

@@ -20,6 +20,7 @@ LIB_PATH = os.path.join(_PKG, "libflide_dbg.so" if os.environ.get("FLIDE_DEBUG_B
 OK, ERR_INVALID, ERR_SHAPE, ERR_CAPACITY, ERR_CUDA, ERR_TIMEOUT, ERR_BOUNDS = range(7)
 F32, BF16, E4M3 = 0, 1, 2
 FLAG_PORTABLE = 1
+ROPE_SCALING = dict(none=0, linear=1, ntk=2, yarn=3)
 COUNTS = 16
 CNT = dict(N=0, T=1, PAST=2, DEPTH=3, SLOTS=4, BRANCH_TOK=5, ROOT_TOK=6, CKPT_ROWS=7,
            CHECK_SITE=12, CHECK_VALUE=13)
@@ -38,7 +39,10 @@ SYMBOLS = ["flide_tree_index_bytes", "flide_tree_index_init", "flide_tree_build"
            "flide_history_append", "flide_history_gather", "flide_selftest_wait_timeout",
            "flide_fork_attn_fp8", "flide_amax", "flide_quantize_e4m3", "flide_fork_attn_paged",
            "flide_plan_state_groups", "flide_copy_rows", "flide_fork_gdn_fp8", "flide_pool_append_batch",
-           "flide_tree_state_slots", "flide_debug_bounds", "flide_strerror"]
+           "flide_tree_state_slots", "flide_debug_bounds", "flide_strerror", "flide_rope_freqs",
+           "flide_rope", "flide_draft_attn_workspace_bytes", "flide_draft_attn",
+           "flide_draft_attn_paged", "flide_verify_draft", "flide_history_mass",
+           "flide_history_evict", "flide_pool_truncate"]
 
 
 class FlideError(RuntimeError):
@@ -139,6 +143,29 @@ def _lib():
         lib.flide_amax.restype = ctypes.c_int
         lib.flide_quantize_e4m3.argtypes = [P, ctypes.c_int64, I32, P, P, P, P]
         lib.flide_quantize_e4m3.restype = ctypes.c_int
+        D, SZ = ctypes.c_double, ctypes.c_size_t
+        lib.flide_rope_freqs.argtypes = [I32, D, I32, D, D, D, D, P, P]
+        lib.flide_rope_freqs.restype = ctypes.c_int
+        lib.flide_rope.argtypes = [P, P, P, P, P, P, P, I32, I32, I32, I32, I32, I32, F, I32, P]
+        lib.flide_rope.restype = ctypes.c_int
+        lib.flide_draft_attn_workspace_bytes.argtypes = [I32, I32, I32, I32, I32]
+        lib.flide_draft_attn_workspace_bytes.restype = SZ
+        lib.flide_draft_attn.argtypes = [P, P, P, P, P, I32, P, I32, I32, I32, I32, P, F, P, P, P, SZ,
+                                         P]
+        lib.flide_draft_attn.restype = ctypes.c_int
+        lib.flide_draft_attn_paged.argtypes = [P, P, P, P, P, I32, I32, P, I32, P, I32, P, I32, I32,
+                                               I32, I32, P, F, P, P, P, SZ, P]
+        lib.flide_draft_attn_paged.restype = ctypes.c_int
+        lib.flide_verify_draft.argtypes = [P, P, P, P, P, P, I32, I32, P, P, P, P]
+        lib.flide_verify_draft.restype = ctypes.c_int
+        lib.flide_history_mass.argtypes = [P, P, P, P, I32, I32, P, I32, P, I32, P, I32, I32, I32, I32,
+                                           P, F, P, P, P]
+        lib.flide_history_mass.restype = ctypes.c_int
+        lib.flide_history_evict.argtypes = [I32, P, I32, P, P, I32, I32, P, P, I32, I32, I32, I32, P,
+                                            I32, I32, I32, P, P, P, I32, P, P, P, P]
+        lib.flide_history_evict.restype = ctypes.c_int
+        lib.flide_pool_truncate.argtypes = [P, I32, I32]
+        lib.flide_pool_truncate.restype = ctypes.c_int
         lib.flide_debug_bounds.argtypes = []
         lib.flide_debug_bounds.restype = ctypes.c_int32
         lib.flide_strerror.argtypes = [ctypes.c_int32]
@@ -594,3 +621,312 @@ def state_slots(tree) -> int:
                                          pa32.ctypes.data_as(ctypes.c_void_p), ctypes.byref(slots)),
            "flide_tree_state_slots")
     return int(slots.value)
+
+
+# ---- speculative decoding over a history --------------------------------------
+
+def _on(where, device, stream, index=None, **named):
+    """Device addresses (None for None) of a call's dense tensors, which (and the
+    tree index) all lie on `device`, the current one, on whose stream the call runs."""
+    if device.type != "cuda":
+        raise ValueError(f"{where}: expected CUDA tensors, got one on {device}")
+    if device.index != torch.cuda.current_device() or (stream is not None and stream.device != device):
+        raise ValueError(f"{where}: the tensors are on {device}; make it the current device and the "
+                         "stream's")
+    if index is not None and index.buf.device != device:
+        raise ValueError(f"{where}: the tree index is on {index.buf.device}, expected {device}")
+    got = []
+    for name, t in named.items():
+        if t is None:
+            got.append(None)
+            continue
+        if t.device != device:
+            raise ValueError(f"{where}: {name} is on {t.device}, expected {device}")
+        if not t.is_contiguous():
+            raise ValueError(f"{where}: {name} must be contiguous, got strides {tuple(t.stride())} for "
+                             f"shape {tuple(t.shape)}")
+        got.append(t.data_ptr())
+    return got
+
+
+def _raw_stream(stream):
+    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+
+
+def _new(shape, dtype, device, stream):
+    """A tensor for a call on `stream`: its memory is that stream's to reuse."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _typed(where, dtype, **named):
+    for name, t in named.items():
+        if t is not None and t.dtype != dtype:
+            raise TypeError(f"{where}: {name} must be {dtype}, got {t.dtype}")
+
+
+def _shaped(where, shape, **named):
+    for name, t in named.items():
+        if t is not None and t.shape != shape:
+            raise ValueError(f"{where}: {name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def rope_freqs(rot_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+               orig_len: float = 0.0, fast: float = 32.0, slow: float = 1.0, device="cuda"):
+    """Rotation frequencies (float64 tensor [rot_dim / 2], radians a position) and
+    the factor mscale for `rope`; scaling "none", "linear", "ntk" or "yarn"."""
+    if scaling not in ROPE_SCALING:
+        raise ValueError(f"rope_freqs: scaling is one of {sorted(ROPE_SCALING)}, got {scaling!r}")
+    freqs = np.empty(max(int(rot_dim) // 2, 1), np.float64)
+    m = ctypes.c_float(1.0)
+    _check(_lib().flide_rope_freqs(int(rot_dim), float(base), ROPE_SCALING[scaling], float(factor),
+                                   float(orig_len), float(fast), float(slow),
+                                   freqs.ctypes.data_as(ctypes.c_void_p), ctypes.byref(m)),
+           "flide_rope_freqs")
+    return torch.from_numpy(freqs).to(device), float(m.value)
+
+
+def rope(q, k, index: TreeIndex, freqs, pos_offset=None, mscale: float = 1.0,
+         interleaved: bool = False, transpose: bool = False, q_out=None, k_out=None, stream=None):
+    """Rotary positions of the stream's queries and keys (q [T, Hq, d], k [T, Hkv, d],
+    float32 or bfloat16; either may be None) at token_pos + pos_offset[request]
+    (int32 [R], optional); freqs and mscale from `rope_freqs`.  q_out / k_out may
+    be q / k (in place).  transpose turns the other way (the gradient).  Returns
+    (q_out, k_out)."""
+    ref = q if q is not None else k
+    if ref is None:
+        raise ValueError("rope: q or k is needed")
+    if ref.dim() != 3 or ref.shape[0] < index.T:
+        raise ValueError(f"rope: expected [T >= {index.T}, heads, d], got {tuple(ref.shape)}")
+    if q is not None and k is not None and (k.dim() != 3 or k.shape[0] != q.shape[0]
+                                            or k.shape[2] != q.shape[2]):
+        raise ValueError(f"rope: expected q [T, Hq, d] and k [T, Hkv, d], got {tuple(q.shape)}, "
+                         f"{tuple(k.shape)}")
+    if q is not None and q_out is None:
+        q_out = _new(q.shape, q.dtype, q.device, stream)
+    if k is not None and k_out is None:
+        k_out = _new(k.shape, k.dtype, k.device, stream)
+    _typed("rope", ref.dtype, q=q, k=k, q_out=q_out, k_out=k_out)
+    if q is not None:
+        _shaped("rope", q.shape, q_out=q_out)
+    if k is not None:
+        _shaped("rope", k.shape, k_out=k_out)
+    _typed("rope", torch.float64, freqs=freqs)
+    if pos_offset is not None:
+        _typed("rope", torch.int32, pos_offset=pos_offset)
+        if pos_offset.numel() < index.R:
+            raise ValueError(f"rope: pos_offset needs {index.R} entries")
+    po, pf, pq, pk, pqo, pko = _on("rope", ref.device, stream, index, pos_offset=pos_offset, freqs=freqs, q=q,
+                                   k=k, q_out=q_out if q is not None else None,
+                                   k_out=k_out if k is not None else None)
+    _check(_lib().flide_rope(ctypes.byref(index.c), po, pf, pq, pk, pqo, pko,
+                             0 if q is None else q.shape[1], 0 if k is None else k.shape[1],
+                             ref.shape[2], 2 * freqs.numel(), interleaved, transpose, mscale,
+                             _dtype_code(ref), _raw_stream(stream)), "flide_rope")
+    return q_out, k_out
+
+
+def _e4m3(t):
+    return t.dtype in (torch.uint8, torch.float8_e4m3fn)
+
+
+def draft_attn_workspace(index: TreeIndex, Hq: int, Hkv: int, d: int, device="cuda", stream=None):
+    """Workspace of `draft_attn` for an index and head layout (one call at a time)."""
+    n = _lib().flide_draft_attn_workspace_bytes(index.R, index.T, Hq, Hkv, d)
+    if n == 0:
+        raise FlideError(ERR_SHAPE, "flide_draft_attn_workspace_bytes")
+    return _new((n,), torch.uint8, device, stream)
+
+
+def _draft_args(where, q, k, v, index, past_k, past_v, descale, out, lse, workspace, stream):
+    """Checks shared by the two draft attention calls; returns the element code and
+    the outputs and workspace, made where they are not given."""
+    if q.dim() != 3 or k.dim() != 3 or v.shape != k.shape or k.shape[0] != q.shape[0] \
+            or k.shape[2] != q.shape[2] or q.shape[0] < index.T:
+        raise ValueError(f"{where}: expected q [T, Hq, d] and k, v [T, Hkv, d] with T >= {index.T}, got "
+                         f"{tuple(q.shape)}, {tuple(k.shape)}, {tuple(v.shape)}")
+    e4m3 = _e4m3(q)
+    for name, t in (("k", k), ("v", v), ("past_k", past_k), ("past_v", past_v)):
+        if t is not None and t.dtype != q.dtype and not (e4m3 and _e4m3(t)):
+            raise TypeError(f"{where}: {name} is {t.dtype}, q is {q.dtype}")
+    if (past_k is None) != (past_v is None) or (past_k is not None and (
+            past_k.shape != past_v.shape or past_k.dim() != 3 or past_k.shape[1:] != k.shape[1:])):
+        raise ValueError(f"{where}: expected past_k, past_v [P, Hkv, d]")
+    if e4m3:
+        if descale is None or descale.dtype != torch.float32 or descale.numel() < 3:
+            raise TypeError(f"{where}: e4m3 codes need descale, a float32 tensor of 3 entries")
+    elif descale is not None:
+        raise TypeError(f"{where}: descale belongs to e4m3 codes")
+    code = E4M3 if e4m3 else _dtype_code(q)
+    kind = torch.bfloat16 if e4m3 else q.dtype
+    if out is None:
+        out = _new(q.shape, kind, q.device, stream)
+    if lse is None:
+        lse = _new(q.shape[:2], torch.float32, q.device, stream)
+    _typed(where, kind, out=out)
+    _typed(where, torch.float32, lse=lse)
+    _shaped(where, q.shape, out=out)
+    _shaped(where, q.shape[:2], lse=lse)
+    if workspace is None:
+        workspace = draft_attn_workspace(index, q.shape[1], k.shape[1], q.shape[2], q.device, stream)
+    return code, out, lse, workspace
+
+
+def draft_attn(q, k, v, index: TreeIndex, scale: float, past_k=None, past_v=None, descale=None,
+               out=None, lse=None, workspace=None, stream=None):
+    """Attention of a few tokens per request (a root and its drafted tree) over a long
+    packed past: fork_attn's result, with the past split over the whole GPU.
+    float32, bfloat16, or e4m3 codes with descale (bf16 out).  Returns (out, lse
+    [T, Hq])."""
+    if past_k is not None and past_k.shape[0] == 0:
+        past_k = past_v = None
+    code, out, lse, workspace = _draft_args("draft_attn", q, k, v, index, past_k, past_v, descale, out,
+                                            lse, workspace, stream)
+    a = _on("draft_attn", q.device, stream, index, q=q, k=k, v=v, past_k=past_k, past_v=past_v,
+            descale=descale, out=out, lse=lse, workspace=workspace)
+    _check(_lib().flide_draft_attn(a[0], a[1], a[2], a[3], a[4], 0 if past_k is None else past_k.shape[0],
+                                   ctypes.byref(index.c), q.shape[1], k.shape[1], q.shape[2], code, a[5],
+                                   scale, a[6], a[7], a[8], workspace.numel() * workspace.element_size(),
+                                   _raw_stream(stream)), "flide_draft_attn")
+    return out, lse
+
+
+def _paged_args(where, index, pool, block_table, req_slot, block_rows, max_blocks):
+    """(blocks, slots) of a pool and its table."""
+    _typed(where, torch.int32, block_table=block_table, req_slot=req_slot)
+    if block_rows <= 0 or max_blocks <= 0:
+        raise ValueError(f"{where}: block_rows and max_blocks must be positive")
+    if req_slot.numel() < index.R:
+        raise ValueError(f"{where}: req_slot needs {index.R} entries")
+    return pool.shape[0] // block_rows, block_table.numel() // max_blocks
+
+
+def draft_attn_paged(q, k, v, index: TreeIndex, scale: float, pool_k, pool_v, block_table, req_slot,
+                     block_rows: int, max_blocks: int, descale=None, out=None, lse=None,
+                     workspace=None, stream=None):
+    """`draft_attn` with the past read in place from a block-paged pool (laid out as
+    for fork_attn_paged; blocks of any multiple of 16 rows)."""
+    code, out, lse, workspace = _draft_args("draft_attn_paged", q, k, v, index, pool_k, pool_v, descale,
+                                            out, lse, workspace, stream)
+    n_blocks, n_slots = _paged_args("draft_attn_paged", index, pool_k, block_table, req_slot, block_rows,
+                                    max_blocks)
+    a = _on("draft_attn_paged", q.device, stream, index, q=q, k=k, v=v, pool_k=pool_k, pool_v=pool_v,
+            block_table=block_table, req_slot=req_slot, descale=descale, out=out, lse=lse,
+            workspace=workspace)
+    _check(_lib().flide_draft_attn_paged(a[0], a[1], a[2], a[3], a[4], n_blocks, block_rows, a[5],
+                                         max_blocks, a[6], n_slots, ctypes.byref(index.c), q.shape[1],
+                                         k.shape[1], q.shape[2], code, a[7], scale, a[8], a[9], a[10],
+                                         workspace.numel() * workspace.element_size(),
+                                         _raw_stream(stream)), "flide_draft_attn_paged")
+    return out, lse
+
+
+def verify_draft(index: TreeIndex, tokens, target, u, u_next, draft=None, n_accept=None,
+                 next_token=None, path=None, stream=None):
+    """Verifies a drafted tree: tokens [T] int32, target (and, for sampled drafts,
+    draft) [T, V] probabilities after each stream token, random numbers u [T] and
+    u_next [R].  Returns n_accept [R], next_token [R] and path [T] (accepted
+    stream rows at each request's stream offset, then -1), all int32."""
+    if target.dim() != 2 or target.shape[0] < index.T:
+        raise ValueError(f"verify_draft: target must be [T >= {index.T}, V], got {tuple(target.shape)}")
+    if draft is not None:
+        _typed("verify_draft", target.dtype, draft=draft)
+        _shaped("verify_draft", target.shape, draft=draft)
+    dev = target.device
+    if n_accept is None:
+        n_accept = _new((index.R,), torch.int32, dev, stream)
+    if next_token is None:
+        next_token = _new((index.R,), torch.int32, dev, stream)
+    if path is None:
+        path = _new((index.T,), torch.int32, dev, stream)
+    _typed("verify_draft", torch.int32, tokens=tokens, n_accept=n_accept, next_token=next_token, path=path)
+    _typed("verify_draft", torch.float32, u=u, u_next=u_next)
+    for name, t, n in (("tokens", tokens, index.T), ("u", u, index.T), ("path", path, index.T),
+                       ("u_next", u_next, index.R), ("n_accept", n_accept, index.R),
+                       ("next_token", next_token, index.R)):
+        if t.numel() < n:
+            raise ValueError(f"verify_draft: {name} needs {n} entries")
+    a = _on("verify_draft", dev, stream, index, tokens=tokens, target=target, draft=draft, u=u, u_next=u_next,
+            n_accept=n_accept, next_token=next_token, path=path)
+    _check(_lib().flide_verify_draft(ctypes.byref(index.c), a[0], a[1], a[2], a[3], a[4], target.shape[1],
+                                     _dtype_code(target), a[5], a[6], a[7], _raw_stream(stream)),
+           "flide_verify_draft")
+    return n_accept, next_token, path
+
+
+def history_mass(q, k, lse, index: TreeIndex, scale: float, pool_k, block_table, req_slot,
+                 block_rows: int, max_blocks: int, mass, mass_out=None, descale=None, stream=None):
+    """Adds the attention weight that the root's tokens gave each history row (and the
+    root's own rows, which the step appends) to mass [n_slots, max_blocks *
+    block_rows] float32; lse from draft_attn_paged.  mass_out defaults to mass (in
+    place).  Returns mass_out."""
+    if q.dim() != 3 or k.dim() != 3 or k.shape[0] != q.shape[0] or k.shape[2] != q.shape[2] \
+            or q.shape[0] < index.T:
+        raise ValueError(f"history_mass: expected q [T, Hq, d] and k [T, Hkv, d] with T >= {index.T}, got "
+                         f"{tuple(q.shape)}, {tuple(k.shape)}")
+    e4m3 = _e4m3(q)
+    for name, t in (("k", k), ("pool_k", pool_k)):
+        if t.dtype != q.dtype and not (e4m3 and _e4m3(t)):
+            raise TypeError(f"history_mass: {name} is {t.dtype}, q is {q.dtype}")
+    if pool_k.dim() != 3 or pool_k.shape[1:] != k.shape[1:]:
+        raise ValueError("history_mass: pool_k must be [n_blocks * block_rows, Hkv, d]")
+    if e4m3 != (descale is not None) or (e4m3 and (descale.dtype != torch.float32 or descale.numel() < 3)):
+        raise TypeError("history_mass: descale, a float32 tensor of 3 entries, goes with e4m3 codes")
+    n_blocks, n_slots = _paged_args("history_mass", index, pool_k, block_table, req_slot, block_rows,
+                                    max_blocks)
+    if mass_out is None:
+        mass_out = mass
+    _typed("history_mass", torch.float32, lse=lse, mass=mass, mass_out=mass_out)
+    _shaped("history_mass", q.shape[:2], lse=lse)
+    _shaped("history_mass", (n_slots, max_blocks * block_rows), mass=mass, mass_out=mass_out)
+    a = _on("history_mass", q.device, stream, index, q=q, k=k, lse=lse, pool_k=pool_k, block_table=block_table,
+            req_slot=req_slot, descale=descale, mass=mass, mass_out=mass_out)
+    _check(_lib().flide_history_mass(a[0], a[1], a[2], a[3], n_blocks, block_rows, a[4], max_blocks, a[5],
+                                     n_slots, ctypes.byref(index.c), q.shape[1], k.shape[1], q.shape[2],
+                                     E4M3 if e4m3 else _dtype_code(q), a[6], scale, a[7], a[8],
+                                     _raw_stream(stream)), "flide_history_mass")
+    return mass_out
+
+
+def history_evict(req_slot, lengths, block_table, block_rows: int, max_blocks: int, pool_k, pool_v, mass,
+                  budget: int, status, sinks: int = 0, recent: int = 0, dst_k=None, dst_v=None,
+                  dst_table=None, mass_out=None, kept=None, stream=None):
+    """Cuts the histories req_slot [R] (-1: none) that are longer than budget rows down
+    to the first `sinks`, the last `recent` and the rows of largest mass, in order,
+    in place or into other blocks (dst_k, dst_v, dst_table, mass_out; all or
+    none).  lengths int32 [n_slots]; status an int32 tensor [1] for device errors.
+    Returns kept [R, budget] int32, the rows kept, then -1."""
+    dst = (dst_k, dst_v, dst_table, mass_out)
+    if any(t is None for t in dst):
+        if any(t is not None for t in dst):
+            raise ValueError("history_evict: dst_k, dst_v, dst_table and mass_out go together")
+        dst_k, dst_v, dst_table, mass_out = pool_k, pool_v, block_table, mass
+    R, n_slots = req_slot.numel(), lengths.numel()
+    if budget <= 0 or block_rows <= 0 or max_blocks <= 0:
+        raise ValueError("history_evict: budget, block_rows and max_blocks must be positive")
+    if kept is None:
+        kept = _new((R, budget), torch.int32, req_slot.device, stream)
+    _typed("history_evict", torch.int32, req_slot=req_slot, lengths=lengths, block_table=block_table,
+           dst_table=dst_table, kept=kept, status=status)
+    _typed("history_evict", torch.float32, mass=mass, mass_out=mass_out)
+    if pool_k.dim() != 3 or dst_k.dim() != 3 or dst_k.shape[1:] != pool_k.shape[1:]:
+        raise ValueError("history_evict: pools must be [n_blocks * block_rows, Hkv, d]")
+    _shaped("history_evict", pool_k.shape, pool_v=pool_v)
+    _shaped("history_evict", dst_k.shape, dst_v=dst_v)
+    _typed("history_evict", pool_k.dtype, pool_v=pool_v, dst_k=dst_k, dst_v=dst_v)
+    _shaped("history_evict", (n_slots, max_blocks * block_rows), mass=mass, mass_out=mass_out)
+    _shaped("history_evict", (R, budget), kept=kept)
+    for name, t in (("block_table", block_table), ("dst_table", dst_table)):
+        if t.numel() < n_slots * max_blocks:
+            raise ValueError(f"history_evict: {name} needs {n_slots * max_blocks} entries")
+    a = _on("history_evict", pool_k.device, stream, req_slot=req_slot, lengths=lengths,
+            block_table=block_table, pool_k=pool_k, pool_v=pool_v, mass=mass, dst_k=dst_k, dst_v=dst_v,
+            dst_table=dst_table, mass_out=mass_out, kept=kept, status=status)
+    _check(_lib().flide_history_evict(R, a[0], n_slots, a[1], a[2], max_blocks, block_rows, a[3], a[4],
+                                      pool_k.shape[0] // block_rows, pool_k.shape[1], pool_k.shape[2],
+                                      E4M3 if _e4m3(pool_k) else _dtype_code(pool_k), a[5], budget, sinks,
+                                      recent, a[6], a[7], a[8], dst_k.shape[0] // block_rows, a[9], a[10],
+                                      a[11], _raw_stream(stream)), "flide_history_evict")
+    return kept

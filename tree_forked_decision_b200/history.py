@@ -24,6 +24,17 @@ Without the packed copy (block_rows a multiple of 128):
     past_len, state_in = store.resume_lengths(slots)
     ... flide_tree_build ...
     o = store.fork_attn_paged(q, k, v, index, scale, slots)   # past read in place
+
+A speculative decoding step (a root of committed tokens and drafted tokens below
+it), with the history bounded to `budget` rows:
+
+    past_len, state_in = store.resume_lengths(slots)
+    ... flide_tree_build; flide.rope(q, k, index, freqs, pos_offset=store.pos_offset(slots)) ...
+    o, lse = store.draft_attn(q, k, v, index, scale, slots)
+    n, token, path = flide.verify_draft(index, tokens, target, u, u_next, draft=draft)
+    store.accumulate_mass(q, k, lse, index, scale, slots)     # before commit
+    store.commit(slots, tree, index, k, v, node_state)
+    store.evict(slots, budget, sinks=4, recent=64)
 """
 from __future__ import annotations
 
@@ -57,6 +68,8 @@ class HistoryStore:
         self.table = torch.full((max_requests * max_blocks,), -1, dtype=torch.int32, device=device)
         self.lengths = torch.zeros(max_requests, dtype=torch.int32, device=device)
         self.status = torch.zeros(1, dtype=torch.int32, device=device)
+        self.mass = None  # attention weight per history row, from accumulate_mass on
+        self.evicted_h = np.zeros(max_requests, np.int32)  # rows evicted per slot
 
     def __del__(self):
         pool = getattr(self, "_pool", None)
@@ -73,6 +86,7 @@ class HistoryStore:
 
     def release(self, slot: int):
         flide._check(self._lib.flide_pool_release(self._pool, slot), "flide_pool_release")
+        self.evicted_h[slot] = 0
         self._sync_table()
 
     def _sync_table(self):
@@ -130,6 +144,60 @@ class HistoryStore:
         req = torch.tensor([int(s) for s in slots], dtype=torch.int32, device=self.device)
         return flide.fork_attn_paged(q, k, v, index, scale, self.pool_k, self.pool_v, self.table,
                                      req, self.block_rows, self.max_blocks, out=out)
+
+    def draft_attn(self, q, k, v, index: flide.TreeIndex, scale: float, slots, out=None, lse=None,
+                   workspace=None):
+        """fork_attn_paged for a few tokens per request over long histories (blocks of
+        any multiple of 16 rows); also returns the log-sum-exp [T, Hq]."""
+        req = torch.tensor([int(s) for s in slots], dtype=torch.int32, device=self.device)
+        return flide.draft_attn_paged(q, k, v, index, scale, self.pool_k, self.pool_v, self.table, req,
+                                      self.block_rows, self.max_blocks, out=out, lse=lse,
+                                      workspace=workspace)
+
+    def pos_offset(self, slots):
+        """Rows evicted from each request's history (int32 [R], device): what its
+        positions are ahead of its past length, for flide.rope."""
+        off = [int(self.evicted_h[s]) if s >= 0 else 0 for s in (int(s) for s in slots)]
+        return torch.tensor(off, dtype=torch.int32, device=self.device)
+
+    def accumulate_mass(self, q, k, lse, index: flide.TreeIndex, scale: float, slots):
+        """Adds the attention weight that this step's root tokens gave each history row,
+        and starts that of the root's own rows: after draft_attn, before commit."""
+        slots = self._once(slots)
+        if self.mass is None:
+            self.mass = torch.zeros((self.max_requests, self.max_blocks * self.block_rows),
+                                    dtype=torch.float32, device=self.device)
+        req = torch.tensor(slots, dtype=torch.int32, device=self.device)
+        flide.history_mass(q, k, lse, index, scale, self.pool_k, self.table, req, self.block_rows,
+                           self.max_blocks, self.mass)
+
+    def evict(self, slots, budget: int, sinks: int = 0, recent: int = 0):
+        """Cuts the histories of `slots` that are longer than `budget` rows down to their
+        first `sinks`, last `recent` and heaviest rows, in place, and frees the blocks
+        past them.  Returns the rows kept, int32 [len(slots), budget], -1 past the end."""
+        slots = self._once(slots)
+        if self.mass is None:
+            raise ValueError("evict needs the rows' attention weight (accumulate_mass)")
+        req = torch.tensor(slots, dtype=torch.int32, device=self.device)
+        kept = flide.history_evict(req, self.lengths, self.table, self.block_rows, self.max_blocks,
+                                   self.pool_k, self.pool_v, self.mass, int(budget), self.status,
+                                   sinks=int(sinks), recent=int(recent))
+        for s in slots:
+            if s >= 0 and self.length(s) > budget:
+                self.evicted_h[s] += self.length(s) - budget
+                flide._check(self._lib.flide_pool_truncate(self._pool, s, int(budget)),
+                             "flide_pool_truncate")
+        self._sync_table()
+        return kept
+
+    @staticmethod
+    def _once(slots):
+        """The slots as ints, each at most once (-1: none)."""
+        slots = [int(s) for s in slots]
+        live = [s for s in slots if s >= 0]
+        if len(set(live)) != len(live):
+            raise ValueError("a slot may stand for one request of a call")
+        return slots
 
     def reserve(self, slots, tree):
         """Host half of commit: reserves each request's root rows in its slot
