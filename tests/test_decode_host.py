@@ -137,7 +137,7 @@ DRAFT = [
     (dict(Hq=12, Hkv=8), S), (dict(d=16), S), (dict(d=100), S), (dict(d=288), S), (dict(dtype=7), S),
     (dict(dtype=flide.E4M3), S), (dict(dtype=flide.E4M3, descale=A, d=64), S), (dict(idx=_idx(R=-1)), S),
     (dict(idx=_idx(T=-1)), S), (dict(idx=_idx(R=4097)), C), (dict(idx=_idx(T=1 << 28)), C), (dict(ws_bytes=100), C),
-    (dict(ws=A + 16), S), (dict(idx=_idx(T=0)), flide.OK), (dict(idx=_idx(R=0)), flide.OK),
+    (dict(ws=A + 16), S), (dict(q=A + 8), S), (dict(idx=_idx(T=0)), flide.OK), (dict(idx=_idx(R=0)), flide.OK),
 ]
 
 
@@ -168,7 +168,7 @@ def test_draft_attn_paged_refusals(lib, kw, code):
 
 @fake
 @pytest.mark.parametrize("kw,code", [x for x in DRAFT if not {"out", "ws", "ws_bytes"} & set(x[0])
-                                     and x[0].get("q", 1) is not NUL and x[1] != C] + PAGED
+                                     and "q" not in x[0] and x[1] != C] + PAGED
                          + [(dict(q=NUL), S), (dict(lse=NUL), S), (dict(mass=NUL), S), (dict(idx=_idx(R=4097)), C)])
 def test_history_mass_refusals(lib, kw, code):
     a = dict(idx=_idx(), q=A, lse=A, pool=A, table=A, slot=A, n_blocks=4, block_rows=16, max_blocks=2, n_slots=2, Hq=16,

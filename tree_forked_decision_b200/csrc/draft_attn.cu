@@ -79,11 +79,52 @@ __device__ __forceinline__ int worker_of(long long U, int W, long long u) {
   return (int)(((u + 1) * W - 1) / U);
 }
 
-// A worker's run: key units [c0, c1) of one item.
+// A worker's run: history rows [k0, k1) of one item (row tile `tile`, kv head
+// hk of a request of `tokens` tokens from t0); base: history_rows.
 struct Run {
-  int r, tile, hk, t0, tokens, hist, k0, k1;
+  int tile, hk, t0, tokens, k0, k1;
   long long base, slot;
 };
+
+// Prefix sums over the requests of their units (of `unit` keys) and items, in
+// shared memory, and for the join kernel in the workspace.
+__device__ __forceinline__ void draft_lists(const DraftParams &p, int unit, long long *unit0,
+                                            long long *item0, long long *part) {
+  const flide_tree_index &x = p.x;
+  request_prefix(x.R, [&](int r) -> long long {
+    int t0;
+    return (long long)tiles_of(request_tokens(x, r, &t0), p.G) * p.Hkv;
+  }, item0, part);
+  request_prefix(x.R, [&](int r) -> long long {
+    long long base;
+    const long long n = history_rows(x, p.hist, r, blockIdx.x == 0, &base);
+    return (item0[r + 1] - item0[r]) * ((n + unit - 1) / unit);
+  }, unit0, part);
+  if (blockIdx.x == 0)
+    for (int r = threadIdx.x; r <= x.R; r += blockDim.x) {
+      p.unit0[r] = unit0[r];
+      p.item0[r] = item0[r];
+    }
+}
+
+// The run that starts at unit u of worker w; returns its units.
+__device__ __forceinline__ int draft_run(const DraftParams &p, const long long *unit0,
+                                         const long long *item0, int unit, long long u,
+                                         long long u_end, int w, Run &run) {
+  const int r = request_of(unit0, p.x.R, u);
+  run.tokens = request_tokens(p.x, r, &run.t0);
+  const int n = history_rows(p.x, p.hist, r, false, &run.base);
+  const int units = (n + unit - 1) / unit;
+  const long long li = (u - unit0[r]) / units;
+  const int c0 = (int)(u - unit0[r] - li * units);
+  const int c1 = (int)min((long long)units, c0 + (u_end - u));
+  run.tile = (int)(li / p.Hkv);
+  run.hk = (int)(li % p.Hkv);
+  run.k0 = c0 * unit;
+  run.k1 = min(n, c1 * unit);
+  run.slot = w + item0[r] + li;
+  return c1 - c0;
+}
 
 // Any element type and head size: CUDA cores, 32 keys a step.
 constexpr int kPT = 128;   // threads
@@ -100,20 +141,7 @@ __global__ void __launch_bounds__(kPT) draft_part_portable(const DraftParams p) 
   long long *unit0 = reinterpret_cast<long long *>(smem), *item0 = unit0 + (R + 1);
   float *sq = smem + 4 * (R + 1) + (4 - (4 * (R + 1)) % 4) % 4, *sk = sq + kRows * ld, *sv = sk + kPKeys * ld;
   float *sp = sv + kPKeys * ld;
-  request_prefix(R, [&](int r) -> long long {
-    int t0;
-    return (long long)tiles_of(request_tokens(x, r, &t0), p.G) * p.Hkv;
-  }, item0, part);
-  request_prefix(R, [&](int r) -> long long {
-    long long base;
-    const long long n = history_rows(x, p.hist, r, blockIdx.x == 0, &base);
-    return (item0[r + 1] - item0[r]) * ((n + kPKeys - 1) / kPKeys);
-  }, unit0, part);
-  if (blockIdx.x == 0)
-    for (int r = tid; r <= R; r += kPT) {
-      p.unit0[r] = unit0[r];
-      p.item0[r] = item0[r];
-    }
+  draft_lists(p, kPKeys, unit0, item0, part);
   const long long U = unit0[R];
   const int w = blockIdx.x, W = workers_of(U, p.workers);
   if (w >= W) return;
@@ -124,23 +152,13 @@ __global__ void __launch_bounds__(kPT) draft_part_portable(const DraftParams p) 
   const float qk_scale = p.scale * kLog2eD * (p.descale ? p.descale[0] * p.descale[1] : 1.f);
   const int nd = d / 32;
   while (u < u_end) {
-    const int r = request_of(unit0, R, u);
-    int t0;
-    const int tokens = request_tokens(x, r, &t0);
-    long long base;
-    const int n = history_rows(x, p.hist, r, false, &base);
-    const int units = (n + kPKeys - 1) / kPKeys;
-    const long long li = (u - unit0[r]) / units;
-    const int c0 = (int)(u - unit0[r] - li * units);
-    const int c1 = (int)min((long long)units, c0 + (u_end - u));
-    const int tile = (int)(li / p.Hkv), hk = (int)(li % p.Hkv);
-    const long long slot = w + item0[r] + li;
-    u += c1 - c0;
+    Run run;
+    u += draft_run(p, unit0, item0, kPKeys, u, u_end, w, run);
     __syncthreads();
     for (int e = tid; e < kRows * d; e += kPT) {
-      const int row = e / d, i = e - row * d, g = tile * kRows + row;
-      sq[row * ld + i] = g < tokens * p.G
-          ? value_of(Q + ((size_t)(t0 + g / p.G) * p.Hq + hk * p.G + g % p.G) * d + i) : 0.f;
+      const int row = e / d, i = e - row * d, g = run.tile * kRows + row;
+      sq[row * ld + i] = g < run.tokens * p.G
+          ? value_of(Q + ((size_t)(run.t0 + g / p.G) * p.Hq + run.hk * p.G + g % p.G) * d + i) : 0.f;
     }
     float m[4], l[4], acc[4][8];
 #pragma unroll
@@ -150,13 +168,13 @@ __global__ void __launch_bounds__(kPT) draft_part_portable(const DraftParams p) 
 #pragma unroll
       for (int j = 0; j < 8; ++j) acc[i][j] = 0.f;
     }
-    for (int c = c0; c < c1; ++c) {
+    for (int k0 = run.k0; k0 < run.k1; k0 += kPKeys) {
       __syncthreads();
-      const int left = min(kPKeys, n - c * kPKeys);
+      const int left = min(kPKeys, run.k1 - k0);
       for (int kr = warp; kr < kPKeys; kr += kPT / 32) {
-        const long long row = kr < left ? history_row(x, p.hist, base, c * kPKeys + kr) : -1;
+        const long long row = kr < left ? history_row(x, p.hist, run.base, k0 + kr) : -1;
         for (int i = lane; i < d; i += 32) {
-          const size_t at = ((size_t)max(row, 0ll) * p.Hkv + hk) * d + i;
+          const size_t at = ((size_t)max(row, 0ll) * p.Hkv + run.hk) * d + i;
           sk[kr * ld + i] = row >= 0 ? value_of(K + at) : 0.f;
           sv[kr * ld + i] = row >= 0 ? value_of(Vp + at) : 0.f;
         }
@@ -200,13 +218,344 @@ __global__ void __launch_bounds__(kPT) draft_part_portable(const DraftParams p) 
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const size_t row = slot * kRows + 4 * warp + j;
+      const size_t row = run.slot * kRows + 4 * warp + j;
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         if (i < nd) p.part_o[row * d + lane + 32 * i] = acc[j][i];
       if (lane == 0) {
         p.part_ml[2 * row] = m[j];
         p.part_ml[2 * row + 1] = l[j];
+      }
+    }
+  }
+}
+
+// ---- tensor-core kernel for few rows -------------------------------------------
+//
+// A tile's 16 rows are one m16n8k16 operand, so a warp needs no tile of keys in
+// shared memory: it streams 16 keys at a time from global memory straight into
+// operand registers and keeps its own running maximum, sum and O.
+//   - S = Q K^T sums over d in any order as long as both operands agree, so a
+//     lane's B operand is what it gets from 16-byte loads of its key row
+//     (lane 4 g + c: key g, bytes 16 c + 64 j): the k index of the instruction
+//     stands for the element that the load puts there, and Q's fragments,
+//     laid out once per run in shared memory, follow it.
+//   - O^T = V^T P^T takes V as the A operand: lane (g, c) loads bytes 16 g of
+//     keys 2c, 2c+1, 2c+8, 2c+9 (a row's 128 bytes by 8 lanes) and byte
+//     permutes pair two keys' elements; row g of tile m is element m of the
+//     lane's own bytes.  P^T is then exactly the accumulator layout of S: the
+//     weights go from one product to the other without leaving their lane.
+// e4m3 codes become half pairs on the way (exact), bf16 stays as it is; the
+// weights are rounded to that type (2^-8 bf16, 2^-11 half, relative) and summed
+// unrounded in 32 bits.  O is rescaled only when a row's maximum grows by more
+// than 2^8.
+//
+// Bound by the history's bytes.
+
+constexpr int kMW = 6;  // warps of a block
+
+__device__ __forceinline__ uint4 ld_stream(const void *p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint32_t word_of(const uint4 &v, int i) {
+  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+}
+// two e4m3 codes (low 16 bits) to a half pair
+__device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t codes) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo;\n\tcvt.u16.u32 lo, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n}" : "=r"(r) : "r"(codes));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+template <bool kHalf>
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  if (kHalf)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};" : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};" : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+template <int D, bool F8>
+struct MmaShape {
+  static constexpr int kRow = D * (F8 ? 1 : 2);  // bytes of a key row
+  static constexpr int kSub = 256 / kRow;        // 16-key groups of a step: 4 KB of K and of V each
+  static constexpr int kCj = kRow / 64;          // a lane's 16-byte loads of a K row
+  static constexpr int kCv = kRow / 128;         // ... of a V row
+  static constexpr int kSteps = D / 16;          // k steps of S, m tiles of O^T
+  static constexpr int kStepKeys = 16 * kSub;
+  static constexpr int kUnit = kMW * kStepKeys;  // one step of every warp
+  static constexpr int kSmem = kRows * D * 4 * kMW + 2 * kMW * kRows * 4;  // O and (max, sum) per warp
+};
+
+template <int D, bool F8>
+__global__ void __launch_bounds__(kMW * 32, 2) draft_part_mma(const DraftParams p) {
+  using S = MmaShape<D, F8>;
+  extern __shared__ float smem[];
+  __shared__ long long part[32];
+  __shared__ uint4 qfrag[S::kSteps * 32];
+  const flide_tree_index &x = p.x;
+  if (failed(x.status)) return;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
+  const int R = x.R;
+  // O [warp][16][D], then max and sum [warp][16]; the prefix arrays after them
+  float *so = smem, *sm = smem + kMW * kRows * D, *sl = sm + kMW * kRows;
+  long long *unit0 = reinterpret_cast<long long *>(sl + kMW * kRows), *item0 = unit0 + (R + 1);
+  draft_lists(p, S::kUnit, unit0, item0, part);
+  const long long U = unit0[R];
+  const int w = blockIdx.x, W = workers_of(U, p.workers);
+  if (w >= W) return;
+  long long u = worker_start(U, W, w);
+  const long long u_end = worker_start(U, W, w + 1);
+  const float qk_scale = p.scale * kLog2eD * (F8 ? p.descale[0] * p.descale[1] : 1.f);
+  const char *Kp = static_cast<const char *>(p.past_k), *Vp = static_cast<const char *>(p.past_v);
+  const size_t stride = (size_t)p.Hkv * S::kRow;
+  while (u < u_end) {
+    Run run;
+    u += draft_run(p, unit0, item0, S::kUnit, u, u_end, w, run);
+    __syncthreads();  // the last run's shared memory is free
+    // Q fragments: lane (g, c) of step s holds rows g, g + 8 at the elements its K loads give
+    for (int e = tid; e < S::kCj * 32; e += kMW * 32) {
+      const int j = e >> 5, eg = (e & 31) >> 2, ec = e & 3;
+      uint4 row[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int qr = run.tile * kRows + eg + 8 * h;
+        row[h] = make_uint4(0u, 0u, 0u, 0u);
+        if (qr < run.tokens * p.G)
+          row[h] = *reinterpret_cast<const uint4 *>(
+              static_cast<const char *>(p.q) +
+              ((size_t)(run.t0 + qr / p.G) * p.Hq + run.hk * p.G + qr % p.G) * S::kRow + 64 * j + 16 * ec);
+      }
+      if (F8) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t a = word_of(row[0], i), b = word_of(row[1], i);
+          qfrag[(4 * j + i) * 32 + (e & 31)] = make_uint4(e4m3x2_to_half2(a), e4m3x2_to_half2(b),
+                                                          e4m3x2_to_half2(a >> 16), e4m3x2_to_half2(b >> 16));
+        }
+      } else {
+        qfrag[(2 * j) * 32 + (e & 31)] = make_uint4(row[0].x, row[1].x, row[0].y, row[1].y);
+        qfrag[(2 * j + 1) * 32 + (e & 31)] = make_uint4(row[0].z, row[1].z, row[0].w, row[1].w);
+      }
+    }
+    __syncthreads();
+
+    float o[2][S::kSteps][4];
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int m = 0; m < S::kSteps; ++m)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[n][m][i] = 0.f;
+    float mx[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};  // rows g, g + 8
+
+    const char *kbase = Kp + (size_t)run.hk * S::kRow + 16 * c, *vbase = Vp + (size_t)run.hk * S::kRow + 16 * g;
+    uint4 kr[S::kSub][2][S::kCj], vr[S::kSub][4][S::kCv];
+    // first row of the 16-key group at history row k (a multiple of 16, as the blocks' sizes)
+    auto row_at = [&](int k) -> long long { return k < run.k1 ? history_row(x, p.hist, run.base, k) : -1; };
+    auto load_k = [&](const long long (&row)[S::kSub], int k0) {
+#pragma unroll
+      for (int s = 0; s < S::kSub; ++s)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const int k = 16 * s + 8 * t + g;
+          const bool ok = row[s] >= 0 && k0 + k < run.k1;
+          const char *src = kbase + (row[s] + 8 * t + g) * stride;
+#pragma unroll
+          for (int j = 0; j < S::kCj; ++j)
+            kr[s][t][j] = ok ? ld_stream(src + 64 * j) : make_uint4(0u, 0u, 0u, 0u);
+        }
+    };
+    auto load_v = [&](const long long (&row)[S::kSub], int k0) {
+#pragma unroll
+      for (int s = 0; s < S::kSub; ++s)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const int k = 2 * c + (t & 1) + 8 * (t >> 1);
+          const bool ok = row[s] >= 0 && k0 + 16 * s + k < run.k1;
+          const char *src = vbase + (row[s] + k) * stride;
+#pragma unroll
+          for (int j = 0; j < S::kCv; ++j)
+            vr[s][t][j] = ok ? ld_stream(src + 128 * j) : make_uint4(0u, 0u, 0u, 0u);
+        }
+    };
+    int k0 = run.k0 + warp * S::kStepKeys;
+    long long row[S::kSub];
+#pragma unroll
+    for (int s = 0; s < S::kSub; ++s) row[s] = row_at(k0 + 16 * s);
+    load_k(row, k0);
+    load_v(row, k0);
+#pragma unroll
+    for (int s = 0; s < S::kSub; ++s) row[s] = row_at(k0 + S::kUnit + 16 * s);
+    for (; k0 < run.k1; k0 += S::kUnit) {
+      float sc[S::kSub][2][4];
+#pragma unroll
+      for (int s = 0; s < S::kSub; ++s)
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sc[s][t][i] = 0.f;
+#pragma unroll
+      for (int st = 0; st < S::kSteps; ++st) {
+        const uint4 a = qfrag[st * 32 + lane];
+#pragma unroll
+        for (int s = 0; s < S::kSub; ++s)
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            uint32_t b0, b1;
+            if (F8) {
+              const uint32_t v = word_of(kr[s][t][st / 4], st % 4);
+              b0 = e4m3x2_to_half2(v);
+              b1 = e4m3x2_to_half2(v >> 16);
+            } else {
+              b0 = word_of(kr[s][t][st / 2], 2 * (st % 2));
+              b1 = word_of(kr[s][t][st / 2], 2 * (st % 2) + 1);
+            }
+            mma16816<F8>(sc[s][t], a.x, a.y, a.z, a.w, b0, b1);
+          }
+      }
+      load_k(row, k0 + S::kUnit);
+      // scores in log2 units, keys past the end out
+      float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+      for (int s = 0; s < S::kSub; ++s)
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const bool in = k0 + 16 * s + 8 * t + 2 * c + (i & 1) < run.k1;
+            const float v = in ? sc[s][t][i] * qk_scale : -INFINITY;
+            sc[s][t][i] = v;
+            top[i >> 1] = fmaxf(top[i >> 1], v);
+          }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 1));
+        top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 2));
+      }
+      if (__any_sync(0xffffffffu, top[0] > mx[0] + 8.f || top[1] > mx[1] + 8.f)) {
+        float f[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float mn = fmaxf(mx[h], top[h]);
+          f[h] = mx[h] == -INFINITY ? 0.f : ex2_approx(mx[h] - mn);
+          mx[h] = mn;
+          sum[h] *= f[h];
+        }
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const float f0 = __shfl_sync(0xffffffffu, f[n], 8 * c), f1 = __shfl_sync(0xffffffffu, f[n], 8 * c + 4);
+#pragma unroll
+          for (int m = 0; m < S::kSteps; ++m) {
+            o[n][m][0] *= f0;
+            o[n][m][1] *= f1;
+            o[n][m][2] *= f0;
+            o[n][m][3] *= f1;
+          }
+        }
+      }
+      const float ref[2] = {mx[0] == -INFINITY ? 0.f : mx[0], mx[1] == -INFINITY ? 0.f : mx[1]};
+#pragma unroll
+      for (int s = 0; s < S::kSub; ++s) {
+        uint32_t b[2][2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float e = ex2_approx(sc[s][t][i] - ref[i >> 1]);
+            sc[s][t][i] = e;
+            sum[i >> 1] += e;
+          }
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+            b[n][t] = F8 ? pack_half2(sc[s][t][2 * n], sc[s][t][2 * n + 1])
+                         : sm100::pack_bf16x2(sc[s][t][2 * n], sc[s][t][2 * n + 1]);
+        }
+#pragma unroll
+        for (int m = 0; m < S::kSteps; ++m) {
+          uint32_t a[4];  // (element m, keys 2c..), (the upper element, keys 2c..), the same of keys 2c + 8..
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int lo = 2 * (i >> 1);                       // keys 2c, 2c+1 or 2c+8, 2c+9
+            const int el = F8 ? m + 8 * (i & 1) : D == 64 ? m + 4 * (i & 1) : m;
+            const int ch = (!F8 && D == 128) ? (i & 1) : 0;
+            if (F8) {
+              const uint32_t v = __byte_perm(word_of(vr[s][lo][ch], el / 4), word_of(vr[s][lo + 1][ch], el / 4),
+                                             (el & 2) ? 0x7362 : 0x5140);
+              a[i] = e4m3x2_to_half2((el & 1) ? v >> 16 : v);
+            } else {
+              a[i] = __byte_perm(word_of(vr[s][lo][ch], el / 2), word_of(vr[s][lo + 1][ch], el / 2),
+                                 (el & 1) ? 0x7632 : 0x5410);
+            }
+          }
+#pragma unroll
+          for (int n = 0; n < 2; ++n) mma16816<F8>(o[n][m], a[0], a[1], a[2], a[3], b[n][0], b[n][1]);
+        }
+      }
+      load_v(row, k0 + S::kUnit);
+#pragma unroll
+      for (int s = 0; s < S::kSub; ++s) row[s] = row_at(k0 + 2 * S::kUnit + 16 * s);
+    }
+    // the warps' results, joined into the run's partial rows
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 1);
+      sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 2);
+      if (c == 0) {
+        sm[warp * kRows + g + 8 * h] = mx[h];
+        sl[warp * kRows + g + 8 * h] = sum[h];
+      }
+    }
+    // lane (g, c) holds rows 2c, 2c + 1 (+ 8 n) at elements 8 g + m (and the upper half's)
+    constexpr int kRun = F8 ? 16 : 8;                         // contiguous elements of a lane
+    constexpr int kUp = F8 ? 8 : D == 64 ? 4 : 64;            // from a tile's row g to its row g + 8
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float *dst = so + (warp * kRows + 8 * n + 2 * c + i) * D + kRun * g;
+#pragma unroll
+        for (int m = 0; m < S::kSteps; ++m) {
+          dst[m] = o[n][m][i];
+          dst[m + kUp] = o[n][m][2 + i];
+        }
+      }
+    __syncthreads();
+    for (int e = tid; e < kRows * D / 4; e += kMW * 32) {
+      const int r = e / (D / 4), i = e - r * (D / 4);
+      float m = sm[r];
+#pragma unroll
+      for (int k = 1; k < kMW; ++k) m = fmaxf(m, sm[k * kRows + r]);
+      const float ref = m == -INFINITY ? 0.f : m;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      float l = 0.f;
+#pragma unroll
+      for (int k = 0; k < kMW; ++k) {
+        const float f = ex2_approx(sm[k * kRows + r] - ref);
+        const float4 v = *reinterpret_cast<const float4 *>(so + (k * kRows + r) * D + 4 * i);
+        acc.x = fmaf(f, v.x, acc.x);
+        acc.y = fmaf(f, v.y, acc.y);
+        acc.z = fmaf(f, v.z, acc.z);
+        acc.w = fmaf(f, v.w, acc.w);
+        l = fmaf(f, sl[k * kRows + r], l);
+      }
+      const size_t at = run.slot * kRows + r;
+      *reinterpret_cast<float4 *>(p.part_o + at * D + 4 * i) = acc;
+      if (i == 0) {
+        p.part_ml[2 * at] = m;
+        p.part_ml[2 * at + 1] = l;
       }
     }
   }
@@ -301,15 +650,32 @@ DraftSpace draft_space(long long R, long long T, long long Hq, long long Hkv, lo
   return s;
 }
 
-template <typename T, typename TOut>
-int draft_launch(DraftParams &p, cudaStream_t s) {
-  const size_t smem = (size_t)(p.x.R + 1) * 16 + 16 +
-                      sizeof(float) * ((size_t)(kRows + 2 * kPKeys) * (p.d + 4) + kRows * kPKeys);
-  if (cudaFuncSetAttribute(draft_part_portable<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)smem) != cudaSuccess)
+// Launches `kernel` on the workers with `smem` bytes of dynamic shared memory.
+int part_launch(void (*kernel)(const DraftParams), const DraftParams &p, int threads, size_t smem,
+                cudaStream_t s) {
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return FLIDE_ERR_CUDA;
-  draft_part_portable<T><<<p.workers, kPT, smem, s>>>(p);
+  kernel<<<p.workers, threads, smem, s>>>(p);
   FLIDE_LAUNCH_CHECK();
+  return FLIDE_OK;
+}
+
+template <typename T>
+int portable_launch(DraftParams &p, int sms, cudaStream_t s) {
+  p.workers = min(kMaxWorkers, 4 * sms);
+  return part_launch(draft_part_portable<T>, p, kPT,
+                     (size_t)(p.x.R + 1) * 16 + 16 +
+                         sizeof(float) * ((size_t)(kRows + 2 * kPKeys) * (p.d + 4) + kRows * kPKeys), s);
+}
+
+template <int D, bool F8>
+int mma_launch(DraftParams &p, int sms, cudaStream_t s) {
+  p.workers = min(kMaxWorkers, 2 * sms);
+  return part_launch(draft_part_mma<D, F8>, p, kMW * 32, MmaShape<D, F8>::kSmem + (size_t)(p.x.R + 1) * 16, s);
+}
+
+template <typename T, typename TOut>
+int join_launch(const DraftParams &p, cudaStream_t s) {
   const long long warps = (long long)p.x.T * p.Hq;
   draft_join_kernel<T, TOut><<<(unsigned)((warps + 7) / 8), 256, 0, s>>>(p);
   FLIDE_LAUNCH_CHECK();
@@ -326,6 +692,7 @@ int draft_attn(const void *q, const void *k, const void *v, const void *past_k, 
   if (dtype == FLIDE_E4M3 && (!descale || d != 128)) return FLIDE_ERR_SHAPE;
   if (idx->R < 0 || idx->T < 0) return FLIDE_ERR_SHAPE;
   if ((uintptr_t)workspace % 256) return FLIDE_ERR_SHAPE;
+  if (((uintptr_t)q | (uintptr_t)k | (uintptr_t)v | (uintptr_t)past_k | (uintptr_t)past_v) % 16) return FLIDE_ERR_SHAPE;
   if (idx->R > kMaxListR || (long long)idx->T * Hq > 0x3fffffffLL) return FLIDE_ERR_CAPACITY;
   if (idx->R == 0 || idx->T == 0) return FLIDE_OK;
   const DraftSpace sp = draft_space(idx->R, idx->T, Hq, Hkv, d);
@@ -349,16 +716,22 @@ int draft_attn(const void *q, const void *k, const void *v, const void *past_k, 
   p.G = Hq / Hkv;
   p.d = d;
   p.scale = scale;
-  p.workers = min(kMaxWorkers, 4 * sms);
   p.out = out;
   p.lse = lse;
   p.unit0 = reinterpret_cast<long long *>(ws + sp.unit0);
   p.item0 = reinterpret_cast<long long *>(ws + sp.item0);
   p.part_ml = reinterpret_cast<float *>(ws + sp.ml);
   p.part_o = reinterpret_cast<float *>(ws + sp.o);
-  if (dtype == FLIDE_F32) return draft_launch<float, float>(p, s);
-  if (dtype == FLIDE_BF16) return draft_launch<__nv_bfloat16, __nv_bfloat16>(p, s);
-  return draft_launch<uint8_t, __nv_bfloat16>(p, s);
+  int rc;
+  if (dtype == FLIDE_F32) rc = portable_launch<float>(p, sms, s);
+  else if (dtype == FLIDE_E4M3) rc = mma_launch<128, true>(p, sms, s);
+  else if (d == 128) rc = mma_launch<128, false>(p, sms, s);
+  else if (d == 64) rc = mma_launch<64, false>(p, sms, s);
+  else rc = portable_launch<__nv_bfloat16>(p, sms, s);
+  if (rc != FLIDE_OK) return rc;
+  if (dtype == FLIDE_F32) return join_launch<float, float>(p, s);
+  if (dtype == FLIDE_BF16) return join_launch<__nv_bfloat16, __nv_bfloat16>(p, s);
+  return join_launch<uint8_t, __nv_bfloat16>(p, s);
 }
 
 }  // namespace
