@@ -27,7 +27,7 @@
 namespace flide {
 namespace {
 
-using sm100::ex2_approx;
+using namespace sm100;
 
 constexpr float kLog2eD = 1.4426950408889634f;
 constexpr float kLn2D = 0.6931471805599453f;
@@ -254,39 +254,6 @@ __global__ void __launch_bounds__(kPT) draft_part_portable(const DraftParams p) 
 
 constexpr int kMW = 6;  // warps of a block
 
-__device__ __forceinline__ uint4 ld_stream(const void *p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-  return v;
-}
-__device__ __forceinline__ uint32_t word_of(const uint4 &v, int i) {
-  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
-}
-// two e4m3 codes (low 16 bits) to a half pair
-__device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t codes) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 lo;\n\tcvt.u16.u32 lo, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n}" : "=r"(r) : "r"(codes));
-  return r;
-}
-__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-template <bool kHalf>
-__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-  if (kHalf)
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};" : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-  else
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};" : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
 template <int D, bool F8>
 struct MmaShape {
   static constexpr int kRow = D * (F8 ? 1 : 2);  // bytes of a key row
@@ -481,7 +448,7 @@ __global__ void __launch_bounds__(kMW * 32, 2) draft_part_mma(const DraftParams 
 #pragma unroll
           for (int n = 0; n < 2; ++n)
             b[n][t] = F8 ? pack_half2(sc[s][t][2 * n], sc[s][t][2 * n + 1])
-                         : sm100::pack_bf16x2(sc[s][t][2 * n], sc[s][t][2 * n + 1]);
+                         : pack_bf16x2(sc[s][t][2 * n], sc[s][t][2 * n + 1]);
         }
 #pragma unroll
         for (int m = 0; m < S::kSteps; ++m) {

@@ -14,8 +14,6 @@
 // `sinks`, the last `recent`, and the rows of largest mass between them (of
 // equal ones the lowest index).  The kept rows stay in order and move to the
 // front of the destination's blocks, in place if they are the source's.
-#include <cuda_fp8.h>
-
 #include "common.cuh"
 #include "sm100.cuh"
 #include "worklist.cuh"
@@ -35,16 +33,7 @@ struct MassParams {
   float scale;
 };
 
-template <typename T>
-__device__ __forceinline__ float element(const T *p) { return load_f(p); }
-template <>
-__device__ __forceinline__ float element<uint8_t>(const uint8_t *p) {
-  __nv_fp8_e4m3 c;
-  c.__x = *p;
-  return (float)c;
-}
-
-// Units of a request: its history rows and its root's rows, kMKeys at a time
+// Units of a request: its history rows and its root's rows, `unit` at a time
 // each.  Requests without a slot have no history and take no part.
 constexpr int kMKeys = 32;
 constexpr int kMThreads = 128;
@@ -55,7 +44,7 @@ __device__ __forceinline__ int root_tokens(const flide_tree_index &x, int r, int
   return n1 > n0 ? x.node_start[n0 + 1] - *t0 : 0;
 }
 
-__device__ __forceinline__ long long mass_units(const MassParams &p, int r, bool report) {
+__device__ __forceinline__ long long mass_units(const MassParams &p, int r, int unit, bool report) {
   const flide_tree_index &x = p.x;
   const int slot = p.hist.req_slot[r];
   if (slot < 0) return 0;
@@ -68,10 +57,10 @@ __device__ __forceinline__ long long mass_units(const MassParams &p, int r, bool
     if (report) set_status(x.status, slot >= p.hist.n_slots ? FLIDE_ERR_INVALID : FLIDE_ERR_CAPACITY);
     return 0;
   }
-  return (n + kMKeys - 1) / kMKeys + (root + kMKeys - 1) / kMKeys;
+  return (n + unit - 1) / unit + (root + unit - 1) / unit;
 }
 
-// Any element type and head size: a lane per key, the heads and tokens split
+// float32, and head sizes of no tensor-core kernel: a lane per key, the heads and tokens split
 // over the warps.
 template <typename T>
 __global__ void __launch_bounds__(kMThreads) mass_kernel_portable(const MassParams p) {
@@ -83,10 +72,9 @@ __global__ void __launch_bounds__(kMThreads) mass_kernel_portable(const MassPara
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, R = x.R, d = p.d, ld = d + 1;
   long long *unit0 = reinterpret_cast<long long *>(smem);
   float *sk = smem + 2 * (R + 1);
-  request_prefix(R, [&](int r) { return mass_units(p, r, blockIdx.x == 0); }, unit0, part);
+  request_prefix(R, [&](int r) { return mass_units(p, r, kMKeys, blockIdx.x == 0); }, unit0, part);
   const T *Q = static_cast<const T *>(p.q), *K = static_cast<const T *>(p.k),
           *Pk = static_cast<const T *>(p.pool_k);
-  const float qk_scale = p.scale * (p.descale ? p.descale[0] * p.descale[1] : 1.f);
   for (long long u = blockIdx.x; u < unit0[R]; u += gridDim.x) {
     const int r = request_of(unit0, R, u);
     int t0;
@@ -105,7 +93,7 @@ __global__ void __launch_bounds__(kMThreads) mass_kernel_portable(const MassPara
       for (int kr = warp; kr < left; kr += kMThreads / 32) {
         const long long row = fresh ? t0 + k0 + kr : history_row(x, p.hist, slot, k0 + kr);
         const T *src = (fresh ? K : Pk) + ((size_t)max(row, 0ll) * p.Hkv + hk) * d;
-        for (int i = lane; i < d; i += 32) sk[kr * ld + i] = row >= 0 ? element(src + i) : 0.f;
+        for (int i = lane; i < d; i += 32) sk[kr * ld + i] = row >= 0 ? load_f(src + i) : 0.f;
       }
       __syncthreads();
       for (int j = warp; j < root * p.G; j += kMThreads / 32) {
@@ -113,9 +101,9 @@ __global__ void __launch_bounds__(kMThreads) mass_kernel_portable(const MassPara
         const T *qr = Q + ((size_t)t * p.Hq + h) * d;
         float s = 0.f;
         if (lane < left)
-          for (int i = 0; i < d; ++i) s = fmaf(element(qr + i), sk[lane * ld + i], s);
+          for (int i = 0; i < d; ++i) s = fmaf(load_f(qr + i), sk[lane * ld + i], s);
         if (lane < left && (!fresh || t0 + k0 + lane <= t))
-          acc += exp2f((s * qk_scale - p.lse[(size_t)t * p.Hq + h]) * kLog2eM);
+          acc += exp2f((s * p.scale - p.lse[(size_t)t * p.Hq + h]) * kLog2eM);
       }
     }
     sums[warp][lane] = acc;
@@ -128,6 +116,159 @@ __global__ void __launch_bounds__(kMThreads) mass_kernel_portable(const MassPara
       p.mass_out[at] = fresh ? all : p.mass[at] + all;
     }
   }
+}
+
+// bf16 rows of 64 or 128 elements and e4m3 rows of 128, on the tensor cores.  A
+// warp takes 16 history rows over all heads, so a row's sum over heads and
+// tokens stays in one lane quad's registers: S^T = K Q^T with the 16 rows as the
+// m16 operand, loaded from global memory straight into its registers, and 8
+// query rows (tokens x heads of the group) as the n8 one, kept in shared memory
+// as the raw 16-byte words that the lanes' k order asks for (see draft_attn.cu).
+// exp(score - lse) of a padding row is exp(-inf) = 0.  The next head's rows are
+// loaded before the current head's are used.  Bound by K's bytes.
+constexpr int kMassWarps = 8;
+constexpr int kMassUnit = 16 * kMassWarps;  // history rows of a unit
+
+template <int D, bool F8>
+struct MassShape {
+  static constexpr int kRow = D * (F8 ? 1 : 2);
+  static constexpr int kCj = kRow / 64;                     // a lane's 16-byte loads of a row
+  static constexpr int kWords = kCj * (F8 ? 2 : 1);         // its 16-byte words of an 8-row query tile
+  static constexpr int kTileBytes = kWords * 32 * 16 + 32;  // and the tile's 8 lse
+  static constexpr int kTiles = 65536 / kTileBytes;         // query tiles held at a time
+};
+
+template <int D, bool F8>
+__global__ void __launch_bounds__(kMassWarps * 32, 2) mass_kernel_mma(const MassParams p) {
+  using S = MassShape<D, F8>;
+  extern __shared__ uint4 qs[];  // [kTiles][kWords][32], then lse [kTiles][8], then the unit prefix
+  __shared__ long long part[32];
+  float *ls = reinterpret_cast<float *>(qs + S::kTiles * S::kWords * 32);
+  long long *unit0 = reinterpret_cast<long long *>(ls + S::kTiles * 8);
+  const flide_tree_index &x = p.x;
+  if (failed(x.status)) return;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3, R = x.R;
+  request_prefix(R, [&](int r) { return mass_units(p, r, kMassUnit, blockIdx.x == 0); }, unit0, part);
+  const long long U = unit0[R];
+  const float sk = F8 ? p.descale[0] * p.descale[1] : 1.f;
+  const float qk_scale = p.scale * sk * kLog2eM;
+  const long long u_end = (blockIdx.x + 1) * U / gridDim.x;
+  int held_r = -1, held_b = -1;  // request and batch of query tiles in shared memory
+  for (long long u = blockIdx.x * U / gridDim.x; u < u_end; ++u) {
+    const int r = request_of(unit0, R, u);
+    int t0;
+    long long slot;
+    const int root = root_tokens(x, r, &t0);
+    const int n = history_rows(x, p.hist, r, false, &slot);
+    slot = p.hist.req_slot[r];
+    const int past_units = (n + kMassUnit - 1) / kMassUnit, cu = (int)(u - unit0[r]);
+    const bool fresh = cu >= past_units;
+    const int len = fresh ? root : n;
+    const int k0 = (fresh ? cu - past_units : cu) * kMassUnit + 16 * warp;
+    const int rows = root * p.G, per = (rows + 7) / 8, tiles = p.Hkv * per;  // tile = head * per + row tile
+    long long row = -1;
+    if (k0 < len) row = fresh ? (long long)t0 + k0 : history_row(x, p.hist, slot, k0);
+    const char *base = static_cast<const char *>(fresh ? p.k : p.pool_k) + 16 * c;
+    const bool ok[2] = {row >= 0 && k0 + g < len, row >= 0 && k0 + g + 8 < len};
+    auto load = [&](int h, uint4 (&kr)[2][S::kCj]) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int j = 0; j < S::kCj; ++j)
+          kr[t][j] = ok[t] ? sm100::ld_stream(base + ((size_t)(row + g + 8 * t) * p.Hkv + h) * S::kRow + 64 * j)
+                           : make_uint4(0u, 0u, 0u, 0u);
+    };
+    uint4 kr[2][S::kCj], nx[2][S::kCj];
+    load(0, nx);
+    float acc[2] = {0.f, 0.f};  // rows k0 + g, k0 + g + 8
+    int head = -1;
+    for (int b0 = 0; b0 < tiles; b0 += S::kTiles) {
+      const int b1 = min(tiles, b0 + S::kTiles);
+      if (held_r != r || held_b != b0) {
+        __syncthreads();
+        for (int e = tid; e < (b1 - b0) * S::kCj * 32; e += kMassWarps * 32) {
+          const int q = e / (S::kCj * 32), j = e / 32 % S::kCj, l = e & 31;
+          const int h = (b0 + q) / per, qr = (b0 + q) % per * 8 + (l >> 2);
+          uint4 v = make_uint4(0u, 0u, 0u, 0u);
+          const size_t at = (size_t)(t0 + qr / p.G) * p.Hq + h * p.G + qr % p.G;
+          if (qr < rows)
+            v = *reinterpret_cast<const uint4 *>(static_cast<const char *>(p.q) + at * S::kRow + 64 * j + 16 * (l & 3));
+          if (F8) {
+            qs[(q * S::kWords + 2 * j) * 32 + l] = make_uint4(sm100::e4m3x2_to_half2(v.x), sm100::e4m3x2_to_half2(v.x >> 16),
+                                                              sm100::e4m3x2_to_half2(v.y), sm100::e4m3x2_to_half2(v.y >> 16));
+            qs[(q * S::kWords + 2 * j + 1) * 32 + l] = make_uint4(sm100::e4m3x2_to_half2(v.z), sm100::e4m3x2_to_half2(v.z >> 16),
+                                                                  sm100::e4m3x2_to_half2(v.w), sm100::e4m3x2_to_half2(v.w >> 16));
+          } else {
+            qs[(q * S::kWords + j) * 32 + l] = v;
+          }
+          if (j == 0 && (l & 3) == 0) ls[q * 8 + (l >> 2)] = qr < rows ? p.lse[at] * kLog2eM : INFINITY;
+        }
+        __syncthreads();
+        held_r = r;
+        held_b = b0;
+      }
+      for (int q = b0; q < b1; ++q) {
+        const int h = q / per;
+        if (h != head) {
+          head = h;
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int j = 0; j < S::kCj; ++j) kr[t][j] = nx[t][j];
+          if (h + 1 < p.Hkv) load(h + 1, nx);
+        }
+        float s[4] = {0.f, 0.f, 0.f, 0.f};
+        const uint4 *qt = qs + (q - b0) * S::kWords * 32 + lane;
+#pragma unroll
+        for (int j = 0; j < S::kWords; ++j) {
+          const uint4 b = qt[j * 32];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            uint32_t a[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              if (F8) {  // word 2 (j % 2) + i of load j / 2: its low and high code pairs
+                const uint32_t v = sm100::word_of(kr[k & 1][j / 2], 2 * (j % 2) + i);
+                a[k] = sm100::e4m3x2_to_half2(k >> 1 ? v >> 16 : v);
+              } else {
+                a[k] = sm100::word_of(kr[k & 1][j], 2 * i + (k >> 1));
+              }
+            }
+            sm100::mma16816<F8>(s, a[0], a[1], a[2], a[3], i ? b.z : b.x, i ? b.w : b.y);
+          }
+        }
+        const int r0 = q % per * 8 + 2 * c;
+        const float2 l2 = *reinterpret_cast<const float2 *>(ls + (q - b0) * 8 + 2 * c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float e = sm100::ex2_approx(fmaf(s[i], qk_scale, -(i & 1 ? l2.y : l2.x)));
+          // a root row is seen by its own token and later ones
+          if (fresh && (r0 + (i & 1)) / p.G < k0 + g + 8 * (i >> 1)) e = 0.f;
+          acc[i >> 1] += e;
+        }
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      acc[t] += __shfl_xor_sync(0xffffffffu, acc[t], 1);
+      acc[t] += __shfl_xor_sync(0xffffffffu, acc[t], 2);
+      if (c == 0 && ok[t]) {
+        const size_t at = (size_t)slot * p.hist.max_blocks * p.hist.block_rows + (fresh ? n : 0) + k0 + g + 8 * t;
+        p.mass_out[at] = fresh ? acc[t] : p.mass[at] + acc[t];
+      }
+    }
+  }
+}
+
+template <int D, bool F8>
+int mass_mma_launch(const MassParams &p, int sms, cudaStream_t s) {
+  const size_t smem = (size_t)MassShape<D, F8>::kTiles * MassShape<D, F8>::kTileBytes + (size_t)(p.x.R + 1) * 8;
+  if (cudaFuncSetAttribute(mass_kernel_mma<D, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)smem) != cudaSuccess)
+    return FLIDE_ERR_CUDA;
+  mass_kernel_mma<D, F8><<<2 * sms, kMassWarps * 32, smem, s>>>(p);
+  FLIDE_LAUNCH_CHECK();
+  return FLIDE_OK;
 }
 
 template <typename T>
@@ -205,6 +346,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
   const bool all = len <= p.budget;
   const int lo = all ? 0 : p.sinks, hi = all ? 0 : len - p.recent;  // candidates
   int want = all ? 0 : p.budget - p.sinks - p.recent;
+  const bool any = want > 0;
   uint32_t prefix = 0, mask = 0;  // codes still in question: (code & mask) == prefix
   if (want > 0) {
     for (int shift = 32 - kBits; ; shift = max(0, shift - kBits)) {
@@ -235,86 +377,131 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
       if (shift == 0) break;
     }
   }
-  // rows above the threshold, the first `want` at it, and the fixed ones.  The
-  // mass of a chunk is read before the chunk's scan and written after it, to
-  // places that are not past the chunk: safe in place.
+  // rows above the threshold, the first `want` at it, and the fixed ones: row i
+  // goes to (sure rows before it) + min(ties before it, want), so one scan of
+  // both counts places four rows a thread.  The masses of a chunk are read
+  // before its scan and written after it, to places not past them: in place works.
   int out = 0, ties = 0;
-  for (int i0 = 0; i0 < len; i0 += kSelThreads) {
-    const int i = i0 + tid;
-    const float v = i < len ? mass[i] : 0.f;
-    bool keep = all || i < lo || i >= hi;
-    int tie = 0;
-    if (!keep && p.budget > p.sinks + p.recent) {
-      const uint32_t c = mass_code(v);
-      keep = c > prefix;
-      tie = c == prefix;
+  for (int i0 = 0; i0 < len; i0 += 4 * kSelThreads) {
+    const int i = i0 + 4 * tid;
+    float v[4];
+    int sure = 0, tie = 0;  // bit k: row i + k
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      v[k] = i + k < len ? mass[i + k] : 0.f;
+      if (i + k >= len) continue;
+      const uint32_t c = mass_code(v[k]);
+      if (all || i + k < lo || i + k >= hi || (any && c > prefix)) sure |= 1 << k;
+      else if (any && c == prefix) tie |= 1 << k;
     }
-    int n_tie = 0, n_keep;
-    const int before = block_excl_scan(tie, scratch, &n_tie);
-    if (tie) keep = ties + before < want;
-    ties += n_tie;
-    keep = keep && i < len;
-    const int j = out + block_excl_scan(keep ? 1 : 0, scratch, &n_keep);
-    if (keep) {
-      kept[j] = i;
-      mass_out[j] = v;
+    int tot;
+    const int before = block_excl_scan(__popc(sure) | __popc(tie) << 16, scratch, &tot);
+    int s = out + (before & 0xffff), e = ties + (before >> 16);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const bool at = tie >> k & 1;
+      if ((sure >> k & 1) || (at && e < want)) {
+        const int j = s + min(e, want);
+        kept[j] = i + k;
+        mass_out[j] = v[k];
+      }
+      s += sure >> k & 1;
+      e += at;
     }
-    out += n_keep;
+    out += tot & 0xffff;
+    ties += tot >> 16;
   }
+  out += min(ties, want);
   for (int j = out + tid; j < p.budget; j += kSelThreads) kept[j] = -1;
 }
 
 constexpr int kMoveThreads = 256;
-constexpr int kSlice = 64;       // bytes of a row that one block moves
-constexpr int kUnroll = 8;       // rows in flight per thread
+constexpr int kUnroll = 8;  // 16-byte words in flight per thread
 
-// Block (slice, request): the slice of every kept row, front to back.  A row
-// never moves backwards past one that is still to be read (kept[j] >= j and
-// ascending), so in one block order is all that in-place movement needs: a
-// chunk is loaded whole before it is stored.
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictParams p) {
+// Where kept row j of a request is and goes; false (status set) without blocks.
+__device__ __forceinline__ bool move_rows(const EvictParams &p, const int32_t *st, const int32_t *dt,
+                                          const int32_t *kept, int j, size_t *from, size_t *to) {
+  const int i = kept[j];
+  const int sb = st[i / p.block_rows], db = dt[j / p.block_rows];
+  if (sb < 0 || sb >= p.n_blocks || db < 0 || db >= p.dst_blocks) {
+    set_status(p.status, FLIDE_ERR_INVALID);
+    return false;
+  }
+  *from = ((size_t)sb * p.block_rows + i % p.block_rows) * p.row_bytes;
+  *to = ((size_t)db * p.block_rows + j % p.block_rows) * p.row_bytes;
+  return true;
+}
+
+// Within a pool.  Block (slice, request) moves `slice` bytes of every kept row,
+// front to back: a row never moves past one that is still to be read (kept is
+// ascending and kept[j] >= j), so in one block order is all that in-place
+// movement needs, and a chunk is loaded whole before it is stored.
+__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictParams p, int slice) {
   const int r = blockIdx.y, tid = threadIdx.x;
   const int len = evict_length(p, r, false);
   if (len < 0) return;
   const int32_t *kept = p.kept + (size_t)r * p.budget;
   const int n = min(len, p.budget);
-  const int slices = (p.row_bytes + kSlice - 1) / kSlice;
+  const int slices = (p.row_bytes + slice - 1) / slice, lanes = slice / 16, rows = kMoveThreads / lanes;
   const bool is_v = (int)blockIdx.x >= slices;
-  const int off = (is_v ? blockIdx.x - slices : blockIdx.x) * kSlice + (tid % (kSlice / 16)) * 16;
+  const int off = (is_v ? blockIdx.x - slices : blockIdx.x) * slice + (tid % lanes) * 16;
   const char *src = is_v ? p.pool_v : p.pool_k;
   char *dst = is_v ? p.dst_v : p.dst_k;
   const size_t slot = p.req_slot[r];
   const int32_t *st = p.table + slot * p.max_blocks, *dt = p.dst_table + slot * p.max_blocks;
-  constexpr int kPer = kMoveThreads / (kSlice / 16);  // rows a step
-  const bool mine = off < p.row_bytes;
   if (n > 0 && kept[0] < 0) return;  // refused by the selection (a slot twice)
-  for (int j0 = 0; j0 < n; j0 += kPer * kUnroll) {
+  for (int j0 = 0; j0 < n; j0 += rows * kUnroll) {
     uint4 v[kUnroll];
     char *to[kUnroll];
 #pragma unroll
     for (int k = 0; k < kUnroll; ++k) {
-      const int j = j0 + k * kPer + tid / (kSlice / 16);
+      const int j = j0 + k * rows + tid / lanes;
+      size_t a, b;
       to[k] = nullptr;
-      if (j >= n || !mine) continue;
-      const int i = kept[j];
-      const int sb = st[i / p.block_rows], db = dt[j / p.block_rows];
-      if (sb < 0 || sb >= p.n_blocks || db < 0 || db >= p.dst_blocks) {
-        set_status(p.status, FLIDE_ERR_INVALID);
-        continue;
-      }
-      const char *from = src + ((size_t)sb * p.block_rows + i % p.block_rows) * p.row_bytes + off;
-      to[k] = dst + ((size_t)db * p.block_rows + j % p.block_rows) * p.row_bytes + off;
-      if (from == to[k]) {
-        to[k] = nullptr;
-        continue;
-      }
-      v[k] = *reinterpret_cast<const uint4 *>(from);
+      if (j >= n || off >= p.row_bytes || !move_rows(p, st, dt, kept, j, &a, &b)) continue;
+      if (src + a == dst + b) continue;
+      to[k] = dst + b + off;
+      v[k] = *reinterpret_cast<const uint4 *>(src + a + off);
     }
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < kUnroll; ++k)
       if (to[k]) *reinterpret_cast<uint4 *>(to[k]) = v[k];
     __syncthreads();
+  }
+}
+
+// Between pools nothing is overwritten: warps copy whole rows in any order.
+__global__ void __launch_bounds__(kMoveThreads) evict_copy_kernel(const EvictParams p) {
+  const int lane = threadIdx.x & 31;
+  const int r = blockIdx.y;
+  const int len = evict_length(p, r, false);
+  if (len < 0) return;
+  const int32_t *kept = p.kept + (size_t)r * p.budget;
+  const int n = min(len, p.budget);
+  if (n > 0 && kept[0] < 0) return;
+  const size_t slot = p.req_slot[r];
+  const int32_t *st = p.table + slot * p.max_blocks, *dt = p.dst_table + slot * p.max_blocks;
+  const int warps = gridDim.x * (kMoveThreads / 32);
+  const int words = p.row_bytes / 16;  // of a K row; its V row's follow
+  for (int j = blockIdx.x * (kMoveThreads / 32) + (threadIdx.x >> 5); j < n; j += warps) {
+    size_t a, b;
+    if (!move_rows(p, st, dt, kept, j, &a, &b)) continue;
+    for (int w0 = lane; w0 < 2 * words; w0 += 32 * kUnroll) {
+      uint4 v[kUnroll];
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k) {
+        const int w = w0 + 32 * k;
+        if (w < 2 * words)
+          v[k] = sm100::ld_stream((w < words ? p.pool_k : p.pool_v) + a + 16 * (size_t)(w < words ? w : w - words));
+      }
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k) {
+        const int w = w0 + 32 * k;
+        if (w < 2 * words)
+          *reinterpret_cast<uint4 *>((w < words ? p.dst_k : p.dst_v) + b + 16 * (size_t)(w < words ? w : w - words)) = v[k];
+      }
+    }
   }
 }
 
@@ -338,6 +525,7 @@ int flide_history_mass(const void *q, const void *k, const float *lse, const voi
   if (dtype != FLIDE_F32 && dtype != FLIDE_BF16 && dtype != FLIDE_E4M3) return FLIDE_ERR_SHAPE;
   if (dtype == FLIDE_E4M3 && (!descale || d != 128)) return FLIDE_ERR_SHAPE;
   if (idx->R < 0 || idx->T < 0) return FLIDE_ERR_SHAPE;
+  if (((uintptr_t)q | (uintptr_t)k | (uintptr_t)pool_k) % 16) return FLIDE_ERR_SHAPE;
   if (idx->R > kMaxListR) return FLIDE_ERR_CAPACITY;
   if (idx->R == 0 || idx->T == 0) return FLIDE_OK;
   int dev = 0, sms = 0;
@@ -361,8 +549,10 @@ int flide_history_mass(const void *q, const void *k, const float *lse, const voi
   p.scale = scale;
   cudaStream_t s = (cudaStream_t)stream;
   if (dtype == FLIDE_F32) return mass_launch<float>(p, sms, s);
-  if (dtype == FLIDE_BF16) return mass_launch<__nv_bfloat16>(p, sms, s);
-  return mass_launch<uint8_t>(p, sms, s);
+  if (dtype == FLIDE_E4M3) return mass_mma_launch<128, true>(p, sms, s);
+  if (d == 128) return mass_mma_launch<128, false>(p, sms, s);
+  if (d == 64) return mass_mma_launch<64, false>(p, sms, s);
+  return mass_launch<__nv_bfloat16>(p, sms, s);
 }
 
 int flide_history_evict(int32_t R, const int32_t *req_slot, int32_t n_slots, const int32_t *hist_len,
@@ -386,6 +576,10 @@ int flide_history_evict(int32_t R, const int32_t *req_slot, int32_t n_slots, con
   if (row_bytes % 16 || row_bytes > (1 << 20)) return FLIDE_ERR_SHAPE;
   if (R > kMaxListR || (int64_t)max_blocks * block_rows > INT32_MAX) return FLIDE_ERR_CAPACITY;
   if (R == 0) return FLIDE_OK;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return FLIDE_ERR_CUDA;
   EvictParams p;
   p.R = R;
   p.n_slots = n_slots;
@@ -412,8 +606,17 @@ int flide_history_evict(int32_t R, const int32_t *req_slot, int32_t n_slots, con
   cudaStream_t s = (cudaStream_t)stream;
   evict_select_kernel<<<R, kSelThreads, 0, s>>>(p);
   FLIDE_LAUNCH_CHECK();
-  const int slices = (int)((row_bytes + kSlice - 1) / kSlice);
-  evict_move_kernel<<<dim3(2 * slices, R), kMoveThreads, 0, s>>>(p);
+  if (dst_k != pool_k && dst_v != pool_v) {
+    const unsigned blocks = (unsigned)min(((int64_t)budget + 7) / 8, max((int64_t)1, (int64_t)16 * sms / R));
+    evict_copy_kernel<<<dim3(blocks, R), kMoveThreads, 0, s>>>(p);
+  } else {
+    // wide slices read and write DRAM in longer runs, narrow ones give a small
+    // batch enough blocks
+    int slice = 256;
+    while (slice > 64 && 2 * ((row_bytes + slice - 1) / slice) * R < 2 * sms) slice /= 2;
+    const unsigned slices = (unsigned)((row_bytes + slice - 1) / slice);
+    evict_move_kernel<<<dim3(2 * slices, R), kMoveThreads, 0, s>>>(p, slice);
+  }
   FLIDE_LAUNCH_CHECK();
   return FLIDE_OK;
 }
