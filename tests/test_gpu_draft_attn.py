@@ -24,6 +24,12 @@ TREES = {
                                           (200, [(-1, 3), (0, 2), (1, 1), (2, 4), (0, 1), (4, 1)]), (0, [(-1, 4)]),
                                           (90, [(-1, 1)] + [(i, 1) for i in range(11)])], 11),
     "wide": lambda: inputs._tree([(700, [(-1, 4)] + [(max(0, i - 3), 1) for i in range(59)])], 59),
+    # 16 and 30 to 70 tokens a request: tiles of 128 and of 256 rows with 4 heads to a group
+    "tile128": lambda: inputs._tree([(n, [(-1, 2)] + [(i // 2, 1) for i in range(14)]) for n in
+                                     (0, 1, 127, 128, 129, 255, 256, 257, 383, 385, 2000)], 4),
+    "tile256": lambda: inputs._tree([(n, [(-1, 3)] + [(i // 2, 1) for i in range(m)]) for n, m in
+                                     ((0, 40), (1, 30), (127, 61), (128, 62), (129, 70), (513, 29), (3001, 61))], 6),
+    "tile128_long": lambda: inputs._tree([(n, [(-1, 1)] + [(0, 1)] * 19) for n in (5100, 4900, 130, 5000)], 1),
     "long_one": lambda: inputs._tree([(5003, [(-1, 1), (0, 1), (1, 1)]), (3, [(-1, 2)])], 2),
     "many": lambda: inputs._tree([(int(n), [(-1, 1 + i % 3), (0, 1), (0, 2), (1, 1)]) for i, n in
                                   enumerate(np.random.default_rng(1).integers(0, 400, 37))], 2),
@@ -79,7 +85,7 @@ def _cat(rows):
 @pytest.mark.parametrize("case", sorted(TREES))
 def test_packed(case, kind):
     tree = TREES[case]()
-    for i, (Hq, Hkv) in enumerate(HEADS if case in ("edges", "odd_requests") else HEADS[1:2]):
+    for i, (Hq, Hkv) in enumerate(HEADS if case in ("edges", "odd_requests", "tile128") else HEADS[1:2]):
         for d in ([128] if kind == "e4m3" else [64, 128, 96, 256] if case == "odd_requests" else [128]):
             x, hist, ds = _inputs(tree, Hq, Hkv, d, kind, 3 + i)
             scale = 1 / math.sqrt(d)
@@ -95,7 +101,7 @@ def test_packed(case, kind):
 
 @pytest.mark.parametrize("kind", ["bf16", "e4m3", "f32"])
 @pytest.mark.parametrize("block_rows", [16, 48, 128, 256])
-@pytest.mark.parametrize("case", ["edges", "odd_requests", "wide", "many"])
+@pytest.mark.parametrize("case", ["edges", "odd_requests", "wide", "tile128", "tile256", "many"])
 def test_paged_with_nan_behind_the_rows(case, block_rows, kind):
     """Rows of a block past a history's end hold NaN, and belong to nobody."""
     tree = TREES[case]()

@@ -17,37 +17,21 @@
 //     fused multiply-adds: a masked key is never multiplied, so what stands in
 //     a sibling branch cannot reach a row, NaN and infinity included.
 // History rows need no mask but their number, and rows past it are not read.
+#include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <math.h>
 
-#include "common.cuh"
+#include <algorithm>
+
+#include "draft.cuh"
 #include "sm100.cuh"
-#include "worklist.cuh"
 
 namespace flide {
 namespace {
 
 using namespace sm100;
 
-constexpr float kLog2eD = 1.4426950408889634f;
 constexpr float kLn2D = 0.6931471805599453f;
-constexpr int kRows = 16;         // query rows of a tile (tokens x heads of the group)
-constexpr int kMaxWorkers = 1024; // what the workspace allows for
-
-struct DraftParams {
-  flide_tree_index x;
-  HistoryView hist;
-  const void *q, *k, *v, *past_k, *past_v;
-  const float *descale;
-  int Hq, Hkv, G, d;
-  float scale;
-  int workers;
-  void *out;
-  float *lse;
-  // workspace: prefix sums of units and items, partial rows and their (max, sum)
-  long long *unit0, *item0;
-  float *part_o, *part_ml;
-};
 
 template <typename T>
 __device__ __forceinline__ float value_of(const T *p) { return load_f(p); }
@@ -58,76 +42,9 @@ __device__ __forceinline__ float value_of<uint8_t>(const uint8_t *p) {
   return (float)c;
 }
 
-// tokens of request r's stream region
-__device__ __forceinline__ int request_tokens(const flide_tree_index &x, int r, int *t0) {
-  const int n0 = x.req_node[r], n1 = x.req_node[r + 1];
-  *t0 = n1 > n0 ? x.node_start[n0] : 0;
-  return n1 > n0 ? x.node_start[n1] - *t0 : 0;
-}
-
-__device__ __forceinline__ int tiles_of(int tokens, int G) {
-  return (int)(((long long)tokens * G + kRows - 1) / kRows);
-}
-
-// workers that get a unit (none of them an empty run: the join reads the slot
-// of every worker between an item's first and last)
-__device__ __forceinline__ int workers_of(long long U, int W) { return (int)min((long long)W, U); }
-// first unit of worker w
-__device__ __forceinline__ long long worker_start(long long U, int W, int w) { return w * U / W; }
-// the worker whose units contain u
-__device__ __forceinline__ int worker_of(long long U, int W, long long u) {
-  return (int)(((u + 1) * W - 1) / U);
-}
-
-// A worker's run: history rows [k0, k1) of one item (row tile `tile`, kv head
-// hk of a request of `tokens` tokens from t0); base: history_rows.
-struct Run {
-  int tile, hk, t0, tokens, k0, k1;
-  long long base, slot;
-};
-
-// Prefix sums over the requests of their units (of `unit` keys) and items, in
-// shared memory, and for the join kernel in the workspace.
-__device__ __forceinline__ void draft_lists(const DraftParams &p, int unit, long long *unit0,
-                                            long long *item0, long long *part) {
-  const flide_tree_index &x = p.x;
-  request_prefix(x.R, [&](int r) -> long long {
-    int t0;
-    return (long long)tiles_of(request_tokens(x, r, &t0), p.G) * p.Hkv;
-  }, item0, part);
-  request_prefix(x.R, [&](int r) -> long long {
-    long long base;
-    const long long n = history_rows(x, p.hist, r, blockIdx.x == 0, &base);
-    return (item0[r + 1] - item0[r]) * ((n + unit - 1) / unit);
-  }, unit0, part);
-  if (blockIdx.x == 0)
-    for (int r = threadIdx.x; r <= x.R; r += blockDim.x) {
-      p.unit0[r] = unit0[r];
-      p.item0[r] = item0[r];
-    }
-}
-
-// The run that starts at unit u of worker w; returns its units.
-__device__ __forceinline__ int draft_run(const DraftParams &p, const long long *unit0,
-                                         const long long *item0, int unit, long long u,
-                                         long long u_end, int w, Run &run) {
-  const int r = request_of(unit0, p.x.R, u);
-  run.tokens = request_tokens(p.x, r, &run.t0);
-  const int n = history_rows(p.x, p.hist, r, false, &run.base);
-  const int units = (n + unit - 1) / unit;
-  const long long li = (u - unit0[r]) / units;
-  const int c0 = (int)(u - unit0[r] - li * units);
-  const int c1 = (int)min((long long)units, c0 + (u_end - u));
-  run.tile = (int)(li / p.Hkv);
-  run.hk = (int)(li % p.Hkv);
-  run.k0 = c0 * unit;
-  run.k1 = min(n, c1 * unit);
-  run.slot = w + item0[r] + li;
-  return c1 - c0;
-}
-
 // Any element type and head size: CUDA cores, 32 keys a step.
 constexpr int kPT = 128;   // threads
+constexpr int kPRows = 16; // rows of a tile
 constexpr int kPKeys = 32; // keys of a unit
 
 template <typename T>
@@ -139,9 +56,9 @@ __global__ void __launch_bounds__(kPT) draft_part_portable(const DraftParams p) 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int d = p.d, ld = d + 4, R = x.R;
   long long *unit0 = reinterpret_cast<long long *>(smem), *item0 = unit0 + (R + 1);
-  float *sq = smem + 4 * (R + 1) + (4 - (4 * (R + 1)) % 4) % 4, *sk = sq + kRows * ld, *sv = sk + kPKeys * ld;
+  float *sq = smem + 4 * (R + 1) + (4 - (4 * (R + 1)) % 4) % 4, *sk = sq + kPRows * ld, *sv = sk + kPKeys * ld;
   float *sp = sv + kPKeys * ld;
-  draft_lists(p, kPKeys, unit0, item0, part);
+  draft_lists(p, unit0, item0, part);
   const long long U = unit0[R];
   const int w = blockIdx.x, W = workers_of(U, p.workers);
   if (w >= W) return;
@@ -153,10 +70,10 @@ __global__ void __launch_bounds__(kPT) draft_part_portable(const DraftParams p) 
   const int nd = d / 32;
   while (u < u_end) {
     Run run;
-    u += draft_run(p, unit0, item0, kPKeys, u, u_end, w, run);
+    u += draft_run(p, unit0, item0, u, u_end, w, run);
     __syncthreads();
-    for (int e = tid; e < kRows * d; e += kPT) {
-      const int row = e / d, i = e - row * d, g = run.tile * kRows + row;
+    for (int e = tid; e < kPRows * d; e += kPT) {
+      const int row = e / d, i = e - row * d, g = run.tile * kPRows + row;
       sq[row * ld + i] = g < run.tokens * p.G
           ? value_of(Q + ((size_t)(run.t0 + g / p.G) * p.Hq + run.hk * p.G + g % p.G) * d + i) : 0.f;
     }
@@ -218,7 +135,7 @@ __global__ void __launch_bounds__(kPT) draft_part_portable(const DraftParams p) 
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const size_t row = run.slot * kRows + 4 * warp + j;
+      const size_t row = run.slot * kPRows + 4 * warp + j;
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         if (i < nd) p.part_o[row * d + lane + 32 * i] = acc[j][i];
@@ -232,7 +149,8 @@ __global__ void __launch_bounds__(kPT) draft_part_portable(const DraftParams p) 
 
 // ---- tensor-core kernel for few rows -------------------------------------------
 //
-// A tile's 16 rows are one m16n8k16 operand, so a warp needs no tile of keys in
+// A tile's 16 rows (or 32: two operands that share a warp's keys) are one
+// m16n8k16 operand, so a warp needs no tile of keys in
 // shared memory: it streams 16 keys at a time from global memory straight into
 // operand registers and keeps its own running maximum, sum and O.
 //   - S = Q K^T sums over d in any order as long as both operands agree, so a
@@ -252,10 +170,11 @@ __global__ void __launch_bounds__(kPT) draft_part_portable(const DraftParams p) 
 //
 // Bound by the history's bytes.
 
-constexpr int kMW = 6;  // warps of a block
-
-template <int D, bool F8>
+template <int D, bool F8, int kMT>
 struct MmaShape {
+  static constexpr int kRows = 16 * kMT;         // query rows of a tile
+  static constexpr int kMW = kMT == 1 ? 6 : 8;   // warps of a block
+  static constexpr int kBlocks = kMT == 1 ? 2 : 1;  // blocks to an SM
   static constexpr int kRow = D * (F8 ? 1 : 2);  // bytes of a key row
   static constexpr int kSub = 256 / kRow;        // 16-key groups of a step: 4 KB of K and of V each
   static constexpr int kCj = kRow / 64;          // a lane's 16-byte loads of a K row
@@ -266,20 +185,23 @@ struct MmaShape {
   static constexpr int kSmem = kRows * D * 4 * kMW + 2 * kMW * kRows * 4;  // O and (max, sum) per warp
 };
 
-template <int D, bool F8>
-__global__ void __launch_bounds__(kMW * 32, 2) draft_part_mma(const DraftParams p) {
-  using S = MmaShape<D, F8>;
+template <int D, bool F8, int kMT>
+__global__ void __launch_bounds__(MmaShape<D, F8, kMT>::kMW * 32, MmaShape<D, F8, kMT>::kBlocks)
+draft_part_mma(const DraftParams p) {
+  using S = MmaShape<D, F8, kMT>;
+  constexpr int kMW = S::kMW, kRows = S::kRows;
   extern __shared__ float smem[];
   __shared__ long long part[32];
-  __shared__ uint4 qfrag[S::kSteps * 32];
+  __shared__ uint4 qfrag[kMT * S::kSteps * 32];
   const flide_tree_index &x = p.x;
+  asm volatile("griddepcontrol.launch_dependents;");
   if (failed(x.status)) return;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
   const int R = x.R;
-  // O [warp][16][D], then max and sum [warp][16]; the prefix arrays after them
+  // O [warp][rows][D], then max and sum [warp][rows]; the prefix arrays after them
   float *so = smem, *sm = smem + kMW * kRows * D, *sl = sm + kMW * kRows;
   long long *unit0 = reinterpret_cast<long long *>(sl + kMW * kRows), *item0 = unit0 + (R + 1);
-  draft_lists(p, S::kUnit, unit0, item0, part);
+  draft_lists(p, unit0, item0, part);
   const long long U = unit0[R];
   const int w = blockIdx.x, W = workers_of(U, p.workers);
   if (w >= W) return;
@@ -290,15 +212,16 @@ __global__ void __launch_bounds__(kMW * 32, 2) draft_part_mma(const DraftParams 
   const size_t stride = (size_t)p.Hkv * S::kRow;
   while (u < u_end) {
     Run run;
-    u += draft_run(p, unit0, item0, S::kUnit, u, u_end, w, run);
+    u += draft_run(p, unit0, item0, u, u_end, w, run);
     __syncthreads();  // the last run's shared memory is free
     // Q fragments: lane (g, c) of step s holds rows g, g + 8 at the elements its K loads give
-    for (int e = tid; e < S::kCj * 32; e += kMW * 32) {
-      const int j = e >> 5, eg = (e & 31) >> 2, ec = e & 3;
+    for (int e = tid; e < kMT * S::kCj * 32; e += kMW * 32) {
+      const int mt = e / (S::kCj * 32), j = (e >> 5) % S::kCj, eg = (e & 31) >> 2, ec = e & 3;
+      uint4 *frag = qfrag + mt * S::kSteps * 32 + (e & 31);
       uint4 row[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int qr = run.tile * kRows + eg + 8 * h;
+        const int qr = run.tile * kRows + 16 * mt + eg + 8 * h;
         row[h] = make_uint4(0u, 0u, 0u, 0u);
         if (qr < run.tokens * p.G)
           row[h] = *reinterpret_cast<const uint4 *>(
@@ -309,24 +232,29 @@ __global__ void __launch_bounds__(kMW * 32, 2) draft_part_mma(const DraftParams 
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const uint32_t a = word_of(row[0], i), b = word_of(row[1], i);
-          qfrag[(4 * j + i) * 32 + (e & 31)] = make_uint4(e4m3x2_to_half2(a), e4m3x2_to_half2(b),
+          frag[(4 * j + i) * 32] = make_uint4(e4m3x2_to_half2(a), e4m3x2_to_half2(b),
                                                           e4m3x2_to_half2(a >> 16), e4m3x2_to_half2(b >> 16));
         }
       } else {
-        qfrag[(2 * j) * 32 + (e & 31)] = make_uint4(row[0].x, row[1].x, row[0].y, row[1].y);
-        qfrag[(2 * j + 1) * 32 + (e & 31)] = make_uint4(row[0].z, row[1].z, row[0].w, row[1].w);
+        frag[(2 * j) * 32] = make_uint4(row[0].x, row[1].x, row[0].y, row[1].y);
+        frag[(2 * j + 1) * 32] = make_uint4(row[0].z, row[1].z, row[0].w, row[1].w);
       }
     }
     __syncthreads();
 
-    float o[2][S::kSteps][4];
+    float o[2 * kMT][S::kSteps][4];
 #pragma unroll
-    for (int n = 0; n < 2; ++n)
+    for (int n = 0; n < 2 * kMT; ++n)
 #pragma unroll
       for (int m = 0; m < S::kSteps; ++m)
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[n][m][i] = 0.f;
-    float mx[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};  // rows g, g + 8
+    float mx[2 * kMT], sum[2 * kMT];  // rows g + 8 n
+#pragma unroll
+    for (int n = 0; n < 2 * kMT; ++n) {
+      mx[n] = -INFINITY;
+      sum[n] = 0.f;
+    }
 
     const char *kbase = Kp + (size_t)run.hk * S::kRow + 16 * c, *vbase = Vp + (size_t)run.hk * S::kRow + 16 * g;
     uint4 kr[S::kSub][2][S::kCj], vr[S::kSub][4][S::kCv];
@@ -367,16 +295,20 @@ __global__ void __launch_bounds__(kMW * 32, 2) draft_part_mma(const DraftParams 
 #pragma unroll
     for (int s = 0; s < S::kSub; ++s) row[s] = row_at(k0 + S::kUnit + 16 * s);
     for (; k0 < run.k1; k0 += S::kUnit) {
-      float sc[S::kSub][2][4];
+      float sc[kMT][S::kSub][2][4];
 #pragma unroll
-      for (int s = 0; s < S::kSub; ++s)
+      for (int q = 0; q < kMT; ++q)
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int s = 0; s < S::kSub; ++s)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) sc[s][t][i] = 0.f;
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sc[q][s][t][i] = 0.f;
 #pragma unroll
       for (int st = 0; st < S::kSteps; ++st) {
-        const uint4 a = qfrag[st * 32 + lane];
+        uint4 a[kMT];
+#pragma unroll
+        for (int q = 0; q < kMT; ++q) a[q] = qfrag[(q * S::kSteps + st) * 32 + lane];
 #pragma unroll
         for (int s = 0; s < S::kSub; ++s)
 #pragma unroll
@@ -390,12 +322,15 @@ __global__ void __launch_bounds__(kMW * 32, 2) draft_part_mma(const DraftParams 
               b0 = word_of(kr[s][t][st / 2], 2 * (st % 2));
               b1 = word_of(kr[s][t][st / 2], 2 * (st % 2) + 1);
             }
-            mma16816<F8>(sc[s][t], a.x, a.y, a.z, a.w, b0, b1);
+#pragma unroll
+            for (int q = 0; q < kMT; ++q) mma16816<F8>(sc[q][s][t], a[q].x, a[q].y, a[q].z, a[q].w, b0, b1);
           }
       }
       load_k(row, k0 + S::kUnit);
       // scores in log2 units, keys past the end out
-      float top[2] = {-INFINITY, -INFINITY};
+      float top[2 * kMT];
+#pragma unroll
+      for (int n = 0; n < 2 * kMT; ++n) top[n] = -INFINITY;
 #pragma unroll
       for (int s = 0; s < S::kSub; ++s)
 #pragma unroll
@@ -403,27 +338,28 @@ __global__ void __launch_bounds__(kMW * 32, 2) draft_part_mma(const DraftParams 
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const bool in = k0 + 16 * s + 8 * t + 2 * c + (i & 1) < run.k1;
-            const float v = in ? sc[s][t][i] * qk_scale : -INFINITY;
-            sc[s][t][i] = v;
-            top[i >> 1] = fmaxf(top[i >> 1], v);
+#pragma unroll
+            for (int q = 0; q < kMT; ++q) {
+              const float v = in ? sc[q][s][t][i] * qk_scale : -INFINITY;
+              sc[q][s][t][i] = v;
+              top[2 * q + (i >> 1)] = fmaxf(top[2 * q + (i >> 1)], v);
+            }
           }
+      bool grown = false;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 1));
-        top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 2));
+      for (int n = 0; n < 2 * kMT; ++n) {
+        top[n] = fmaxf(top[n], __shfl_xor_sync(0xffffffffu, top[n], 1));
+        top[n] = fmaxf(top[n], __shfl_xor_sync(0xffffffffu, top[n], 2));
+        grown |= top[n] > mx[n] + 8.f;
       }
-      if (__any_sync(0xffffffffu, top[0] > mx[0] + 8.f || top[1] > mx[1] + 8.f)) {
-        float f[2];
+      if (__any_sync(0xffffffffu, grown)) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float mn = fmaxf(mx[h], top[h]);
-          f[h] = mx[h] == -INFINITY ? 0.f : ex2_approx(mx[h] - mn);
-          mx[h] = mn;
-          sum[h] *= f[h];
-        }
-#pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          const float f0 = __shfl_sync(0xffffffffu, f[n], 8 * c), f1 = __shfl_sync(0xffffffffu, f[n], 8 * c + 4);
+        for (int n = 0; n < 2 * kMT; ++n) {
+          const float mn = fmaxf(mx[n], top[n]);
+          const float f = mx[n] == -INFINITY ? 0.f : ex2_approx(mx[n] - mn);
+          mx[n] = mn;
+          sum[n] *= f;
+          const float f0 = __shfl_sync(0xffffffffu, f, 8 * c), f1 = __shfl_sync(0xffffffffu, f, 8 * c + 4);
 #pragma unroll
           for (int m = 0; m < S::kSteps; ++m) {
             o[n][m][0] *= f0;
@@ -433,23 +369,19 @@ __global__ void __launch_bounds__(kMW * 32, 2) draft_part_mma(const DraftParams 
           }
         }
       }
-      const float ref[2] = {mx[0] == -INFINITY ? 0.f : mx[0], mx[1] == -INFINITY ? 0.f : mx[1]};
 #pragma unroll
       for (int s = 0; s < S::kSub; ++s) {
-        uint32_t b[2][2];
+        uint32_t b[2 * kMT][2];
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
+        for (int t = 0; t < 2; ++t)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float e = ex2_approx(sc[s][t][i] - ref[i >> 1]);
-            sc[s][t][i] = e;
-            sum[i >> 1] += e;
+          for (int n = 0; n < 2 * kMT; ++n) {
+            const float ref = mx[n] == -INFINITY ? 0.f : mx[n];
+            const float e0 = ex2_approx(sc[n >> 1][s][t][2 * (n & 1)] - ref);
+            const float e1 = ex2_approx(sc[n >> 1][s][t][2 * (n & 1) + 1] - ref);
+            sum[n] += e0 + e1;
+            b[n][t] = F8 ? pack_half2(e0, e1) : pack_bf16x2(e0, e1);
           }
-#pragma unroll
-          for (int n = 0; n < 2; ++n)
-            b[n][t] = F8 ? pack_half2(sc[s][t][2 * n], sc[s][t][2 * n + 1])
-                         : pack_bf16x2(sc[s][t][2 * n], sc[s][t][2 * n + 1]);
-        }
 #pragma unroll
         for (int m = 0; m < S::kSteps; ++m) {
           uint32_t a[4];  // (element m, keys 2c..), (the upper element, keys 2c..), the same of keys 2c + 8..
@@ -468,7 +400,7 @@ __global__ void __launch_bounds__(kMW * 32, 2) draft_part_mma(const DraftParams 
             }
           }
 #pragma unroll
-          for (int n = 0; n < 2; ++n) mma16816<F8>(o[n][m], a[0], a[1], a[2], a[3], b[n][0], b[n][1]);
+          for (int n = 0; n < 2 * kMT; ++n) mma16816<F8>(o[n][m], a[0], a[1], a[2], a[3], b[n][0], b[n][1]);
         }
       }
       load_v(row, k0 + S::kUnit);
@@ -477,19 +409,19 @@ __global__ void __launch_bounds__(kMW * 32, 2) draft_part_mma(const DraftParams 
     }
     // the warps' results, joined into the run's partial rows
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 1);
-      sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 2);
+    for (int n = 0; n < 2 * kMT; ++n) {
+      sum[n] += __shfl_xor_sync(0xffffffffu, sum[n], 1);
+      sum[n] += __shfl_xor_sync(0xffffffffu, sum[n], 2);
       if (c == 0) {
-        sm[warp * kRows + g + 8 * h] = mx[h];
-        sl[warp * kRows + g + 8 * h] = sum[h];
+        sm[warp * kRows + g + 8 * n] = mx[n];
+        sl[warp * kRows + g + 8 * n] = sum[n];
       }
     }
     // lane (g, c) holds rows 2c, 2c + 1 (+ 8 n) at elements 8 g + m (and the upper half's)
     constexpr int kRun = F8 ? 16 : 8;                         // contiguous elements of a lane
     constexpr int kUp = F8 ? 8 : D == 64 ? 4 : 64;            // from a tile's row g to its row g + 8
 #pragma unroll
-    for (int n = 0; n < 2; ++n)
+    for (int n = 0; n < 2 * kMT; ++n)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         float *dst = so + (warp * kRows + 8 * n + 2 * c + i) * D + kRun * g;
@@ -528,10 +460,11 @@ __global__ void __launch_bounds__(kMW * 32, 2) draft_part_mma(const DraftParams 
   }
 }
 
-// One warp per (token, query head): the tokens on its path, then the partial
-// results of its history, then the output row and its log-sum-exp.
+// Any element type and head size: one warp per (token, query head): the tokens on
+// its path, then the partial results of its history, then the output row and its
+// log-sum-exp.
 template <typename T, typename TOut>
-__global__ void __launch_bounds__(256) draft_join_kernel(const DraftParams p) {
+__global__ void __launch_bounds__(256) draft_join_portable(const DraftParams p) {
   const flide_tree_index &x = p.x;
   if (failed(x.status)) return;
   const int lane = threadIdx.x & 31;
@@ -575,12 +508,12 @@ __global__ void __launch_bounds__(256) draft_join_kernel(const DraftParams p) {
   const long long per = items > 0 ? (p.unit0[r + 1] - ua) / items : 0;  // units of one item
   if (per > 0) {
     const int row = (t - x.node_start[x.req_node[r]]) * p.G + h % p.G;
-    const long long li = (long long)(row / kRows) * p.Hkv + hk;
+    const long long li = (long long)(row / p.tile_rows) * p.Hkv + hk;
     const long long u0 = ua + li * per;
     const int W = workers_of(U, p.workers);
     const int w0 = worker_of(U, W, u0), w1 = worker_of(U, W, u0 + per - 1);
     for (int w = w0; w <= w1; ++w) {
-      const size_t pr = (size_t)(w + p.item0[r] + li) * kRows + row % kRows;
+      const size_t pr = (size_t)(w + p.item0[r] + li) * p.slot_rows + row % p.tile_rows;
       const float pm = p.part_ml[2 * pr], pl = p.part_ml[2 * pr + 1];
       const float mn = fmaxf(m, pm), ref = mn == -INFINITY ? 0.f : mn;
       const float f = exp2f(m - ref), g = exp2f(pm - ref);
@@ -599,21 +532,215 @@ __global__ void __launch_bounds__(256) draft_join_kernel(const DraftParams p) {
   if (p.lse && lane == 0) p.lse[(size_t)t * p.Hq + h] = (m + log2f(l)) * kLn2D;
 }
 
+// D elements of type T as they lie for an 8-lane group: a lane's are kE / kW words
+// of kW, word i at element (8 i + lane) kW, so that a group reads whole rows.
+template <typename T, int D>
+struct Row8 {
+  static constexpr int kE = D / 8;
+  static __device__ __forceinline__ void load(const T *p, int l, float (&v)[kE]) {
+    constexpr int kW = sizeof(T) == 1 ? 16 : sizeof(T) == 2 ? 8 : 4;
+#pragma unroll
+    for (int i = 0; i < kE / kW; ++i) {
+      const uint4 w = *reinterpret_cast<const uint4 *>(p + (8 * i + l) * kW);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t u = word_of(w, j);
+        float *o = v + i * kW + j * (kW / 4);
+        if constexpr (sizeof(T) == 4) {
+          o[0] = __uint_as_float(u);
+        } else if constexpr (sizeof(T) == 2) {
+          o[0] = __uint_as_float(u << 16);
+          o[1] = __uint_as_float(u & 0xffff0000u);
+        } else {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t pair = e4m3x2_to_half2(h ? u >> 16 : u);
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&pair));
+            o[2 * h] = f.x;
+            o[2 * h + 1] = f.y;
+          }
+        }
+      }
+    }
+  }
+  // element of v[e]
+  static __device__ __forceinline__ int at(int e, int l) {
+    constexpr int kW = sizeof(T) == 1 ? 16 : sizeof(T) == 2 ? 8 : 4;
+    return (8 * (e / kW) + l) * kW + e % kW;
+  }
+};
+
+// bf16 and e4m3, d of 64 or 128: one warp per (token, query head) as four groups
+// of eight lanes, each with its own running (max, sum, O) over every fourth key
+// of the token's path and every fourth partial of its history, so that four
+// rows are on their way at a time; joined by shuffles at the end.  The path is
+// found by all lanes at once (a lane per ancestor).  Runs beside the part kernel
+// (programmatic launch) up to where it needs its results.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) draft_join_kernel(const DraftParams p) {
+  using Row = Row8<T, D>;
+  constexpr int kE = Row::kE;
+  const flide_tree_index &x = p.x;
+  const int lane = threadIdx.x & 31, grp = lane >> 3, l8 = lane & 7;
+  const long long job = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+  const int t = (int)(job / p.Hq), h = (int)(job % p.Hq), hk = h / p.G;
+  const bool live = !failed(x.status) && t < x.counts[FLIDE_CNT_T];
+  float m = -INFINITY, l = 0.f, acc[kE];
+#pragma unroll
+  for (int e = 0; e < kE; ++e) acc[e] = 0.f;
+  int r = 0;
+  if (live) {
+    const T *Q = static_cast<const T *>(p.q), *K = static_cast<const T *>(p.k), *Vs = static_cast<const T *>(p.v);
+    const float qk_scale = p.scale * kLog2eD * (p.descale ? p.descale[0] * p.descale[1] : 1.f);
+    float qv[kE];
+    Row::load(Q + ((size_t)t * p.Hq + h) * D, l8, qv);
+    const int n = (int)checked(x.status, x.counts, x.token_node[t], x.counts[FLIDE_CNT_N], 801);
+    r = x.node_req[n];
+    for (int a0 = x.anc_ptr[n], a1 = x.anc_ptr[n + 1]; a0 < a1; a0 += 32) {
+      int first = 0, len = 0;  // this lane's ancestor: its keys
+      if (a0 + lane < a1) {
+        const int node = x.anc_node[a0 + lane];
+        first = x.node_start[node];
+        len = (node == n ? t + 1 : x.node_start[node + 1]) - first;
+      }
+      const int end = warp_incl_scan(len), total = __shfl_sync(0xffffffffu, end, 31);
+      const int na = min(32, a1 - a0);
+      for (int k0 = 0; k0 < total; k0 += 4) {
+        const int k = k0 + grp;
+        int j = 0;
+        for (int a = 0; a < na; ++a) {
+          const int e = __shfl_sync(0xffffffffu, end, a), f = __shfl_sync(0xffffffffu, first, a);
+          const int b = __shfl_sync(0xffffffffu, len, a);
+          if (k >= e - b && k < e) j = f + k - (e - b);
+        }
+        const bool on = k < total;
+        float kv[kE], vv[kE];
+        if (on) {
+          Row::load(K + ((size_t)j * p.Hkv + hk) * D, l8, kv);
+          Row::load(Vs + ((size_t)j * p.Hkv + hk) * D, l8, vv);
+        }
+        float s = 0.f;
+        if (on) {
+#pragma unroll
+          for (int e = 0; e < kE; ++e) s = fmaf(qv[e], kv[e], s);
+        }
+        s += __shfl_xor_sync(0xffffffffu, s, 1);
+        s += __shfl_xor_sync(0xffffffffu, s, 2);
+        s += __shfl_xor_sync(0xffffffffu, s, 4);
+        if (on) {
+          s *= qk_scale;
+          const float mn = fmaxf(m, s), ref = mn == -INFINITY ? 0.f : mn;
+          const float f = ex2_approx(m - ref), w = ex2_approx(s - ref);
+          l = l * f + w;
+          m = mn;
+#pragma unroll
+          for (int e = 0; e < kE; ++e) acc[e] = fmaf(w, vv[e], acc[e] * f);
+        }
+      }
+    }
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the part kernel's results
+  if (!live || failed(x.status)) return;
+  const long long U = p.unit0[x.R], ua = p.unit0[r], ia = p.item0[r];
+  const long long items = p.item0[r + 1] - ia;
+  const long long per = items > 0 ? (p.unit0[r + 1] - ua) / items : 0;  // units of one item
+  if (per > 0) {
+    const int row = (t - x.node_start[x.req_node[r]]) * p.G + h % p.G;
+    const long long li = (long long)(row / p.tile_rows) * p.Hkv + hk;
+    const long long u0 = ua + li * per;
+    const int W = workers_of(U, p.workers);
+    const int w0 = worker_of(U, W, u0), w1 = worker_of(U, W, u0 + per - 1);
+    const int parts = (w1 - w0 + 1) << p.halves;
+    for (int i = grp; i < parts; i += 4) {
+      const size_t pr = (size_t)(w0 + (i >> p.halves) + ia + li) * p.slot_rows + row % p.tile_rows +
+                        ((i & p.halves) ? p.slot_rows / 2 : 0);
+      const float2 ml = *reinterpret_cast<const float2 *>(p.part_ml + 2 * pr);
+      float v[kE];
+#pragma unroll
+      for (int e = 0; e < kE; e += 4)
+        *reinterpret_cast<float4 *>(v + e) =
+            *reinterpret_cast<const float4 *>(p.part_o + pr * D + Row::at(e, l8));
+      if (ml.x == -INFINITY) continue;  // an empty partial
+      const float mn = fmaxf(m, ml.x);
+      const float f = ex2_approx(m - mn), g = ex2_approx(ml.x - mn);
+      l = l * f + ml.y * g;
+      m = mn;
+#pragma unroll
+      for (int e = 0; e < kE; ++e) acc[e] = fmaf(g, v[e], acc[e] * f);
+    }
+  }
+  // the four groups' results
+  float mt = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+  mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 16));
+  const float f = m == -INFINITY ? 0.f : ex2_approx(m - mt);
+  l *= f;
+  l += __shfl_xor_sync(0xffffffffu, l, 8);
+  l += __shfl_xor_sync(0xffffffffu, l, 16);
+  const float inv = (p.descale ? p.descale[2] : 1.f) / l;
+#pragma unroll
+  for (int e = 0; e < kE; ++e) {
+    acc[e] *= f;
+    acc[e] += __shfl_xor_sync(0xffffffffu, acc[e], 8);
+    acc[e] += __shfl_xor_sync(0xffffffffu, acc[e], 16);
+    acc[e] *= inv;
+  }
+  // a group stores a quarter of its lanes' elements
+  __nv_bfloat16 *O = static_cast<__nv_bfloat16 *>(p.out) + ((size_t)t * p.Hq + h) * D;
+#pragma unroll
+  for (int e = 0; e < kE; e += 4)
+    if (e / 4 % 4 == grp || (kE < 16 && e / 4 == grp))
+      *reinterpret_cast<uint2 *>(O + Row::at(e, l8)) =
+          make_uint2(pack_bf16x2(acc[e], acc[e + 1]), pack_bf16x2(acc[e + 2], acc[e + 3]));
+  if (p.lse && lane == 0) p.lse[(size_t)t * p.Hq + h] = (mt + log2f(l)) * kLn2D;
+}
+
+// ---- host ----------------------------------------------------------------------
+
+// Which part kernel, by the query rows of a request on average (the capacities:
+// the host sees no more): up to 16 rows one 16-row tile, up to 32 one of 32, and
+// above that, where the tcgen05 kernel takes the type and head layout, tiles of
+// 128 or 256; elsewhere more 32-row tiles, each a pass over the keys.
+enum Variant { kPortable, kMma16, kMma32, kWide128, kWide256 };
+
+Variant variant_of(long long R, long long T, int G, int d, int dtype) {
+  if (dtype == FLIDE_F32 || (d != 64 && d != 128)) return kPortable;
+  const long long rows = (T * G + R - 1) / (R > 0 ? R : 1);
+  if (rows <= 16) return kMma16;
+  if (rows <= 32 || dtype != FLIDE_BF16 || d != 128 || 128 % G) return kMma32;
+  return rows <= 128 || R > 2048 ? kWide128 : kWide256;  // 256 rows leave less room for the lists
+}
+
+struct Shape {
+  int tile_rows, slot_rows, halves;
+};
+Shape shape_of(Variant v) {
+  switch (v) {
+    case kMma32: return {32, 32, 0};
+    case kWide128: return {128, 256, 1};
+    case kWide256: return {256, 256, 0};
+    default: return {16, 16, 0};
+  }
+}
+
+constexpr int kMaxWorkers = 640;  // of any variant: what the workspace allows for
+constexpr int kWideWorkers = 160; // of the wide ones, one to an SM
+
 struct DraftSpace {
   size_t unit0, item0, ml, o, total;
 };
 
 // Bytes of the workspace's parts: a slot for every worker and item.
-DraftSpace draft_space(long long R, long long T, long long Hq, long long Hkv, long long d) {
-  const long long G = Hq / Hkv;
-  const long long slots = kMaxWorkers + ((T * G + kRows - 1) / kRows + R) * Hkv;
-  auto up = [](size_t v) { return (v + 255) / 256 * 256; };
+DraftSpace draft_space(long long R, long long T, int Hkv, int G, int d, Variant v) {
+  const Shape sh = shape_of(v);
+  const long long slots = (v >= kWide128 ? kWideWorkers : kMaxWorkers) +
+                          ((T * G + sh.tile_rows - 1) / sh.tile_rows + R) * Hkv;
+  auto up = [](size_t n) { return (n + 255) / 256 * 256; };
   DraftSpace s;
   s.unit0 = 0;
   s.item0 = up((R + 1) * sizeof(long long));
   s.ml = s.item0 + up((R + 1) * sizeof(long long));
-  s.o = s.ml + up((size_t)slots * kRows * 2 * sizeof(float));
-  s.total = s.o + up((size_t)slots * kRows * d * sizeof(float));
+  s.o = s.ml + up((size_t)slots * sh.slot_rows * 2 * sizeof(float));
+  s.total = s.o + up((size_t)slots * sh.slot_rows * d * sizeof(float));
   return s;
 }
 
@@ -630,27 +757,45 @@ int part_launch(void (*kernel)(const DraftParams), const DraftParams &p, int thr
 template <typename T>
 int portable_launch(DraftParams &p, int sms, cudaStream_t s) {
   p.workers = min(kMaxWorkers, 4 * sms);
+  p.unit = kPKeys;
   return part_launch(draft_part_portable<T>, p, kPT,
                      (size_t)(p.x.R + 1) * 16 + 16 +
-                         sizeof(float) * ((size_t)(kRows + 2 * kPKeys) * (p.d + 4) + kRows * kPKeys), s);
+                         sizeof(float) * ((size_t)(kPRows + 2 * kPKeys) * (p.d + 4) + kPRows * kPKeys), s);
 }
 
-template <int D, bool F8>
+template <int D, bool F8, int kMT>
 int mma_launch(DraftParams &p, int sms, cudaStream_t s) {
-  p.workers = min(kMaxWorkers, 2 * sms);
-  return part_launch(draft_part_mma<D, F8>, p, kMW * 32, MmaShape<D, F8>::kSmem + (size_t)(p.x.R + 1) * 16, s);
+  using S = MmaShape<D, F8, kMT>;
+  p.workers = min(kMaxWorkers, S::kBlocks * sms);
+  p.unit = S::kUnit;
+  return part_launch(draft_part_mma<D, F8, kMT>, p, S::kMW * 32, S::kSmem + (size_t)(p.x.R + 1) * 16, s);
 }
 
 template <typename T, typename TOut>
-int join_launch(const DraftParams &p, cudaStream_t s) {
+int join_portable_launch(const DraftParams &p, cudaStream_t s) {
   const long long warps = (long long)p.x.T * p.Hq;
-  draft_join_kernel<T, TOut><<<(unsigned)((warps + 7) / 8), 256, 0, s>>>(p);
+  draft_join_portable<T, TOut><<<(unsigned)((warps + 7) / 8), 256, 0, s>>>(p);
   FLIDE_LAUNCH_CHECK();
   return FLIDE_OK;
 }
 
+template <typename T, int D>
+int join_launch(const DraftParams &p, cudaStream_t s) {
+  const long long warps = (long long)p.x.T * p.Hq;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((warps + 7) / 8));
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, draft_join_kernel<T, D>, p) == cudaSuccess ? FLIDE_OK : FLIDE_ERR_CUDA;
+}
+
 int draft_attn(const void *q, const void *k, const void *v, const void *past_k, const void *past_v,
-               const HistoryView &hist, const flide_tree_index *idx, int Hq, int Hkv, int d, int dtype,
+               const HistoryView &hist, int past_rows, const flide_tree_index *idx, int Hq, int Hkv, int d, int dtype,
                const float *descale, float scale, void *out, float *lse, void *workspace,
                size_t workspace_bytes, cudaStream_t s) {
   if (!idx || !q || !k || !v || !out || !workspace) return FLIDE_ERR_SHAPE;
@@ -662,7 +807,9 @@ int draft_attn(const void *q, const void *k, const void *v, const void *past_k, 
   if (((uintptr_t)q | (uintptr_t)k | (uintptr_t)v | (uintptr_t)past_k | (uintptr_t)past_v) % 16) return FLIDE_ERR_SHAPE;
   if (idx->R > kMaxListR || (long long)idx->T * Hq > 0x3fffffffLL) return FLIDE_ERR_CAPACITY;
   if (idx->R == 0 || idx->T == 0) return FLIDE_OK;
-  const DraftSpace sp = draft_space(idx->R, idx->T, Hq, Hkv, d);
+  const Variant var = variant_of(idx->R, idx->T, Hq / Hkv, d, dtype);
+  const Shape sh = shape_of(var);
+  const DraftSpace sp = draft_space(idx->R, idx->T, Hkv, Hq / Hkv, d, var);
   if (workspace_bytes < sp.total) return FLIDE_ERR_CAPACITY;
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
@@ -683,6 +830,9 @@ int draft_attn(const void *q, const void *k, const void *v, const void *past_k, 
   p.G = Hq / Hkv;
   p.d = d;
   p.scale = scale;
+  p.tile_rows = sh.tile_rows;
+  p.slot_rows = sh.slot_rows;
+  p.halves = sh.halves;
   p.out = out;
   p.lse = lse;
   p.unit0 = reinterpret_cast<long long *>(ws + sp.unit0);
@@ -690,15 +840,29 @@ int draft_attn(const void *q, const void *k, const void *v, const void *past_k, 
   p.part_ml = reinterpret_cast<float *>(ws + sp.ml);
   p.part_o = reinterpret_cast<float *>(ws + sp.o);
   int rc;
-  if (dtype == FLIDE_F32) rc = portable_launch<float>(p, sms, s);
-  else if (dtype == FLIDE_E4M3) rc = mma_launch<128, true>(p, sms, s);
-  else if (d == 128) rc = mma_launch<128, false>(p, sms, s);
-  else if (d == 64) rc = mma_launch<64, false>(p, sms, s);
-  else rc = portable_launch<__nv_bfloat16>(p, sms, s);
+  switch (var) {
+    case kPortable:
+      rc = dtype == FLIDE_F32 ? portable_launch<float>(p, sms, s) : portable_launch<__nv_bfloat16>(p, sms, s);
+      if (rc != FLIDE_OK) return rc;
+      return dtype == FLIDE_F32 ? join_portable_launch<float, float>(p, s)
+                                : join_portable_launch<__nv_bfloat16, __nv_bfloat16>(p, s);
+    case kMma16:
+      rc = dtype == FLIDE_E4M3 ? mma_launch<128, true, 1>(p, sms, s)
+           : d == 128          ? mma_launch<128, false, 1>(p, sms, s)
+                               : mma_launch<64, false, 1>(p, sms, s);
+      break;
+    case kMma32:
+      rc = dtype == FLIDE_E4M3 ? mma_launch<128, true, 2>(p, sms, s)
+           : d == 128          ? mma_launch<128, false, 2>(p, sms, s)
+                               : mma_launch<64, false, 2>(p, sms, s);
+      break;
+    default:
+      p.workers = min(kWideWorkers, sms);
+      rc = draft_wide_launch(p, past_rows, s);
+  }
   if (rc != FLIDE_OK) return rc;
-  if (dtype == FLIDE_F32) return join_launch<float, float>(p, s);
-  if (dtype == FLIDE_BF16) return join_launch<__nv_bfloat16, __nv_bfloat16>(p, s);
-  return join_launch<uint8_t, __nv_bfloat16>(p, s);
+  if (dtype == FLIDE_E4M3) return join_launch<uint8_t, 128>(p, s);
+  return d == 128 ? join_launch<__nv_bfloat16, 128>(p, s) : join_launch<__nv_bfloat16, 64>(p, s);
 }
 
 }  // namespace
@@ -708,7 +872,11 @@ extern "C" {
 
 size_t flide_draft_attn_workspace_bytes(int32_t R, int32_t T, int32_t Hq, int32_t Hkv, int32_t d) {
   if (R < 0 || T < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || d <= 0) return 0;
-  return flide::draft_space(R, T, Hq, Hkv, d).total;
+  size_t most = 0;  // the element type, which chooses the kernel too, is not known here
+  for (int dtype : {FLIDE_F32, FLIDE_BF16, FLIDE_E4M3})
+    most = std::max(most, flide::draft_space(R, T, Hkv, Hq / Hkv, d,
+                                             flide::variant_of(R, T, Hq / Hkv, d, dtype)).total);
+  return most;
 }
 
 int flide_draft_attn(const void *q, const void *k, const void *v, const void *past_k,
@@ -718,7 +886,7 @@ int flide_draft_attn(const void *q, const void *k, const void *v, const void *pa
                      flide_stream stream) {
   if (past_rows < 0 || (past_k == nullptr) != (past_v == nullptr)) return FLIDE_ERR_SHAPE;
   const flide::HistoryView h{nullptr, nullptr, 0, 0, 0, 0, past_k ? past_rows : 0};
-  return flide::draft_attn(q, k, v, past_k, past_v, h, idx, Hq, Hkv, d, dtype, descale, scale, out,
+  return flide::draft_attn(q, k, v, past_k, past_v, h, past_k ? past_rows : 0, idx, Hq, Hkv, d, dtype, descale, scale, out,
                            lse, workspace, workspace_bytes, (cudaStream_t)stream);
 }
 
@@ -731,8 +899,9 @@ int flide_draft_attn_paged(const void *q, const void *k, const void *v, const vo
   if (!pool_k || !pool_v || !block_table || !req_slot) return FLIDE_ERR_SHAPE;
   if (n_blocks <= 0 || max_blocks <= 0 || n_slots <= 0 || block_rows <= 0 || block_rows % 16)
     return FLIDE_ERR_SHAPE;
+  if ((long long)n_blocks * block_rows > 0x7fffffffLL) return FLIDE_ERR_CAPACITY;
   const flide::HistoryView h{block_table, req_slot, max_blocks, block_rows, n_blocks, n_slots, 0};
-  return flide::draft_attn(q, k, v, pool_k, pool_v, h, idx, Hq, Hkv, d, dtype, descale, scale, out,
+  return flide::draft_attn(q, k, v, pool_k, pool_v, h, n_blocks * block_rows, idx, Hq, Hkv, d, dtype, descale, scale, out,
                            lse, workspace, workspace_bytes, (cudaStream_t)stream);
 }
 

@@ -1,0 +1,415 @@
+// draft_wide.cu -- draft attention's part kernel for wide trees, on tcgen05.
+//
+// A tile of query rows (tokens x heads of the group) is one or two 128-row
+// operands.  Keys come in tiles of 128 by TMA, K and V each through a ring of
+// stages; S = Q K^T and O += P V accumulate in TMEM, the softmax reads S and
+// writes P there, one row a thread.  Two softmax warpgroups work on two S
+// buffers, so the tensor core always has the other one's products to do:
+//   - 256 rows: each warpgroup has its own 128 rows, both see every key tile;
+//   - 128 rows: both have the same rows and take every second key tile; their
+//     (O, max, sum) are two partials for the join.  One operand's softmax alone
+//     would leave the tensor core and the memory idle half the time.
+// A block (one to an SM) takes its share of the batch's key tiles as runs
+// inside one (request, row tile, kv head) item (draft.cuh); barriers count over
+// the block's life, so the next run's loads are in flight while the last tiles
+// of a run are computed.  V rows behind the history's end are zeroed in shared
+// memory before they are multiplied: their weight is 0, but what stands there
+// may be NaN.
+//
+// 256 rows are bound by the two warpgroups' softmax and the MMA issue (see
+// attn_tc.cu), 128 rows by the history's bytes.  Every wait is bounded (2 s);
+// on expiry the block records FLIDE_ERR_TIMEOUT, waits for its own copies and
+// MMAs, frees TMEM and ends.
+#include <cstddef>
+#include <cuda.h>
+
+#include "draft.cuh"
+#include "sm100.cuh"
+
+namespace flide {
+namespace {
+
+using namespace sm100;
+
+constexpr int kBM = 128, kBN = 128;
+constexpr int kWThreads = 320;
+constexpr uint64_t kWaitNs = 2000000000ull;
+
+// Shared memory in 32 KB tiles: Q's operands, then the stages of K and of V; the
+// barriers and the block's lists (16 bytes a request) after them.  128 rows leave
+// room for a third stage while the lists are short.
+constexpr int kMaxStages = 3;
+constexpr int kSmemMax = 232448;
+enum {
+  bQ = 0,
+  bQFree = 1,
+  bK = 2,                     // [stages]
+  bKFree = bK + kMaxStages,   // [stages]
+  bV = bKFree + kMaxStages,   // [stages]
+  bVFree = bV + kMaxStages,   // [stages]
+  bS = bVFree + kMaxStages,   // [2 S buffers]
+  bP = bS + 2,                // [2], 4 warps
+  bOFree = bP + 2,            // [2], 4 warps
+  bO = bOFree + 2,
+  bDrain = bO + 1,
+  kBars = bDrain + 1
+};
+struct Misc {
+  uint32_t tmem;
+  int abort, stop;
+  long long part[32];
+};
+constexpr size_t wide_smem(int halves, int stages, int R) {
+  return (size_t)(halves + 2 * stages) * 32768 + 256 + sizeof(Misc) + (size_t)(R + 1) * 16 + 1024;
+}
+
+struct WideMaps {
+  CUtensorMap q, k, v;
+};
+
+template <int kHalves>
+__global__ void __launch_bounds__(kWThreads, 1)
+draft_part_wide(const __grid_constant__ WideMaps maps, const DraftParams p, int mtok, int box_rows,
+                int stages) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  const uint32_t sb = smem_u32(smem);
+  const int s_k = kHalves * 32768, s_v = s_k + stages * 32768, s_bar = s_v + stages * 32768;
+  Misc &ms = *reinterpret_cast<Misc *>(smem + s_bar + 256);
+  volatile int *abort_flag = &ms.abort;
+  long long *unit0 = reinterpret_cast<long long *>(&ms + 1), *item0 = unit0 + (p.x.R + 1);
+  const flide_tree_index &x = p.x;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  auto bar = [&](int i) -> uint32_t { return sb + s_bar + 8 * i; };
+  asm volatile("griddepcontrol.launch_dependents;");
+  // the status word may change while the grid runs: one thread's reading counts
+  if (tid == 0) {
+    for (int i = 0; i < kBars; ++i)
+      mbar_init(bar(i), (i >= bP && i < bP + 2) || (i >= bOFree && i < bOFree + 2) ? 4u : 1u);
+    fence_mbar_init();
+    ms.abort = 0;
+    ms.stop = failed(x.status);
+  }
+  __syncthreads();
+  if (ms.stop) return;
+  draft_lists(p, unit0, item0, ms.part);
+  const long long U = unit0[x.R];
+  const int w = blockIdx.x, W = workers_of(U, p.workers);
+  if (w >= W) return;
+  if (warp == 9) {
+    tmem_alloc(sb + s_bar + 256 + (uint32_t)offsetof(Misc, tmem), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ms.tmem;
+  long long u = worker_start(U, W, w);
+  const long long u_end = worker_start(U, W, w + 1);
+  // step i of a run: S buffer i & 1, key tile i (128 rows) or i / 2 (256 rows)
+  auto tile_of = [](int i) { return kHalves == 2 ? i >> 1 : i; };
+  // first and last step that a key tile is used by
+  auto opens = [](int i) { return kHalves == 1 || !(i & 1); };
+  auto closes = [](int i) { return kHalves == 1 || (i & 1); };
+
+  if (warp == 8) {
+    // -------------------------------------------------------------- producer
+    if (lane == 0) {
+      prefetch_tmap(&maps.q);
+      prefetch_tmap(&maps.k);
+      prefetch_tmap(&maps.v);
+    }
+    const int boxes = kBN / box_rows;
+    auto wait = [&](int b, uint32_t parity) {
+      return __all_sync(0xffffffffu, mbar_wait(bar(b), parity, abort_flag, kWaitNs));
+    };
+    bool ok = true;
+    int rc = 0, kt = 0;  // runs, key tiles so far
+    for (; u < u_end && ok; ++rc) {
+      Run run;
+      u += draft_run(p, unit0, item0, u, u_end, w, run);
+      if (rc > 0 && !(ok = wait(bQFree, (rc - 1) & 1))) break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(bar(bQ), kHalves * 32768);
+        for (int h = 0; h < kHalves; ++h)
+          for (int s = 0; s < 2; ++s)
+            tma_load_3d(sb + h * 32768 + s * 16384, &maps.q, bar(bQ), 64 * s, run.hk * p.G,
+                        run.t0 + (run.tile * kHalves + h) * mtok);
+      }
+      for (int k0 = run.k0; k0 < run.k1; k0 += kBN, ++kt) {
+        const int st = kt % stages;
+        const uint32_t turn = (uint32_t)(kt / stages - 1) & 1;
+        // boxes that hold history rows (a lane each); the rest of the tile keeps
+        // what the stage held, and is masked
+        const int used = min(boxes, (run.k1 - k0 + box_rows - 1) / box_rows);
+        long long row = 0;
+        if (lane < used) {
+          row = history_row(x, p.hist, run.base, k0 + lane * box_rows);
+          if (row < 0) row = 0;  // no block: read row 0, the call is flagged
+        }
+        if (kt >= stages && !(ok = wait(bKFree + st, turn))) break;
+        if (lane == 0) mbar_arrive_expect_tx(bar(bK + st), used * box_rows * 256);
+        __syncwarp();
+        if (lane < used)
+          for (int s = 0; s < 2; ++s)
+            tma_load_3d(sb + s_k + st * 32768 + s * 16384 + lane * box_rows * 128, &maps.k, bar(bK + st),
+                        64 * s, run.hk, (int)row);
+        if (kt >= stages && !(ok = wait(bVFree + st, turn))) {
+          // K of this tile is in flight, V is not
+          mbar_wait(bar(bK + st), (kt / stages) & 1, abort_flag, kWaitNs, false);
+          break;
+        }
+        if (lane == 0) mbar_arrive_expect_tx(bar(bV + st), used * box_rows * 256);
+        __syncwarp();
+        if (lane < used)
+          for (int s = 0; s < 2; ++s)
+            tma_load_3d(sb + s_v + st * 32768 + s * 16384 + lane * box_rows * 128, &maps.v, bar(bV + st),
+                        64 * s, run.hk, (int)row);
+      }
+    }
+    // no copy may be in flight when the block ends
+    if (rc > 0) mbar_wait(bar(bQ), (rc - 1) & 1, abort_flag, kWaitNs, false);
+    for (int t = max(0, kt - stages); t < kt; ++t) {
+      mbar_wait(bar(bK + t % stages), (t / stages) & 1, abort_flag, kWaitNs, false);
+      mbar_wait(bar(bV + t % stages), (t / stages) & 1, abort_flag, kWaitNs, false);
+    }
+  } else if (warp == 9) {
+    // -------------------------------------------------------------- MMA
+    if (lane == 0) {
+      constexpr uint32_t id_s = idesc_bf16(kBM, kBN, false), id_pv = idesc_bf16(kBM, 128, true);
+      auto wait = [&](int b, uint32_t parity) { return mbar_wait(bar(b), parity, abort_flag, kWaitNs); };
+      bool ok = true;
+      int rc = 0, kt0 = 0;
+      uint32_t np[2] = {0, 0};  // weights taken per S buffer
+      for (; u < u_end && ok; ++rc) {
+        Run run;
+        u += draft_run(p, unit0, item0, u, u_end, w, run);
+        const int tiles = (run.k1 - run.k0 + kBN - 1) / kBN, steps = tiles * kHalves;
+        // S of step i, from its key tile's stage
+        auto scores = [&](int i) -> bool {
+          const int t = kt0 + tile_of(i), st = t % stages, h = i & 1;
+          if (opens(i) && !wait(bK + st, (t / stages) & 1)) return false;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) {
+            const uint32_t o = (kk >> 2) * 16384 + (kk & 3) * 32;
+            mma_bf16(tmem + h * 256, sdesc_sw128(sb + (kHalves == 2 ? h : 0) * 32768 + o, 16, 1024),
+                     sdesc_sw128(sb + s_k + st * 32768 + o, 16, 1024), id_s, kk > 0 ? 1u : 0u);
+          }
+          mma_commit(bar(bS + h));
+          if (closes(i)) mma_commit(bar(bKFree + st));
+          return true;
+        };
+        if (!(ok = wait(bQ, rc & 1))) break;
+        for (int i = 0; i < min(2, steps) && ok; ++i) ok = scores(i);
+        for (int i = 0; i < steps && ok; ++i) {
+          const int t = kt0 + tile_of(i), st = t % stages, h = i & 1;
+          ok = wait(bP + h, np[h]++ & 1) && (!opens(i) || wait(bV + st, (t / stages) & 1)) &&
+               (i >= 2 || rc == 0 || wait(bOFree + h, (rc - 1) & 1));
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            mma_bf16_ts(tmem + h * 256 + 128, tmem + h * 256 + kk * 8,
+                        sdesc_sw128(sb + s_v + st * 32768 + kk * 2048, 16384, 1024), id_pv,
+                        (i >= 2 || kk > 0) ? 1u : 0u);
+          if (closes(i)) mma_commit(bar(bVFree + st));
+          if (i + 2 < steps) ok = scores(i + 2);
+        }
+        if (!ok) break;
+        // the second half had no step: its phase is waited for all the same
+        if (steps == 1 && rc > 0 && !(ok = wait(bOFree + 1, (rc - 1) & 1))) break;
+        mma_commit(bar(bQFree));
+        mma_commit(bar(bO));
+        kt0 += tiles;
+      }
+      // every MMA issued here is complete before TMEM is freed
+      mma_commit(bar(bDrain));
+      mbar_wait(bar(bDrain), 0, abort_flag, kWaitNs, false);
+    }
+  } else {
+    // -------------------------------------------------------------- softmax
+    const int h = warp >> 2, row = (warp & 3) * 32 + lane;  // S buffer; its row = TMEM lane
+    const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t t_s = tl + h * 256, t_o = tl + h * 256 + 128;
+    const float c = p.scale * kLog2eD;
+    auto wait = [&](int b, uint32_t parity) {
+      return __all_sync(0xffffffffu, mbar_wait(bar(b), parity, abort_flag, kWaitNs));
+    };
+    bool ok = true;
+    uint32_t ns = 0;  // score tiles taken
+    int rc = 0, kt0 = 0;
+    for (; u < u_end && ok; ++rc) {
+      Run run;
+      u += draft_run(p, unit0, item0, u, u_end, w, run);
+      const int tiles = (run.k1 - run.k0 + kBN - 1) / kBN, steps = tiles * kHalves;
+      float m = -INFINITY, l = 0.f;
+      for (int i = h; i < steps; i += 2) {
+        const int kt = tile_of(i), left = run.k1 - run.k0 - kt * kBN;
+        if (!(ok = wait(bS + h, ns++ & 1))) break;
+        tc_fence_after();
+        uint32_t sr[128];
+        tmem_ld128(t_s, sr);
+        if (left < kBN) {
+#pragma unroll
+          for (int j = 0; j < kBN; ++j)
+            if (j >= left) sr[j] = 0xff800000u;  // -inf
+          if (opens(i)) {
+            // V rows behind the history: zero, whatever was there
+            const int st = (kt0 + kt) % stages;
+            if (!(ok = wait(bV + st, ((kt0 + kt) / stages) & 1))) break;
+            for (int e = left * 8 + (tid & 127); e < kBN * 8; e += 128) {
+              uint4 *z = reinterpret_cast<uint4 *>(smem + s_v + st * 32768) + e;
+              z[0] = make_uint4(0u, 0u, 0u, 0u);
+              z[1024] = make_uint4(0u, 0u, 0u, 0u);  // the upper 64 elements
+            }
+            fence_proxy_async_smem();
+          }
+        }
+        // row max: 8 chains of three-input max
+        float mx[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) mx[k] = __uint_as_float(sr[k]);
+#pragma unroll
+        for (int j = 8; j < kBN; j += 16) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            mx[k] = fmax3f(mx[k], __uint_as_float(sr[j + 2 * k < kBN ? j + 2 * k : 0]),
+                           __uint_as_float(sr[j + 2 * k + 1 < kBN ? j + 2 * k + 1 : 0]));
+        }
+        const float mt = c * fmaxf(fmax3f(mx[0], mx[1], mx[2]), fmax3f(fmax3f(mx[3], mx[4], mx[5]), mx[6], mx[7]));
+        if (i < 2) {
+          m = mt;
+        } else if (__any_sync(0xffffffffu, mt > m + 8.f)) {
+          // this buffer's last PV is complete: it was issued before this S
+          const float mn = fmaxf(m, mt), f = mn == -INFINITY ? 1.f : exp2f(m - mn);
+#pragma unroll 1
+          for (int c4 = 0; c4 < 4; ++c4) {
+            uint32_t r32[32];
+            tmem_ld32(t_o + 32 * c4, r32);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) r32[j] = __float_as_uint(__uint_as_float(r32[j]) * f);
+            tmem_st32(t_o + 32 * c4, r32);
+          }
+          l *= f;
+          m = mn;
+        }
+        const float ref = m == -INFINITY ? 0.f : m;
+        const uint64_t c2 = f2_pack(c, c), nm2 = f2_pack(-ref, -ref);
+        uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+        for (int j = 0; j < kBN; j += 2) {
+          float x0, x1;
+          f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[j]), __uint_as_float(sr[j + 1])), c2, nm2), x0, x1);
+          const float e0 = ex2_approx(x0), e1 = ex2_approx(x1);
+          acc[(j >> 1) & 3] = f2_add(acc[(j >> 1) & 3], f2_pack(e0, e1));
+          sr[j >> 1] = pack_bf16x2(e0, e1);
+        }
+        {
+          float a0, a1, b0, b1;
+          f2_unpack(f2_add(acc[0], acc[1]), a0, a1);
+          f2_unpack(f2_add(acc[2], acc[3]), b0, b1);
+          l += (a0 + a1) + (b0 + b1);
+        }
+        tmem_st64(t_s, *reinterpret_cast<uint32_t(*)[64]>(sr));
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(bP + h));
+      }
+      if (!ok || !(ok = wait(bO, rc & 1))) break;
+      tc_fence_after();
+      const size_t at = (size_t)run.slot * 256 + h * 128 + row;
+      if (h < steps) {
+        float *o = p.part_o + at * 128;
+#pragma unroll 1
+        for (int c4 = 0; c4 < 4; ++c4) {
+          uint32_t r32[32];
+          tmem_ld32(t_o + 32 * c4, r32);
+#pragma unroll
+          for (int j = 0; j < 32; j += 4)
+            *reinterpret_cast<uint4 *>(o + 32 * c4 + j) = make_uint4(r32[j], r32[j + 1], r32[j + 2], r32[j + 3]);
+        }
+      }
+      *reinterpret_cast<float2 *>(p.part_ml + 2 * at) = make_float2(m, l);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(bOFree + h));
+      kt0 += tiles;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (ms.abort && tid == 0) set_status(x.status, FLIDE_ERR_TIMEOUT);
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                              const cuuint64_t *, const cuuint32_t *, const cuuint32_t *,
+                              CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
+                              CUtensorMapFloatOOBfill);
+
+EncodeFn encode_tiled() {
+  static std::atomic<EncodeFn> cached{nullptr};  // host threads may race on a first call
+  EncodeFn fn = cached.load(std::memory_order_acquire);
+  if (!fn) {
+    void *ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess) {
+      fn = (EncodeFn)ptr;
+      cached.store(fn, std::memory_order_release);
+    }
+  }
+  return fn;
+}
+
+// [rows, heads, 128] bf16 as (element, head, row); box of 64 elements (128
+// swizzled bytes) x box_heads x box_rows
+bool wide_map(CUtensorMap *m, const void *base, int heads, long rows, int box_heads, int box_rows) {
+  EncodeFn enc = encode_tiled();
+  if (!enc || rows <= 0) return false;
+  const cuuint64_t dims[3] = {128, (cuuint64_t)heads, (cuuint64_t)rows};
+  const cuuint64_t strides[2] = {256, (cuuint64_t)heads * 256};
+  const cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_rows}, step[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, step,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int kHalves>
+int wide_launch(const DraftParams &p, const WideMaps &maps, int mtok, int box_rows, cudaStream_t s) {
+  int stages = kHalves == 2 ? 2 : kMaxStages;
+  while (wide_smem(kHalves, stages, p.x.R) > kSmemMax) --stages;
+  if (stages < 2) return FLIDE_ERR_CAPACITY;
+  const size_t smem = wide_smem(kHalves, stages, p.x.R);
+  if (cudaFuncSetAttribute(draft_part_wide<kHalves>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)smem) != cudaSuccess)
+    return FLIDE_ERR_CUDA;
+  draft_part_wide<kHalves><<<p.workers, kWThreads, smem, s>>>(maps, p, mtok, box_rows, stages);
+  FLIDE_LAUNCH_CHECK();
+  return FLIDE_OK;
+}
+
+}  // namespace
+
+int draft_wide_launch(const DraftParams &p0, int past_rows, cudaStream_t s) {
+  DraftParams p = p0;
+  p.unit = kBN;
+  const int mtok = kBM / p.G;
+  // rows of a box: a tile's, or the most that divides both it and a block
+  int box_rows = kBN;
+  if (p.hist.block_table)
+    while (p.hist.block_rows % box_rows) box_rows /= 2;
+  WideMaps maps;
+  const bool past = p.past_k != nullptr && past_rows > 0;  // without: no unit, no load
+  if (!wide_map(&maps.q, p.q, p.Hq, p.x.T, p.G, mtok) ||
+      !wide_map(&maps.k, past ? p.past_k : p.k, p.Hkv, past ? past_rows : p.x.T, 1, box_rows) ||
+      !wide_map(&maps.v, past ? p.past_v : p.v, p.Hkv, past ? past_rows : p.x.T, 1, box_rows))
+    return FLIDE_ERR_CUDA;
+  return p.halves ? wide_launch<1>(p, maps, mtok, box_rows, s) : wide_launch<2>(p, maps, mtok, box_rows, s);
+}
+
+}  // namespace flide
