@@ -45,7 +45,12 @@ __device__ __forceinline__ int workers_of(long long U, int W) { return (int)min(
 __device__ __forceinline__ long long worker_start(long long U, int W, int w) { return w * U / W; }
 // the worker whose units contain u
 __device__ __forceinline__ int worker_of(long long U, int W, long long u) {
-  return (int)(((u + 1) * W - 1) / U);
+  // a 64-bit quotient by way of a double's, put right by one where that rounded
+  const long long num = (u + 1) * W - 1;
+  int w = (int)((double)num / (double)U);
+  if ((long long)w * U > num) --w;
+  else if ((long long)(w + 1) * U <= num) ++w;
+  return w;
 }
 
 // A worker's run: history rows [k0, k1) of one item (row tile `tile`, kv head

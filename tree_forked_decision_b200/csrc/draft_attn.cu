@@ -532,23 +532,25 @@ __global__ void __launch_bounds__(256) draft_join_portable(const DraftParams p) 
   if (p.lse && lane == 0) p.lse[(size_t)t * p.Hq + h] = (m + log2f(l)) * kLn2D;
 }
 
-// D elements of type T as they lie for an 8-lane group: a lane's are kE / kW words
-// of kW, word i at element (8 i + lane) kW, so that a group reads whole rows.
+// D elements of type T as they lie for an 8-lane group: a lane's are kWords words
+// of 16 bytes, word i at byte (8 i + lane) 16, so that a group reads whole rows.
 template <typename T, int D>
 struct Row8 {
   static constexpr int kE = D / 8;
-  static __device__ __forceinline__ void load(const T *p, int l, float (&v)[kE]) {
-    constexpr int kW = sizeof(T) == 1 ? 16 : sizeof(T) == 2 ? 8 : 4;
+  static constexpr int kW = 16 / sizeof(T);
+  static constexpr int kWords = kE / kW;
+  static __device__ __forceinline__ void load(const T *p, int l, uint4 (&w)[kWords]) {
 #pragma unroll
-    for (int i = 0; i < kE / kW; ++i) {
-      const uint4 w = *reinterpret_cast<const uint4 *>(p + (8 * i + l) * kW);
+    for (int i = 0; i < kWords; ++i) w[i] = *reinterpret_cast<const uint4 *>(p + (8 * i + l) * kW);
+  }
+  static __device__ __forceinline__ void unpack(const uint4 (&w)[kWords], float (&v)[kE]) {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const uint32_t u = word_of(w, j);
+        const uint32_t u = word_of(w[i], j);
         float *o = v + i * kW + j * (kW / 4);
-        if constexpr (sizeof(T) == 4) {
-          o[0] = __uint_as_float(u);
-        } else if constexpr (sizeof(T) == 2) {
+        if constexpr (sizeof(T) == 2) {
           o[0] = __uint_as_float(u << 16);
           o[1] = __uint_as_float(u & 0xffff0000u);
         } else {
@@ -561,42 +563,47 @@ struct Row8 {
           }
         }
       }
-    }
   }
   // element of v[e]
-  static __device__ __forceinline__ int at(int e, int l) {
-    constexpr int kW = sizeof(T) == 1 ? 16 : sizeof(T) == 2 ? 8 : 4;
-    return (8 * (e / kW) + l) * kW + e % kW;
-  }
+  static __device__ __forceinline__ int at(int e, int l) { return (8 * (e / kW) + l) * kW + e % kW; }
 };
 
 // bf16 and e4m3, d of 64 or 128: one warp per (token, query head) as four groups
 // of eight lanes, each with its own running (max, sum, O) over every fourth key
-// of the token's path and every fourth partial of its history, so that four
-// rows are on their way at a time; joined by shuffles at the end.  The path is
-// found by all lanes at once (a lane per ancestor).  Runs beside the part kernel
-// (programmatic launch) up to where it needs its results.
+// of the token's path and every fourth partial of its history; joined by shuffles
+// at the end.  Bound by latency: five dependent loads stand before the path's
+// first product and two before the first partial, so rows are kept apart (a warp
+// for all heads of a group took 5 us a head) and few registers let 32 warps share
+// an SM.  Starts beside the part kernel (programmatic launch) and waits for its
+// results only where it needs them.
+constexpr int kJoinWarps = 8;
+constexpr int kPath = 64;  // keys of a path listed at a time
+
 template <typename T, int D>
-__global__ void __launch_bounds__(256) draft_join_kernel(const DraftParams p) {
+__global__ void __launch_bounds__(kJoinWarps * 32, 4) draft_join_kernel(const DraftParams p) {
   using Row = Row8<T, D>;
   constexpr int kE = Row::kE;
+  __shared__ int path_rows[kJoinWarps][kPath];
   const flide_tree_index &x = p.x;
   const int lane = threadIdx.x & 31, grp = lane >> 3, l8 = lane & 7;
+  int *path = path_rows[threadIdx.x >> 5];
   const long long job = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-  const int t = (int)(job / p.Hq), h = (int)(job % p.Hq), hk = h / p.G;
+  const int t = (int)(job / p.Hq), h = (int)(job - (long long)t * p.Hq), hk = h / p.G;
+  const size_t head = (size_t)t * p.Hq + h;
   const bool live = !failed(x.status) && t < x.counts[FLIDE_CNT_T];
   float m = -INFINITY, l = 0.f, acc[kE];
 #pragma unroll
   for (int e = 0; e < kE; ++e) acc[e] = 0.f;
   int r = 0;
   if (live) {
-    const T *Q = static_cast<const T *>(p.q), *K = static_cast<const T *>(p.k), *Vs = static_cast<const T *>(p.v);
+    const T *K = static_cast<const T *>(p.k), *Vs = static_cast<const T *>(p.v);
     const float qk_scale = p.scale * kLog2eD * (p.descale ? p.descale[0] * p.descale[1] : 1.f);
-    float qv[kE];
-    Row::load(Q + ((size_t)t * p.Hq + h) * D, l8, qv);
+    uint4 qw[Row::kWords];
+    Row::load(static_cast<const T *>(p.q) + head * D, l8, qw);
     const int n = (int)checked(x.status, x.counts, x.token_node[t], x.counts[FLIDE_CNT_N], 801);
     r = x.node_req[n];
-    for (int a0 = x.anc_ptr[n], a1 = x.anc_ptr[n + 1]; a0 < a1; a0 += 32) {
+    const int a1 = x.anc_ptr[n + 1];
+    for (int a0 = x.anc_ptr[n]; a0 < a1; a0 += 32) {
       int first = 0, len = 0;  // this lane's ancestor: its keys
       if (a0 + lane < a1) {
         const int node = x.anc_node[a0 + lane];
@@ -604,69 +611,81 @@ __global__ void __launch_bounds__(256) draft_join_kernel(const DraftParams p) {
         len = (node == n ? t + 1 : x.node_start[node + 1]) - first;
       }
       const int end = warp_incl_scan(len), total = __shfl_sync(0xffffffffu, end, 31);
-      const int na = min(32, a1 - a0);
-      for (int k0 = 0; k0 < total; k0 += 4) {
-        const int k = k0 + grp;
-        int j = 0;
-        for (int a = 0; a < na; ++a) {
-          const int e = __shfl_sync(0xffffffffu, end, a), f = __shfl_sync(0xffffffffu, first, a);
-          const int b = __shfl_sync(0xffffffffu, len, a);
-          if (k >= e - b && k < e) j = f + k - (e - b);
-        }
-        const bool on = k < total;
-        float kv[kE], vv[kE];
-        if (on) {
-          Row::load(K + ((size_t)j * p.Hkv + hk) * D, l8, kv);
-          Row::load(Vs + ((size_t)j * p.Hkv + hk) * D, l8, vv);
-        }
-        float s = 0.f;
-        if (on) {
+      for (int b0 = 0; b0 < total; b0 += kPath) {
+        __syncwarp();
+        for (int i = max(b0, end - len); i < min(b0 + kPath, end); ++i) path[i - b0] = first + i - (end - len);
+        __syncwarp();
+        const int cnt = min(kPath, total - b0);
+        for (int k0 = 0; k0 < cnt; k0 += 4) {
+          const bool on = k0 + grp < cnt;
+          const size_t at = ((size_t)path[on ? k0 + grp : 0] * p.Hkv + hk) * D;
+          uint4 kw[Row::kWords], vw[Row::kWords];
+          Row::load(K + at, l8, kw);
+          Row::load(Vs + at, l8, vw);
+          float f[kE], s = 0.f;
+          {
+            float qv[kE];
+            Row::unpack(qw, qv);
+            Row::unpack(kw, f);
 #pragma unroll
-          for (int e = 0; e < kE; ++e) s = fmaf(qv[e], kv[e], s);
-        }
-        s += __shfl_xor_sync(0xffffffffu, s, 1);
-        s += __shfl_xor_sync(0xffffffffu, s, 2);
-        s += __shfl_xor_sync(0xffffffffu, s, 4);
-        if (on) {
+            for (int e = 0; e < kE; ++e) s = fmaf(qv[e], f[e], s);
+          }
+          s += __shfl_xor_sync(0xffffffffu, s, 1);
+          s += __shfl_xor_sync(0xffffffffu, s, 2);
+          s += __shfl_xor_sync(0xffffffffu, s, 4);
+          if (!on) continue;
           s *= qk_scale;
           const float mn = fmaxf(m, s), ref = mn == -INFINITY ? 0.f : mn;
-          const float f = ex2_approx(m - ref), w = ex2_approx(s - ref);
-          l = l * f + w;
+          const float o = ex2_approx(m - ref), w = ex2_approx(s - ref);
+          l = l * o + w;
           m = mn;
+          Row::unpack(vw, f);
 #pragma unroll
-          for (int e = 0; e < kE; ++e) acc[e] = fmaf(w, vv[e], acc[e] * f);
+          for (int e = 0; e < kE; ++e) acc[e] = fmaf(w, f[e], acc[e] * o);
         }
       }
     }
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the part kernel's results
   if (!live || failed(x.status)) return;
-  const long long U = p.unit0[x.R], ua = p.unit0[r], ia = p.item0[r];
-  const long long items = p.item0[r + 1] - ia;
-  const long long per = items > 0 ? (p.unit0[r + 1] - ua) / items : 0;  // units of one item
-  if (per > 0) {
-    const int row = (t - x.node_start[x.req_node[r]]) * p.G + h % p.G;
-    const long long li = (long long)(row / p.tile_rows) * p.Hkv + hk;
-    const long long u0 = ua + li * per;
+  const long long U = p.unit0[x.R], ua = p.unit0[r], ub = p.unit0[r + 1], ia = p.item0[r];
+  if (ub > ua) {
+    const long long per = (ub - ua) / (p.item0[r + 1] - ia);  // units of one item
+    const int row = (t - x.node_start[x.req_node[r]]) * p.G + h - hk * p.G;
+    const int tile = row / p.tile_rows;
+    const long long li = (long long)tile * p.Hkv + hk, u0 = ua + li * per;
     const int W = workers_of(U, p.workers);
     const int w0 = worker_of(U, W, u0), w1 = worker_of(U, W, u0 + per - 1);
     const int parts = (w1 - w0 + 1) << p.halves;
-    for (int i = grp; i < parts; i += 4) {
-      const size_t pr = (size_t)(w0 + (i >> p.halves) + ia + li) * p.slot_rows + row % p.tile_rows +
-                        ((i & p.halves) ? p.slot_rows / 2 : 0);
-      const float2 ml = *reinterpret_cast<const float2 *>(p.part_ml + 2 * pr);
-      float v[kE];
+    const size_t pr0 = (size_t)(w0 + ia + li) * p.slot_rows + row - tile * p.tile_rows;
+    auto partial = [&](int i, float2 &ml, float4 (&v)[kE / 4]) {
+      const size_t pr = pr0 + (size_t)(i >> p.halves) * p.slot_rows + ((i & p.halves) ? p.slot_rows / 2 : 0);
+      ml = *reinterpret_cast<const float2 *>(p.part_ml + 2 * pr);
 #pragma unroll
-      for (int e = 0; e < kE; e += 4)
-        *reinterpret_cast<float4 *>(v + e) =
-            *reinterpret_cast<const float4 *>(p.part_o + pr * D + Row::at(e, l8));
-      if (ml.x == -INFINITY) continue;  // an empty partial
-      const float mn = fmaxf(m, ml.x);
-      const float f = ex2_approx(m - mn), g = ex2_approx(ml.x - mn);
-      l = l * f + ml.y * g;
+      for (int e = 0; e < kE / 4; ++e)
+        v[e] = *reinterpret_cast<const float4 *>(p.part_o + pr * D + Row::at(4 * e, l8));
+    };
+    float2 ml;
+    float4 v[kE / 4];
+    if (grp < parts) partial(grp, ml, v);
+    for (int i = grp; i < parts; i += 4) {
+      const float2 ml0 = ml;
+      float4 v0[kE / 4];
+#pragma unroll
+      for (int e = 0; e < kE / 4; ++e) v0[e] = v[e];
+      if (i + 4 < parts) partial(i + 4, ml, v);
+      if (ml0.x == -INFINITY) continue;  // an empty partial
+      const float mn = fmaxf(m, ml0.x);
+      const float f = ex2_approx(m - mn), g = ex2_approx(ml0.x - mn);
+      l = l * f + ml0.y * g;
       m = mn;
 #pragma unroll
-      for (int e = 0; e < kE; ++e) acc[e] = fmaf(g, v[e], acc[e] * f);
+      for (int e = 0; e < kE / 4; ++e) {
+        acc[4 * e] = fmaf(g, v0[e].x, acc[4 * e] * f);
+        acc[4 * e + 1] = fmaf(g, v0[e].y, acc[4 * e + 1] * f);
+        acc[4 * e + 2] = fmaf(g, v0[e].z, acc[4 * e + 2] * f);
+        acc[4 * e + 3] = fmaf(g, v0[e].w, acc[4 * e + 3] * f);
+      }
     }
   }
   // the four groups' results
@@ -684,14 +703,14 @@ __global__ void __launch_bounds__(256) draft_join_kernel(const DraftParams p) {
     acc[e] += __shfl_xor_sync(0xffffffffu, acc[e], 16);
     acc[e] *= inv;
   }
-  // a group stores a quarter of its lanes' elements
-  __nv_bfloat16 *O = static_cast<__nv_bfloat16 *>(p.out) + ((size_t)t * p.Hq + h) * D;
+  // a group stores a quarter of its lanes' elements (64: the first two groups a half)
+  __nv_bfloat16 *O = static_cast<__nv_bfloat16 *>(p.out) + head * D;
 #pragma unroll
   for (int e = 0; e < kE; e += 4)
-    if (e / 4 % 4 == grp || (kE < 16 && e / 4 == grp))
+    if (e / 4 == grp)
       *reinterpret_cast<uint2 *>(O + Row::at(e, l8)) =
           make_uint2(pack_bf16x2(acc[e], acc[e + 1]), pack_bf16x2(acc[e + 2], acc[e + 3]));
-  if (p.lse && lane == 0) p.lse[(size_t)t * p.Hq + h] = (mt + log2f(l)) * kLn2D;
+  if (p.lse && lane == 0) p.lse[head] = (mt + log2f(l)) * kLn2D;
 }
 
 // ---- host ----------------------------------------------------------------------
@@ -786,8 +805,8 @@ int join_launch(const DraftParams &p, cudaStream_t s) {
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((warps + 7) / 8));
-  cfg.blockDim = dim3(256);
+  cfg.gridDim = dim3((unsigned)((warps + kJoinWarps - 1) / kJoinWarps));
+  cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.stream = s;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
