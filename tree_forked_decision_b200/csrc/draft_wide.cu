@@ -63,6 +63,19 @@ constexpr size_t wide_smem(int halves, int stages, int R) {
   return (size_t)(halves + 2 * stages) * 32768 + 256 + sizeof(Misc) + (size_t)(R + 1) * 16 + 1024;
 }
 
+// A key tile's stage and how often the ring has been round (its parity is that of
+// the stage's barriers); a division per tile would stand between two products.
+struct Ring {
+  int st = 0;
+  uint32_t turn = 0;
+  __device__ __forceinline__ void next(int stages) {
+    if (++st == stages) {
+      st = 0;
+      turn ^= 1;
+    }
+  }
+};
+
 struct WideMaps {
   CUtensorMap q, k, v;
 };
@@ -108,9 +121,8 @@ draft_part_wide(const __grid_constant__ WideMaps maps, const DraftParams p, int 
   const long long u_end = worker_start(U, W, w + 1);
   // step i of a run: S buffer i & 1, key tile i (128 rows) or i / 2 (256 rows)
   auto tile_of = [](int i) { return kHalves == 2 ? i >> 1 : i; };
-  // first and last step that a key tile is used by
+  // first step that a key tile is used by
   auto opens = [](int i) { return kHalves == 1 || !(i & 1); };
-  auto closes = [](int i) { return kHalves == 1 || (i & 1); };
 
   if (warp == 8) {
     // -------------------------------------------------------------- producer
@@ -125,6 +137,7 @@ draft_part_wide(const __grid_constant__ WideMaps maps, const DraftParams p, int 
     };
     bool ok = true;
     int rc = 0, kt = 0;  // runs, key tiles so far
+    Ring ring;
     for (; u < u_end && ok; ++rc) {
       Run run;
       u += draft_run(p, unit0, item0, u, u_end, w, run);
@@ -136,17 +149,20 @@ draft_part_wide(const __grid_constant__ WideMaps maps, const DraftParams p, int 
             tma_load_3d(sb + h * 32768 + s * 16384, &maps.q, bar(bQ), 64 * s, run.hk * p.G,
                         run.t0 + (run.tile * kHalves + h) * mtok);
       }
+      // boxes that hold history rows, a lane each (the rest of the last tile keeps
+      // what the stage held, and is masked); looked up a tile ahead
+      auto row_at = [&](int k0) -> long long {
+        const int k = k0 + lane * box_rows;
+        if (lane >= boxes || k >= run.k1) return -1;
+        return max(history_row(x, p.hist, run.base, k), 0ll);  // no block: row 0, the call is flagged
+      };
+      long long next = row_at(run.k0);
       for (int k0 = run.k0; k0 < run.k1; k0 += kBN, ++kt) {
-        const int st = kt % stages;
-        const uint32_t turn = (uint32_t)(kt / stages - 1) & 1;
-        // boxes that hold history rows (a lane each); the rest of the tile keeps
-        // what the stage held, and is masked
+        const int st = ring.st;
+        const uint32_t turn = ring.turn ^ 1;  // the stage's last use
         const int used = min(boxes, (run.k1 - k0 + box_rows - 1) / box_rows);
-        long long row = 0;
-        if (lane < used) {
-          row = history_row(x, p.hist, run.base, k0 + lane * box_rows);
-          if (row < 0) row = 0;  // no block: read row 0, the call is flagged
-        }
+        const long long row = next;
+        next = row_at(k0 + kBN);
         if (kt >= stages && !(ok = wait(bKFree + st, turn))) break;
         if (lane == 0) mbar_arrive_expect_tx(bar(bK + st), used * box_rows * 256);
         __syncwarp();
@@ -156,7 +172,7 @@ draft_part_wide(const __grid_constant__ WideMaps maps, const DraftParams p, int 
                         64 * s, run.hk, (int)row);
         if (kt >= stages && !(ok = wait(bVFree + st, turn))) {
           // K of this tile is in flight, V is not
-          mbar_wait(bar(bK + st), (kt / stages) & 1, abort_flag, kWaitNs, false);
+          mbar_wait(bar(bK + st), ring.turn, abort_flag, kWaitNs, false);
           break;
         }
         if (lane == 0) mbar_arrive_expect_tx(bar(bV + st), used * box_rows * 256);
@@ -165,6 +181,7 @@ draft_part_wide(const __grid_constant__ WideMaps maps, const DraftParams p, int 
           for (int s = 0; s < 2; ++s)
             tma_load_3d(sb + s_v + st * 32768 + s * 16384 + lane * box_rows * 128, &maps.v, bar(bV + st),
                         64 * s, run.hk, (int)row);
+        ring.next(stages);
       }
     }
     // no copy may be in flight when the block ends
@@ -179,49 +196,60 @@ draft_part_wide(const __grid_constant__ WideMaps maps, const DraftParams p, int 
       constexpr uint32_t id_s = idesc_bf16(kBM, kBN, false), id_pv = idesc_bf16(kBM, 128, true);
       auto wait = [&](int b, uint32_t parity) { return mbar_wait(bar(b), parity, abort_flag, kWaitNs); };
       bool ok = true;
-      int rc = 0, kt0 = 0;
-      uint32_t np[2] = {0, 0};  // weights taken per S buffer
+      int rc = 0;
+      uint32_t np[2] = {0, 0};  // weights taken per S buffer, mod 2
+      Ring rs, rv;              // key tiles of the scores and of the products with V
       for (; u < u_end && ok; ++rc) {
         Run run;
         u += draft_run(p, unit0, item0, u, u_end, w, run);
-        const int tiles = (run.k1 - run.k0 + kBN - 1) / kBN, steps = tiles * kHalves;
-        // S of step i, from its key tile's stage
-        auto scores = [&](int i) -> bool {
-          const int t = kt0 + tile_of(i), st = t % stages, h = i & 1;
-          if (opens(i) && !wait(bK + st, (t / stages) & 1)) return false;
+        const int steps = (run.k1 - run.k0 + kBN - 1) / kBN * kHalves;
+        // S of the next step, in S buffer h
+        auto scores = [&](int h) -> bool {
+          if ((kHalves == 1 || h == 0) && !wait(bK + rs.st, rs.turn)) return false;
           tc_fence_after();
+          const uint32_t k_at = sb + s_k + rs.st * 32768;
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk) {
             const uint32_t o = (kk >> 2) * 16384 + (kk & 3) * 32;
             mma_bf16(tmem + h * 256, sdesc_sw128(sb + (kHalves == 2 ? h : 0) * 32768 + o, 16, 1024),
-                     sdesc_sw128(sb + s_k + st * 32768 + o, 16, 1024), id_s, kk > 0 ? 1u : 0u);
+                     sdesc_sw128(k_at + o, 16, 1024), id_s, kk > 0 ? 1u : 0u);
           }
           mma_commit(bar(bS + h));
-          if (closes(i)) mma_commit(bar(bKFree + st));
+          if (kHalves == 1 || h == 1) {
+            mma_commit(bar(bKFree + rs.st));
+            rs.next(stages);
+          }
+          return true;
+        };
+        // O += P V of step i, in S buffer h = i & 1
+        auto products = [&](int i, int h) -> bool {
+          if (!wait(bP + h, np[h])) return false;
+          np[h] ^= 1;
+          if ((kHalves == 1 || h == 0) && !wait(bV + rv.st, rv.turn)) return false;
+          if (i < 2 && rc > 0 && !wait(bOFree + h, (rc - 1) & 1)) return false;
+          tc_fence_after();
+          const uint32_t v_at = sb + s_v + rv.st * 32768;
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            mma_bf16_ts(tmem + h * 256 + 128, tmem + h * 256 + kk * 8, sdesc_sw128(v_at + kk * 2048, 16384, 1024),
+                        id_pv, (i >= 2 || kk > 0) ? 1u : 0u);
+          if (kHalves == 1 || h == 1) {
+            mma_commit(bar(bVFree + rv.st));
+            rv.next(stages);
+          }
           return true;
         };
         if (!(ok = wait(bQ, rc & 1))) break;
-        for (int i = 0; i < min(2, steps) && ok; ++i) ok = scores(i);
-        for (int i = 0; i < steps && ok; ++i) {
-          const int t = kt0 + tile_of(i), st = t % stages, h = i & 1;
-          ok = wait(bP + h, np[h]++ & 1) && (!opens(i) || wait(bV + st, (t / stages) & 1)) &&
-               (i >= 2 || rc == 0 || wait(bOFree + h, (rc - 1) & 1));
-          if (!ok) break;
-          tc_fence_after();
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            mma_bf16_ts(tmem + h * 256 + 128, tmem + h * 256 + kk * 8,
-                        sdesc_sw128(sb + s_v + st * 32768 + kk * 2048, 16384, 1024), id_pv,
-                        (i >= 2 || kk > 0) ? 1u : 0u);
-          if (closes(i)) mma_commit(bar(bVFree + st));
-          if (i + 2 < steps) ok = scores(i + 2);
+        ok = scores(0) && (steps < 2 || scores(1));
+        for (int i = 0; i < steps && ok; i += 2) {
+          ok = products(i, 0) && (i + 2 >= steps || scores(0));
+          if (ok && i + 1 < steps) ok = products(i + 1, 1) && (i + 3 >= steps || scores(1));
         }
         if (!ok) break;
         // the second half had no step: its phase is waited for all the same
         if (steps == 1 && rc > 0 && !(ok = wait(bOFree + 1, (rc - 1) & 1))) break;
         mma_commit(bar(bQFree));
         mma_commit(bar(bO));
-        kt0 += tiles;
       }
       // every MMA issued here is complete before TMEM is freed
       mma_commit(bar(bDrain));
@@ -237,7 +265,7 @@ draft_part_wide(const __grid_constant__ WideMaps maps, const DraftParams p, int 
       return __all_sync(0xffffffffu, mbar_wait(bar(b), parity, abort_flag, kWaitNs));
     };
     bool ok = true;
-    uint32_t ns = 0;  // score tiles taken
+    uint32_t ns = 0;  // score tiles taken, mod 2
     int rc = 0, kt0 = 0;
     for (; u < u_end && ok; ++rc) {
       Run run;
@@ -246,7 +274,8 @@ draft_part_wide(const __grid_constant__ WideMaps maps, const DraftParams p, int 
       float m = -INFINITY, l = 0.f;
       for (int i = h; i < steps; i += 2) {
         const int kt = tile_of(i), left = run.k1 - run.k0 - kt * kBN;
-        if (!(ok = wait(bS + h, ns++ & 1))) break;
+        if (!(ok = wait(bS + h, ns))) break;
+        ns ^= 1;
         tc_fence_after();
         uint32_t sr[128];
         tmem_ld128(t_s, sr);
