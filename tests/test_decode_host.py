@@ -213,7 +213,7 @@ def test_verify_refusals(lib, kw, code):
 def test_workspace_bytes(lib):
     f = lib.flide_draft_attn_workspace_bytes
     assert f(-1, 4, 8, 2, 128) == 0 and f(1, 4, 8, 3, 128) == 0 and f(1, 4, 0, 1, 128) == 0 and f(1, 4, 8, 2, 0) == 0
-    assert f(1, 4, 8, 2, 128) > 0 and f(8, 64, 8, 2, 128) > f(1, 64, 8, 2, 128)
+    assert 0 < f(8, 8, 8, 2, 128) < f(8, 64, 8, 2, 128) < f(8, 640, 8, 2, 128)
 
 
 # ---- the binding's own checks: host tensors, types and shapes never reach the library ----

@@ -103,6 +103,6 @@ __device__ __forceinline__ int draft_run(const DraftParams &p, const long long *
 }
 
 // draft_wide.cu: 128- or 256-row tiles on tcgen05 (bf16, d == 128)
-int draft_wide_launch(const DraftParams &p, int past_rows, cudaStream_t s);
+int draft_wide_launch(const DraftParams &p, int past_rows, int dev, cudaStream_t s);
 
 }  // namespace flide

@@ -24,6 +24,7 @@
 #include <algorithm>
 
 #include "draft.cuh"
+#include "launch.cuh"
 #include "sm100.cuh"
 
 namespace flide {
@@ -763,31 +764,30 @@ DraftSpace draft_space(long long R, long long T, int Hkv, int G, int d, Variant 
   return s;
 }
 
-// Launches `kernel` on the workers with `smem` bytes of dynamic shared memory.
-int part_launch(void (*kernel)(const DraftParams), const DraftParams &p, int threads, size_t smem,
-                cudaStream_t s) {
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-    return FLIDE_ERR_CUDA;
-  kernel<<<p.workers, threads, smem, s>>>(p);
+// Launches a part kernel on the workers with `smem` bytes of dynamic shared memory.
+template <auto kKernel>
+int part_launch(const DraftParams &p, int dev, int threads, size_t smem, cudaStream_t s) {
+  if (!allow_smem<kKernel>(dev)) return FLIDE_ERR_CUDA;
+  kKernel<<<p.workers, threads, smem, s>>>(p);
   FLIDE_LAUNCH_CHECK();
   return FLIDE_OK;
 }
 
 template <typename T>
-int portable_launch(DraftParams &p, int sms, cudaStream_t s) {
+int portable_launch(DraftParams &p, int dev, int sms, cudaStream_t s) {
   p.workers = min(kMaxWorkers, 4 * sms);
   p.unit = kPKeys;
-  return part_launch(draft_part_portable<T>, p, kPT,
-                     (size_t)(p.x.R + 1) * 16 + 16 +
-                         sizeof(float) * ((size_t)(kPRows + 2 * kPKeys) * (p.d + 4) + kPRows * kPKeys), s);
+  return part_launch<draft_part_portable<T>>(
+      p, dev, kPT, (size_t)(p.x.R + 1) * 16 + 16 +
+                       sizeof(float) * ((size_t)(kPRows + 2 * kPKeys) * (p.d + 4) + kPRows * kPKeys), s);
 }
 
 template <int D, bool F8, int kMT>
-int mma_launch(DraftParams &p, int sms, cudaStream_t s) {
+int mma_launch(DraftParams &p, int dev, int sms, cudaStream_t s) {
   using S = MmaShape<D, F8, kMT>;
   p.workers = min(kMaxWorkers, S::kBlocks * sms);
   p.unit = S::kUnit;
-  return part_launch(draft_part_mma<D, F8, kMT>, p, S::kMW * 32, S::kSmem + (size_t)(p.x.R + 1) * 16, s);
+  return part_launch<draft_part_mma<D, F8, kMT>>(p, dev, S::kMW * 32, S::kSmem + (size_t)(p.x.R + 1) * 16, s);
 }
 
 template <typename T, typename TOut>
@@ -861,23 +861,23 @@ int draft_attn(const void *q, const void *k, const void *v, const void *past_k, 
   int rc;
   switch (var) {
     case kPortable:
-      rc = dtype == FLIDE_F32 ? portable_launch<float>(p, sms, s) : portable_launch<__nv_bfloat16>(p, sms, s);
+      rc = dtype == FLIDE_F32 ? portable_launch<float>(p, dev, sms, s) : portable_launch<__nv_bfloat16>(p, dev, sms, s);
       if (rc != FLIDE_OK) return rc;
       return dtype == FLIDE_F32 ? join_portable_launch<float, float>(p, s)
                                 : join_portable_launch<__nv_bfloat16, __nv_bfloat16>(p, s);
     case kMma16:
-      rc = dtype == FLIDE_E4M3 ? mma_launch<128, true, 1>(p, sms, s)
-           : d == 128          ? mma_launch<128, false, 1>(p, sms, s)
-                               : mma_launch<64, false, 1>(p, sms, s);
+      rc = dtype == FLIDE_E4M3 ? mma_launch<128, true, 1>(p, dev, sms, s)
+           : d == 128          ? mma_launch<128, false, 1>(p, dev, sms, s)
+                               : mma_launch<64, false, 1>(p, dev, sms, s);
       break;
     case kMma32:
-      rc = dtype == FLIDE_E4M3 ? mma_launch<128, true, 2>(p, sms, s)
-           : d == 128          ? mma_launch<128, false, 2>(p, sms, s)
-                               : mma_launch<64, false, 2>(p, sms, s);
+      rc = dtype == FLIDE_E4M3 ? mma_launch<128, true, 2>(p, dev, sms, s)
+           : d == 128          ? mma_launch<128, false, 2>(p, dev, sms, s)
+                               : mma_launch<64, false, 2>(p, dev, sms, s);
       break;
     default:
       p.workers = min(kWideWorkers, sms);
-      rc = draft_wide_launch(p, past_rows, s);
+      rc = draft_wide_launch(p, past_rows, dev, s);
   }
   if (rc != FLIDE_OK) return rc;
   if (dtype == FLIDE_E4M3) return join_launch<uint8_t, 128>(p, s);

@@ -24,6 +24,7 @@
 #include <cuda.h>
 
 #include "draft.cuh"
+#include "launch.cuh"
 #include "sm100.cuh"
 
 namespace flide {
@@ -409,14 +410,12 @@ bool wide_map(CUtensorMap *m, const void *base, int heads, long rows, int box_he
 }
 
 template <int kHalves>
-int wide_launch(const DraftParams &p, const WideMaps &maps, int mtok, int box_rows, cudaStream_t s) {
+int wide_launch(const DraftParams &p, const WideMaps &maps, int mtok, int box_rows, int dev, cudaStream_t s) {
   int stages = kHalves == 2 ? 2 : kMaxStages;
   while (wide_smem(kHalves, stages, p.x.R) > kSmemMax) --stages;
   if (stages < 2) return FLIDE_ERR_CAPACITY;
   const size_t smem = wide_smem(kHalves, stages, p.x.R);
-  if (cudaFuncSetAttribute(draft_part_wide<kHalves>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)smem) != cudaSuccess)
-    return FLIDE_ERR_CUDA;
+  if (!allow_smem<draft_part_wide<kHalves>>(dev)) return FLIDE_ERR_CUDA;
   draft_part_wide<kHalves><<<p.workers, kWThreads, smem, s>>>(maps, p, mtok, box_rows, stages);
   FLIDE_LAUNCH_CHECK();
   return FLIDE_OK;
@@ -424,7 +423,7 @@ int wide_launch(const DraftParams &p, const WideMaps &maps, int mtok, int box_ro
 
 }  // namespace
 
-int draft_wide_launch(const DraftParams &p0, int past_rows, cudaStream_t s) {
+int draft_wide_launch(const DraftParams &p0, int past_rows, int dev, cudaStream_t s) {
   DraftParams p = p0;
   p.unit = kBN;
   const int mtok = kBM / p.G;
@@ -438,7 +437,7 @@ int draft_wide_launch(const DraftParams &p0, int past_rows, cudaStream_t s) {
       !wide_map(&maps.k, past ? p.past_k : p.k, p.Hkv, past ? past_rows : p.x.T, 1, box_rows) ||
       !wide_map(&maps.v, past ? p.past_v : p.v, p.Hkv, past ? past_rows : p.x.T, 1, box_rows))
     return FLIDE_ERR_CUDA;
-  return p.halves ? wide_launch<1>(p, maps, mtok, box_rows, s) : wide_launch<2>(p, maps, mtok, box_rows, s);
+  return p.halves ? wide_launch<1>(p, maps, mtok, box_rows, dev, s) : wide_launch<2>(p, maps, mtok, box_rows, dev, s);
 }
 
 }  // namespace flide

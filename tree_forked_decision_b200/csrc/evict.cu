@@ -15,6 +15,7 @@
 // equal ones the lowest index).  The kept rows stay in order and move to the
 // front of the destination's blocks, in place if they are the source's.
 #include "common.cuh"
+#include "launch.cuh"
 #include "sm100.cuh"
 #include "worklist.cuh"
 
@@ -261,22 +262,18 @@ __global__ void __launch_bounds__(kMassWarps * 32, 2) mass_kernel_mma(const Mass
 }
 
 template <int D, bool F8>
-int mass_mma_launch(const MassParams &p, int sms, cudaStream_t s) {
+int mass_mma_launch(const MassParams &p, int dev, int sms, cudaStream_t s) {
   const size_t smem = (size_t)MassShape<D, F8>::kTiles * MassShape<D, F8>::kTileBytes + (size_t)(p.x.R + 1) * 8;
-  if (cudaFuncSetAttribute(mass_kernel_mma<D, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)smem) != cudaSuccess)
-    return FLIDE_ERR_CUDA;
+  if (!allow_smem<mass_kernel_mma<D, F8>>(dev)) return FLIDE_ERR_CUDA;
   mass_kernel_mma<D, F8><<<2 * sms, kMassWarps * 32, smem, s>>>(p);
   FLIDE_LAUNCH_CHECK();
   return FLIDE_OK;
 }
 
 template <typename T>
-int mass_launch(const MassParams &p, int sms, cudaStream_t s) {
+int mass_launch(const MassParams &p, int dev, int sms, cudaStream_t s) {
   const size_t smem = (size_t)(p.x.R + 1) * 8 + sizeof(float) * kMKeys * (p.d + 1);
-  if (cudaFuncSetAttribute(mass_kernel_portable<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)smem) != cudaSuccess)
-    return FLIDE_ERR_CUDA;
+  if (!allow_smem<mass_kernel_portable<T>>(dev)) return FLIDE_ERR_CUDA;
   mass_kernel_portable<T><<<8 * sms, kMThreads, smem, s>>>(p);
   FLIDE_LAUNCH_CHECK();
   return FLIDE_OK;
@@ -548,11 +545,11 @@ int flide_history_mass(const void *q, const void *k, const float *lse, const voi
   p.d = d;
   p.scale = scale;
   cudaStream_t s = (cudaStream_t)stream;
-  if (dtype == FLIDE_F32) return mass_launch<float>(p, sms, s);
-  if (dtype == FLIDE_E4M3) return mass_mma_launch<128, true>(p, sms, s);
-  if (d == 128) return mass_mma_launch<128, false>(p, sms, s);
-  if (d == 64) return mass_mma_launch<64, false>(p, sms, s);
-  return mass_launch<__nv_bfloat16>(p, sms, s);
+  if (dtype == FLIDE_F32) return mass_launch<float>(p, dev, sms, s);
+  if (dtype == FLIDE_E4M3) return mass_mma_launch<128, true>(p, dev, sms, s);
+  if (d == 128) return mass_mma_launch<128, false>(p, dev, sms, s);
+  if (d == 64) return mass_mma_launch<64, false>(p, dev, sms, s);
+  return mass_launch<__nv_bfloat16>(p, dev, sms, s);
 }
 
 int flide_history_evict(int32_t R, const int32_t *req_slot, int32_t n_slots, const int32_t *hist_len,

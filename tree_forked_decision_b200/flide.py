@@ -625,32 +625,35 @@ def state_slots(tree) -> int:
 
 # ---- speculative decoding over a history --------------------------------------
 
-def _on(where, device, stream, index=None, **named):
-    """Device addresses (None for None) of a call's dense tensors, which (and the
-    tree index) all lie on `device`, the current one, on whose stream the call runs."""
-    if device.type != "cuda":
-        raise ValueError(f"{where}: expected CUDA tensors, got one on {device}")
-    if device.index != torch.cuda.current_device() or (stream is not None and stream.device != device):
-        raise ValueError(f"{where}: the tensors are on {device}; make it the current device and the "
+def _on(where, ref, stream, index=None, **named):
+    """Device addresses (None for None) of a call's dense tensors, and the stream it
+    runs on: the tensors and the tree index lie on ref's device, which is the
+    current one and the stream's."""
+    dev = ref.get_device()
+    if dev < 0:
+        raise ValueError(f"{where}: expected CUDA tensors, got one on {ref.device}")
+    if dev != torch._C._cuda_getDevice() or (stream is not None and stream.device_index != dev):
+        raise ValueError(f"{where}: the tensors are on {ref.device}; make it the current device and the "
                          "stream's")
-    if index is not None and index.buf.device != device:
-        raise ValueError(f"{where}: the tree index is on {index.buf.device}, expected {device}")
+    if index is not None and index.buf.get_device() != dev:
+        raise ValueError(f"{where}: the tree index is on {index.buf.device}, expected {ref.device}")
     got = []
-    for name, t in named.items():
+    for t in named.values():
         if t is None:
             got.append(None)
-            continue
-        if t.device != device:
-            raise ValueError(f"{where}: {name} is on {t.device}, expected {device}")
-        if not t.is_contiguous():
+        elif t.get_device() == dev and t.is_contiguous():
+            got.append(t.data_ptr())
+        else:
+            break
+    else:
+        got.append(torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
+        return got
+    for name, t in named.items():  # names the one that stopped the loop
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{where}: {name} is on {t.device}, expected {ref.device}")
+        if t is not None and not t.is_contiguous():
             raise ValueError(f"{where}: {name} must be contiguous, got strides {tuple(t.stride())} for "
                              f"shape {tuple(t.shape)}")
-        got.append(t.data_ptr())
-    return got
-
-
-def _raw_stream(stream):
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
 
 
 def _new(shape, dtype, device, stream):
@@ -663,7 +666,7 @@ def _new(shape, dtype, device, stream):
 
 def _typed(where, dtype, **named):
     for name, t in named.items():
-        if t is not None and t.dtype != dtype:
+        if t is not None and t.dtype is not dtype:
             raise TypeError(f"{where}: {name} must be {dtype}, got {t.dtype}")
 
 
@@ -718,13 +721,13 @@ def rope(q, k, index: TreeIndex, freqs, pos_offset=None, mscale: float = 1.0,
         _typed("rope", torch.int32, pos_offset=pos_offset)
         if pos_offset.numel() < index.R:
             raise ValueError(f"rope: pos_offset needs {index.R} entries")
-    po, pf, pq, pk, pqo, pko = _on("rope", ref.device, stream, index, pos_offset=pos_offset, freqs=freqs, q=q,
+    po, pf, pq, pk, pqo, pko, st = _on("rope", ref, stream, index, pos_offset=pos_offset, freqs=freqs, q=q,
                                    k=k, q_out=q_out if q is not None else None,
                                    k_out=k_out if k is not None else None)
     _check(_lib().flide_rope(ctypes.byref(index.c), po, pf, pq, pk, pqo, pko,
                              0 if q is None else q.shape[1], 0 if k is None else k.shape[1],
                              ref.shape[2], 2 * freqs.numel(), interleaved, transpose, mscale,
-                             _dtype_code(ref), _raw_stream(stream)), "flide_rope")
+                             _dtype_code(ref), st), "flide_rope")
     return q_out, k_out
 
 
@@ -784,12 +787,12 @@ def draft_attn(q, k, v, index: TreeIndex, scale: float, past_k=None, past_v=None
         past_k = past_v = None
     code, out, lse, workspace = _draft_args("draft_attn", q, k, v, index, past_k, past_v, descale, out,
                                             lse, workspace, stream)
-    a = _on("draft_attn", q.device, stream, index, q=q, k=k, v=v, past_k=past_k, past_v=past_v,
+    a = _on("draft_attn", q, stream, index, q=q, k=k, v=v, past_k=past_k, past_v=past_v,
             descale=descale, out=out, lse=lse, workspace=workspace)
     _check(_lib().flide_draft_attn(a[0], a[1], a[2], a[3], a[4], 0 if past_k is None else past_k.shape[0],
                                    ctypes.byref(index.c), q.shape[1], k.shape[1], q.shape[2], code, a[5],
                                    scale, a[6], a[7], a[8], workspace.numel() * workspace.element_size(),
-                                   _raw_stream(stream)), "flide_draft_attn")
+                                   a[-1]), "flide_draft_attn")
     return out, lse
 
 
@@ -812,14 +815,14 @@ def draft_attn_paged(q, k, v, index: TreeIndex, scale: float, pool_k, pool_v, bl
                                             out, lse, workspace, stream)
     n_blocks, n_slots = _paged_args("draft_attn_paged", index, pool_k, block_table, req_slot, block_rows,
                                     max_blocks)
-    a = _on("draft_attn_paged", q.device, stream, index, q=q, k=k, v=v, pool_k=pool_k, pool_v=pool_v,
+    a = _on("draft_attn_paged", q, stream, index, q=q, k=k, v=v, pool_k=pool_k, pool_v=pool_v,
             block_table=block_table, req_slot=req_slot, descale=descale, out=out, lse=lse,
             workspace=workspace)
     _check(_lib().flide_draft_attn_paged(a[0], a[1], a[2], a[3], a[4], n_blocks, block_rows, a[5],
                                          max_blocks, a[6], n_slots, ctypes.byref(index.c), q.shape[1],
                                          k.shape[1], q.shape[2], code, a[7], scale, a[8], a[9], a[10],
                                          workspace.numel() * workspace.element_size(),
-                                         _raw_stream(stream)), "flide_draft_attn_paged")
+                                         a[-1]), "flide_draft_attn_paged")
     return out, lse
 
 
@@ -848,10 +851,10 @@ def verify_draft(index: TreeIndex, tokens, target, u, u_next, draft=None, n_acce
                        ("next_token", next_token, index.R)):
         if t.numel() < n:
             raise ValueError(f"verify_draft: {name} needs {n} entries")
-    a = _on("verify_draft", dev, stream, index, tokens=tokens, target=target, draft=draft, u=u, u_next=u_next,
+    a = _on("verify_draft", target, stream, index, tokens=tokens, target=target, draft=draft, u=u, u_next=u_next,
             n_accept=n_accept, next_token=next_token, path=path)
     _check(_lib().flide_verify_draft(ctypes.byref(index.c), a[0], a[1], a[2], a[3], a[4], target.shape[1],
-                                     _dtype_code(target), a[5], a[6], a[7], _raw_stream(stream)),
+                                     _dtype_code(target), a[5], a[6], a[7], a[-1]),
            "flide_verify_draft")
     return n_accept, next_token, path
 
@@ -881,12 +884,12 @@ def history_mass(q, k, lse, index: TreeIndex, scale: float, pool_k, block_table,
     _typed("history_mass", torch.float32, lse=lse, mass=mass, mass_out=mass_out)
     _shaped("history_mass", q.shape[:2], lse=lse)
     _shaped("history_mass", (n_slots, max_blocks * block_rows), mass=mass, mass_out=mass_out)
-    a = _on("history_mass", q.device, stream, index, q=q, k=k, lse=lse, pool_k=pool_k, block_table=block_table,
+    a = _on("history_mass", q, stream, index, q=q, k=k, lse=lse, pool_k=pool_k, block_table=block_table,
             req_slot=req_slot, descale=descale, mass=mass, mass_out=mass_out)
     _check(_lib().flide_history_mass(a[0], a[1], a[2], a[3], n_blocks, block_rows, a[4], max_blocks, a[5],
                                      n_slots, ctypes.byref(index.c), q.shape[1], k.shape[1], q.shape[2],
                                      E4M3 if e4m3 else _dtype_code(q), a[6], scale, a[7], a[8],
-                                     _raw_stream(stream)), "flide_history_mass")
+                                     a[-1]), "flide_history_mass")
     return mass_out
 
 
@@ -921,12 +924,12 @@ def history_evict(req_slot, lengths, block_table, block_rows: int, max_blocks: i
     for name, t in (("block_table", block_table), ("dst_table", dst_table)):
         if t.numel() < n_slots * max_blocks:
             raise ValueError(f"history_evict: {name} needs {n_slots * max_blocks} entries")
-    a = _on("history_evict", pool_k.device, stream, req_slot=req_slot, lengths=lengths,
+    a = _on("history_evict", pool_k, stream, req_slot=req_slot, lengths=lengths,
             block_table=block_table, pool_k=pool_k, pool_v=pool_v, mass=mass, dst_k=dst_k, dst_v=dst_v,
             dst_table=dst_table, mass_out=mass_out, kept=kept, status=status)
     _check(_lib().flide_history_evict(R, a[0], n_slots, a[1], a[2], max_blocks, block_rows, a[3], a[4],
                                       pool_k.shape[0] // block_rows, pool_k.shape[1], pool_k.shape[2],
                                       E4M3 if _e4m3(pool_k) else _dtype_code(pool_k), a[5], budget, sinks,
                                       recent, a[6], a[7], a[8], dst_k.shape[0] // block_rows, a[9], a[10],
-                                      a[11], _raw_stream(stream)), "flide_history_evict")
+                                      a[11], a[-1]), "flide_history_evict")
     return kept
