@@ -32,7 +32,7 @@ namespace flide {
 namespace {
 
 constexpr int kCluster = 8;
-constexpr int kVThreads = 512;
+constexpr int kVThreads = 256;  // four blocks to an SM: 74 trees at a time
 constexpr int kVWarps = kVThreads / 32;
 constexpr int kMaxNodes = 4096;  // nodes of one request
 constexpr int kMaxKids = 1024;   // continuations of one token
@@ -57,8 +57,18 @@ __device__ __forceinline__ double warp_sum_d(double v) {
   return v;
 }
 
+template <int k>
+struct Kind {
+  static constexpr int value = k;
+};
+
+constexpr int kHeld = 512;  // branch tokens whose candidates are looked up beforehand
+
 struct VerifyShared {
-  int parent[kMaxNodes];  // request-local parent of each node
+  int start[kMaxNodes + 1];     // first stream row of each node (and the end)
+  int16_t parent[kMaxNodes];    // request-local parent of each node
+  int tok[kHeld];               // a drafted token, its random number and its
+  float u[kHeld], px[kHeld], qx[kHeld];  // probabilities at the token before it
   int kid_token[kMaxKids];
   double seg[kMaxSegs];
   double warp[kVWarps];
@@ -66,8 +76,23 @@ struct VerifyShared {
   int stop;
 };
 
-template <typename T>
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kVThreads)
+// Entries v .. v + 3 of a row (0 past `end`); kVec: rows are whole 4-entry words.
+template <typename T, bool kVec>
+__device__ __forceinline__ float4 load4(const T *row, int v, int end) {
+  if constexpr (kVec && sizeof(T) == 4) {
+    return v < end ? __ldg(reinterpret_cast<const float4 *>(row + v)) : make_float4(0.f, 0.f, 0.f, 0.f);
+  } else if constexpr (kVec) {
+    const uint2 w = v < end ? __ldg(reinterpret_cast<const uint2 *>(row + v)) : make_uint2(0u, 0u);
+    return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
+                       __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
+  } else {
+    return make_float4(v < end ? load_f(row + v) : 0.f, v + 1 < end ? load_f(row + v + 1) : 0.f,
+                       v + 2 < end ? load_f(row + v + 2) : 0.f, v + 3 < end ? load_f(row + v + 3) : 0.f);
+  }
+}
+
+template <typename T, bool kVec>
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kVThreads, 4)
 verify_kernel(const VerifyParams p) {
   __shared__ VerifyShared sh;
   cg::cluster_group cluster = cg::this_cluster();
@@ -94,8 +119,10 @@ verify_kernel(const VerifyParams p) {
     cluster.sync();  // block 0's flag has been read
     return;
   }
-  for (int i = tid; i < nn; i += kVThreads)
-    sh.parent[i] = i == 0 ? -1 : x.anc_node[x.anc_ptr[n0 + i + 1] - 2] - n0;
+  for (int i = tid; i <= nn; i += kVThreads) {
+    sh.start[i] = x.node_start[n0 + i];
+    if (i < nn) sh.parent[i] = (int16_t)(i == 0 ? -1 : x.anc_node[x.anc_ptr[n0 + i + 1] - 2] - n0);
+  }
   __syncthreads();
 
   const T *P = static_cast<const T *>(p.target), *Q = static_cast<const T *>(p.draft);
@@ -107,33 +134,89 @@ verify_kernel(const VerifyParams p) {
   const int seg_len = max(128, ((slice + kMaxSegs - 1) / kMaxSegs + 127) / 128 * 128);
   const int n_seg = (v_hi - v_lo + seg_len - 1) / seg_len;
 
-  int cur = x.node_start[n0 + 1] - 1, node = 0, taken = 0;
+  // what a walk can ask of the drafted tokens, all at once: a walk that loads it
+  // token by token waits for three loads in a row at every level
+  const int branch = sh.start[1];
+  struct Candidate {
+    int tok;
+    float u, px, qx;
+  };
+  auto look_up = [&](int row, int before) -> Candidate {
+    Candidate k{p.tokens[row], p.u[row], 0.f, 0.f};
+    if (k.tok >= 0 && k.tok < V) {
+      k.px = load_f(P + (size_t)before * V + k.tok);
+      if (sampled) k.qx = load_f(Q + (size_t)before * V + k.tok);
+    }
+    return k;
+  };
+  for (int i = tid; i < min(kHeld, end - branch); i += kVThreads) {
+    const int row = branch + i, m = x.token_node[row] - n0;
+    const Candidate k = look_up(row, row > sh.start[m] ? row - 1 : sh.start[sh.parent[m] + 1] - 1);
+    sh.tok[i] = k.tok;
+    sh.u[i] = k.u;
+    sh.px[i] = k.px;
+    sh.qx[i] = k.qx;
+  }
+  __syncthreads();
+
+  int cur = branch - 1, node = 0, taken = 0;
   int flip = 0;
   double c = 0., D = 1.;
   int n_out = 0;  // point masses rejected at this token
 
   // weight of entry v in the residual of the current token
-  auto weight = [&](const T *prow, const T *qrow, int v) -> double {
-    double w = prob_of(load_f(prow + v));
+  auto weight = [&](int v, float pv, float qv) -> double {
+    double w = prob_of(pv);
     if (sampled) {
-      if (c > 0.) w = w - c * prob_of(load_f(qrow + v));
+      if (c > 0.) w = fma(-c, prob_of(qv), w);
       return w > 0. ? w : 0.;
     }
     for (int i = 0; i < n_out; ++i)
       if (sh.kid_token[i] == v) return 0.;
     return w;
   };
+  // this block's segment sums, kind: 0 the row p, 1 (p - c q)+, 2 p without the
+  // rejected tokens (kept apart: the test for each entry cost more than its sum)
+  auto sum_segments = [&](const T *prow, const T *qrow, auto kind) {
+    constexpr int kKind = decltype(kind)::value;
+    constexpr int kAhead = 4;  // segments on their way per warp
+    for (int s0 = warp; s0 < n_seg; s0 += kAhead * kVWarps) {
+      double acc[kAhead] = {0., 0., 0., 0.};
+      for (int o = 4 * lane; o < seg_len; o += 128) {
+        float4 a[kAhead], b[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          const int v = v_lo + (s0 + k * kVWarps) * seg_len + o;
+          a[k] = load4<T, kVec>(prow, v, v_hi);
+          if (kKind == 1) b[k] = load4<T, kVec>(qrow, v, v_hi);
+        }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          const float pv[4] = {a[k].x, a[k].y, a[k].z, a[k].w}, qv[4] = {b[k].x, b[k].y, b[k].z, b[k].w};
+          double w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (kKind == 1) w[i] = fmax(fma(-c, (double)fmaxf(qv[i], 0.f), (double)fmaxf(pv[i], 0.f)), 0.);
+            else if (kKind == 0) w[i] = (double)fmaxf(pv[i], 0.f);
+            else w[i] = weight(v_lo + (s0 + k * kVWarps) * seg_len + o + i, pv[i], 0.f);
+          }
+          acc[k] += (w[0] + w[1]) + (w[2] + w[3]);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const double t = warp_sum_d(acc[k]);
+        if (lane == 0 && s0 + k * kVWarps < n_seg) sh.seg[s0 + k * kVWarps] = t;
+      }
+    }
+  };
   // sum of the weights over the vocabulary, the same bits in every block;
   // leaves each segment's sum in sh.seg and each block's in its sh.total
   auto sum_weights = [&](const T *prow, const T *qrow) -> double {
     __syncthreads();
-    for (int s = warp; s < n_seg; s += kVWarps) {
-      const int a = v_lo + s * seg_len, b = min(v_hi, a + seg_len);
-      double acc = 0.;
-      for (int v = a + lane; v < b; v += 32) acc += weight(prow, qrow, v);
-      acc = warp_sum_d(acc);
-      if (lane == 0) sh.seg[s] = acc;
-    }
+    if (sampled && c > 0.) sum_segments(prow, qrow, Kind<1>{});
+    else if (sampled || n_out == 0) sum_segments(prow, qrow, Kind<0>{});
+    else sum_segments(prow, qrow, Kind<2>{});
     __syncthreads();
     if (warp == 0) {
       double acc = 0.;
@@ -157,61 +240,73 @@ verify_kernel(const VerifyParams p) {
   };
 
   const T *prow, *qrow;
+  double all = -1.;  // sum of the residual at the current token, if a pass has formed it
   for (;;) {
     prow = P + (size_t)cur * V;
-    qrow = sampled ? Q + (size_t)cur * V : nullptr;
+    qrow = sampled ? Q + (size_t)cur * V : prow;
     c = 0.;
     D = 1.;
+    all = -1.;
     n_out = 0;
-    const bool inside = cur + 1 < x.node_start[n0 + node + 1];  // the node goes on
+    const bool inside = cur + 1 < sh.start[node + 1];  // the node goes on
     int m = inside ? node : next_kid(node);
     int down = -1, tried = 0;
-    while (m < nn) {
-      const int row = inside ? cur + 1 : x.node_start[n0 + m];
-      const int tok = p.tokens[row];
-      if (++tried > kMaxKids) {
-        if (rank == 0 && tid == 0) set_status(x.status, FLIDE_ERR_CAPACITY);
-        break;
+    while (m < nn && down < 0) {
+      // up to 32 continuations at a time, a lane each (every warp alike)
+      int mine = -1, kids = 0;
+      for (; kids < 32 && m < nn; ++kids) {
+        if (lane == kids) mine = m;
+        m = inside ? nn : next_kid(m);
       }
-      if (tok < 0 || tok >= V) {
-        if (rank == 0 && tid == 0) set_status(x.status, FLIDE_ERR_INVALID);  // never accepted
-      } else {
-        const double u = (double)p.u[row], px = prob_of(load_f(prow + tok));
-        if (sampled) {
-          const double qx = prob_of(load_f(qrow + tok));
-          const double left = c > 0. ? px - c * qx : px;
-          if (u * qx * D < left) {
-            down = row;
+      int row = -1;
+      Candidate own{-1, 0.f, 0.f, 0.f};
+      if (mine >= 0) {
+        row = inside ? cur + 1 : sh.start[mine];
+        const int i = row - branch;
+        own = i < kHeld ? Candidate{sh.tok[i], sh.u[i], sh.px[i], sh.qx[i]} : look_up(row, cur);
+      }
+      for (int k = 0; k < kids && down < 0; ++k) {
+        const int k_row = __shfl_sync(0xffffffffu, row, k), k_tok = __shfl_sync(0xffffffffu, own.tok, k);
+        const double k_u = __shfl_sync(0xffffffffu, own.u, k), k_p = prob_of(__shfl_sync(0xffffffffu, own.px, k));
+        const double k_q = prob_of(__shfl_sync(0xffffffffu, own.qx, k));
+        if (++tried > kMaxKids) {
+          if (rank == 0 && tid == 0) set_status(x.status, FLIDE_ERR_CAPACITY);
+          m = nn;
+          break;
+        }
+        if (k_tok < 0 || k_tok >= V) {
+          if (rank == 0 && tid == 0) set_status(x.status, FLIDE_ERR_INVALID);  // never accepted
+        } else if (sampled) {
+          if (k_u * k_q * D < fma(-c, k_q, k_p)) {
+            down = k_row;
           } else {
             c += D;
-            D = sum_weights(prow, qrow);
+            all = D = sum_weights(prow, qrow);
           }
         } else {
           bool gone = false;
-          for (int i = 0; i < n_out; ++i) gone |= sh.kid_token[i] == tok;
-          if (!gone && u * D < px) {
-            down = row;
+          for (int i = 0; i < n_out; ++i) gone |= sh.kid_token[i] == k_tok;
+          if (!gone && k_u * D < k_p) {
+            down = k_row;
           } else if (!gone) {
-            D -= px;
+            D -= k_p;
             __syncthreads();
-            if (tid == 0) sh.kid_token[n_out] = tok;
+            if (tid == 0) sh.kid_token[n_out] = k_tok;
             __syncthreads();
             ++n_out;
           }
         }
+        if (down >= 0) node = __shfl_sync(0xffffffffu, mine, k);
       }
-      if (down >= 0 || inside) break;
-      m = next_kid(m);
     }
     if (down < 0) break;
     if (rank == 0 && tid == 0) p.path[first + taken] = down;
     ++taken;
     cur = down;
-    node = m;
   }
 
   // the next token: first entry whose cumulative weight passes u * sum
-  double all = sum_weights(prow, qrow);
+  if (all < 0.) all = sum_weights(prow, qrow);
   if (!(all > 0.)) {  // nothing left (rounding): the target row itself
     c = 0.;
     n_out = 0;
@@ -237,23 +332,40 @@ verify_kernel(const VerifyParams p) {
     if (owner < 0 || !isfinite(all)) p.next_token[r] = -1;
   }
   if (owner < 0 || !isfinite(all) || rank != owner || warp != 0) return;
-  int s_hit = -1, s_last = -1;
+  // the segment: lanes sum runs of segments, then the run that holds the aim is
+  // looked through
+  const int per = (n_seg + 31) / 32;
+  double run = 0.;
+  int s_last = -1;
+  for (int s = lane * per; s < min(n_seg, (lane + 1) * per); ++s) {
+    run += sh.seg[s];
+    if (sh.seg[s] > 0.) s_last = s;
+  }
+  double upto = run;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const double y = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += y;
+  }
+  s_last = __reduce_max_sync(0xffffffffu, s_last);
+  const unsigned held = __ballot_sync(0xffffffffu, !fell && run > 0. && before + upto > aim);
+  int s_hit = -1;
   double acc = before;
-  for (int s = 0; s < n_seg; ++s) {
-    const double t = sh.seg[s];
-    if (t > 0.) s_last = s;
-    if (s_hit < 0) {
-      if (!fell && acc + t > aim) s_hit = s;
-      else acc += t;
+  if (held) {
+    const int at = __ffs(held) - 1;
+    acc += __shfl_sync(0xffffffffu, upto - run, at);
+    for (int s = at * per; s < min(n_seg, (at + 1) * per) && s_hit < 0; ++s) {
+      if (acc + sh.seg[s] > aim) s_hit = s;
+      else acc += sh.seg[s];
     }
   }
-  bool to_end = fell || s_hit < 0;
-  const int s = s_hit >= 0 ? s_hit : s_last;
+  const bool to_end = s_hit < 0;
+  const int s = to_end ? s_last : s_hit;
   const int a = v_lo + s * seg_len, b = min(v_hi, a + seg_len);
   int pick = -1, positive = -1;
   for (int v0 = a; v0 < b; v0 += 32) {
     const int v = v0 + lane;
-    const double w = v < b ? weight(prow, qrow, v) : 0.;
+    const double w = v < b ? weight(v, load_f(prow + v), load_f(qrow + v)) : 0.;
     double incl = w;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -289,8 +401,12 @@ extern "C" int flide_verify_draft(const flide_tree_index *idx, const int32_t *to
   const VerifyParams p{*idx, tokens, target, draft, u, u_next, V, n_accept, next_token, path};
   cudaStream_t s = (cudaStream_t)stream;
   const unsigned grid = (unsigned)idx->R * kCluster;
-  if (dtype == FLIDE_F32) verify_kernel<float><<<grid, kVThreads, 0, s>>>(p);
-  else verify_kernel<__nv_bfloat16><<<grid, kVThreads, 0, s>>>(p);
+  // rows of whole 16-byte (bf16: 8-byte) words are read as such
+  const bool vec = V % 4 == 0 && ((uintptr_t)target | (uintptr_t)draft) % 16 == 0;
+  if (dtype == FLIDE_F32 && vec) verify_kernel<float, true><<<grid, kVThreads, 0, s>>>(p);
+  else if (dtype == FLIDE_F32) verify_kernel<float, false><<<grid, kVThreads, 0, s>>>(p);
+  else if (vec) verify_kernel<__nv_bfloat16, true><<<grid, kVThreads, 0, s>>>(p);
+  else verify_kernel<__nv_bfloat16, false><<<grid, kVThreads, 0, s>>>(p);
   FLIDE_LAUNCH_CHECK();
   return FLIDE_OK;
 }
