@@ -17,8 +17,8 @@
 // residual by inverse CDF.  All of this is in 64 bits, so a decision does not
 // hang on the order of a sum.
 //
-// A cluster of 8 blocks walks one request: every block takes an eighth of the
-// vocabulary in each pass and repeats the walk's decisions from the same
+// A cluster of 8 (or 16) blocks walks one request: every block takes its part of
+// the vocabulary in each pass and repeats the walk's decisions from the same
 // numbers (sums are exchanged through distributed shared memory in a fixed
 // order).  Bound by the latency of the walk's dependent loads for one tree,
 // by the rows' bytes for a batch.
@@ -31,7 +31,6 @@ namespace cg = cooperative_groups;
 namespace flide {
 namespace {
 
-constexpr int kCluster = 8;
 constexpr int kVThreads = 256;  // four blocks to an SM: 74 trees at a time
 constexpr int kVWarps = kVThreads / 32;
 constexpr int kMaxNodes = 4096;  // nodes of one request
@@ -92,13 +91,13 @@ __device__ __forceinline__ float4 load4(const T *row, int v, int end) {
 }
 
 template <typename T, bool kVec>
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kVThreads, 4)
+__global__ void __launch_bounds__(kVThreads, 4)
 verify_kernel(const VerifyParams p) {
   __shared__ VerifyShared sh;
   cg::cluster_group cluster = cg::this_cluster();
   const flide_tree_index &x = p.x;
-  const int rank = (int)cluster.block_rank();
-  const int r = blockIdx.x / kCluster;
+  const int rank = (int)cluster.block_rank(), blocks = (int)cluster.num_blocks();
+  const int r = blockIdx.x / blocks;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // the status word may change while this kernel runs (another cluster's bad
   // token), so one block's reading decides for its whole cluster
@@ -129,7 +128,7 @@ verify_kernel(const VerifyParams p) {
   const bool sampled = Q != nullptr;
   const int V = p.V;
   // this block's slice and its segments (contiguous, at most kMaxSegs)
-  const int slice = ((V + kCluster - 1) / kCluster + 127) / 128 * 128;
+  const int slice = ((V + blocks - 1) / blocks + 127) / 128 * 128;
   const int v_lo = min(V, rank * slice), v_hi = min(V, v_lo + slice);
   const int seg_len = max(128, ((slice + kMaxSegs - 1) / kMaxSegs + 127) / 128 * 128);
   const int n_seg = (v_hi - v_lo + seg_len - 1) / seg_len;
@@ -181,7 +180,7 @@ verify_kernel(const VerifyParams p) {
     constexpr int kKind = decltype(kind)::value;
     constexpr int kAhead = 4;  // segments on their way per warp
     for (int s0 = warp; s0 < n_seg; s0 += kAhead * kVWarps) {
-      double acc[kAhead] = {0., 0., 0., 0.};
+      double acc[kAhead] = {};
       for (int o = 4 * lane; o < seg_len; o += 128) {
         float4 a[kAhead], b[kAhead];
 #pragma unroll
@@ -226,7 +225,7 @@ verify_kernel(const VerifyParams p) {
     }
     cluster.sync();
     double all = 0.;
-    for (int b = 0; b < kCluster; ++b) all += cluster.map_shared_rank(sh.total, b)[flip];
+    for (int b = 0; b < blocks; ++b) all += cluster.map_shared_rank(sh.total, b)[flip];
     flip ^= 1;
     return all;
   };
@@ -316,7 +315,7 @@ verify_kernel(const VerifyParams p) {
   const double aim = (double)p.u_next[r] * all;
   double before = 0.;
   int owner = -1, last = -1;
-  for (int b = 0; b < kCluster; ++b) {
+  for (int b = 0; b < blocks; ++b) {
     const double t = cluster.map_shared_rank(sh.total, b)[flip];
     if (t > 0.) last = b;
     if (owner < 0) {
@@ -384,6 +383,30 @@ verify_kernel(const VerifyParams p) {
   if (lane == 0) p.next_token[r] = pick >= 0 ? pick : positive;
 }
 
+template <typename T, bool kVec>
+int verify_launch(const VerifyParams &p, bool wide, int dev, cudaStream_t s) {
+  static std::atomic<bool> allowed[64];  // zero-initialised: false
+  if (wide && (dev < 0 || dev >= 64 || !allowed[dev].load(std::memory_order_acquire))) {
+    if (cudaFuncSetAttribute(verify_kernel<T, kVec>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
+        cudaSuccess)
+      return FLIDE_ERR_CUDA;
+    if (dev >= 0 && dev < 64) allowed[dev].store(true, std::memory_order_release);
+  }
+  const unsigned blocks = wide ? 16 : 8;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = blocks;
+  at.val.clusterDim.y = 1;
+  at.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)p.x.R * blocks);
+  cfg.blockDim = dim3(kVThreads);
+  cfg.stream = s;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, verify_kernel<T, kVec>, p) == cudaSuccess ? FLIDE_OK : FLIDE_ERR_CUDA;
+}
+
 }  // namespace
 }  // namespace flide
 
@@ -400,13 +423,18 @@ extern "C" int flide_verify_draft(const flide_tree_index *idx, const int32_t *to
   if (idx->R == 0) return FLIDE_OK;
   const VerifyParams p{*idx, tokens, target, draft, u, u_next, V, n_accept, next_token, path};
   cudaStream_t s = (cudaStream_t)stream;
-  const unsigned grid = (unsigned)idx->R * kCluster;
-  // rows of whole 16-byte (bf16: 8-byte) words are read as such
+    // rows of whole 16-byte (bf16: 8-byte) words are read as such
   const bool vec = V % 4 == 0 && ((uintptr_t)target | (uintptr_t)draft) % 16 == 0;
-  if (dtype == FLIDE_F32 && vec) verify_kernel<float, true><<<grid, kVThreads, 0, s>>>(p);
-  else if (dtype == FLIDE_F32) verify_kernel<float, false><<<grid, kVThreads, 0, s>>>(p);
-  else if (vec) verify_kernel<__nv_bfloat16, true><<<grid, kVThreads, 0, s>>>(p);
-  else verify_kernel<__nv_bfloat16, false><<<grid, kVThreads, 0, s>>>(p);
-  FLIDE_LAUNCH_CHECK();
-  return FLIDE_OK;
+  // 16 blocks to a cluster where every tree has its 16 at once and its rows are
+  // long: a pass over 131072 entries takes 4 us instead of 6, the wider exchange
+  // costs 2 us a call (8192 entries: 11 instead of 9 us)
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return FLIDE_ERR_CUDA;
+  const bool wide = V >= 32768 && idx->R * 16 <= 4 * sms;
+  if (dtype == FLIDE_F32)
+    return vec ? verify_launch<float, true>(p, wide, dev, s) : verify_launch<float, false>(p, wide, dev, s);
+  return vec ? verify_launch<__nv_bfloat16, true>(p, wide, dev, s)
+             : verify_launch<__nv_bfloat16, false>(p, wide, dev, s);
 }
