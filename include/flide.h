@@ -566,8 +566,10 @@ size_t flide_draft_attn_workspace_bytes(int32_t R, int32_t T, int32_t Hq, int32_
  *          idx->T, Hq, Hkv, d) bytes; one call at a time
  * Rows past the stream's last token are left as they were.  A key that a row
  * does not see takes no part in its result, whatever its value.  q, k, v and
- * the past 16-byte aligned.  The softmax weights are rounded to the input's
- * precision (e4m3: to half) before they multiply v; their sum is not.
+ * the past 16-byte aligned.  The softmax weights are rounded to bf16 before they
+ * multiply v (not for FLIDE_F32; e4m3: to half, or to the sum of two e4m3 values:
+ * relative error <= 2^-8, absolute <= 2^-16 of the row's largest weight); their
+ * sum is not.
  * Host errors: FLIDE_ERR_SHAPE, FLIDE_ERR_CAPACITY (workspace too small, more
  * than 4096 requests, T * Hq past 2^30), FLIDE_ERR_CUDA; device errors as
  * flide_fork_attn. */

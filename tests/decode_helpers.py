@@ -29,14 +29,14 @@ def step(t):
 
 
 def attention(tree, q, k, v, pk, pv, scale):
-    """(o, lse, sum of w |v|, largest sum of |q k| * scale) per token and head, in 64 bits;
-    pk, pv: a list of each request's history rows."""
+    """(o, lse, sum of w |v|, largest w times the sum of |v|, largest sum of |q k| * scale) per token
+    and head, in 64 bits; pk, pv: a list of each request's history rows."""
     T, Hq, d = q.shape
     G = Hq // k.shape[1]
     q, k, v = (x.double() for x in (q, k, v))
     req, _, sees = layout(tree)
     o, lse = torch.zeros(T, Hq, d, dtype=torch.float64), torch.zeros(T, Hq, dtype=torch.float64)
-    wv, size = torch.zeros(T, Hq, d, dtype=torch.float64), 0.0
+    wv, peak, size = torch.zeros_like(o), torch.zeros_like(o), 0.0
     for t in range(len(req)):
         kk = torch.cat([pk[req[t]].double(), k[sees[t]]]).repeat_interleave(G, 1)
         vv = torch.cat([pv[req[t]].double(), v[sees[t]]]).repeat_interleave(G, 1)
@@ -46,17 +46,19 @@ def attention(tree, q, k, v, pk, pv, scale):
         w = torch.softmax(s, 1)
         o[t] = torch.einsum("hn,nhd->hd", w, vv)
         wv[t] = torch.einsum("hn,nhd->hd", w, vv.abs())
-    return o, lse, wv, size
+        peak[t] = w.amax(1, keepdim=True) * vv.abs().sum(0)
+    return o, lse, wv, peak, size
 
 
-def attention_tolerance(o, wv, size, d, keys, out_type, weight_step):
-    """Elementwise bound: the output's rounding, the rounded weights, and 32-bit sums.
+def attention_tolerance(o, wv, peak, size, d, keys, out_type, weight_step, weight_least=0.0):
+    """Elementwise bound: the output's rounding, the rounded weights (off by weight_step of
+    themselves, or weight_least of the row's largest), and 32-bit sums.
     A score is d products summed in 32 bits, off by at most (d + 4) 2^-24 of the sum of
     their sizes; that shifts its weight and the total by the same factor (hence 2 x).
     exp2 and its argument add 2^-20; keys 32-bit additions (keys + 8) 2^-24."""
     ds = (d + 4) * 2.0 ** -24 * size
     return step(out_type) * o.abs() + (weight_step + 2 * ds + 2.0 ** -20 + 2 * (keys + 8) * 2.0 ** -24) * wv \
-        + 1e-12
+        + weight_least * peak + 1e-12
 
 
 def lse_tolerance(lse, size, d, keys):

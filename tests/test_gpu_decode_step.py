@@ -78,10 +78,10 @@ def test_episode(block_rows):
             want = _turn(x16, pos + off, freqs.cpu())
             tol = dh.step(torch.bfloat16) * want.abs() + 6e-7 * x16.double().abs().amax(-1, keepdim=True) * 2
             assert bool(((gpu.double().cpu() - want).abs() <= tol).all())
-        ow, lw, wv, size = dh.attention(tree, qd.cpu(), kd.cpu(), vd.cpu(), past_k, past_v, scale)
+        ow, lw, wv, peak, size = dh.attention(tree, qd.cpu(), kd.cpu(), vd.cpu(), past_k, past_v, scale)
         keys = 128 + tree.T
         err = (o.double().cpu() - ow).abs()
-        assert bool((err <= dh.attention_tolerance(ow, wv, size, d, keys, torch.bfloat16, 2.0 ** -8)).all())
+        assert bool((err <= dh.attention_tolerance(ow, wv, peak, size, d, keys, torch.bfloat16, 2.0 ** -8)).all())
         assert bool(((lse.double().cpu() - lw).abs() <= dh.lse_tolerance(lw, size, d, keys)).all())
         n_w, t_w, p_w = dh.verify(tree, tokens, target.cpu().numpy(), None, u.numpy(), un.numpy())
         assert n_acc.tolist() == n_w.tolist() and nxt.tolist() == t_w.tolist() and path.tolist() == p_w.tolist()

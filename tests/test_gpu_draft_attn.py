@@ -24,12 +24,14 @@ TREES = {
                                           (200, [(-1, 3), (0, 2), (1, 1), (2, 4), (0, 1), (4, 1)]), (0, [(-1, 4)]),
                                           (90, [(-1, 1)] + [(i, 1) for i in range(11)])], 11),
     "wide": lambda: inputs._tree([(700, [(-1, 4)] + [(max(0, i - 3), 1) for i in range(59)])], 59),
-    # 16 and 30 to 70 tokens a request: tiles of 128 and of 256 rows with 4 heads to a group
+    # 16, 20 and 30 to 70 tokens a request: with 4 heads to a group tiles of 64, 128 and 256 rows
     "tile128": lambda: inputs._tree([(n, [(-1, 2)] + [(i // 2, 1) for i in range(14)]) for n in
                                      (0, 1, 127, 128, 129, 255, 256, 257, 383, 385, 2000)], 4),
     "tile256": lambda: inputs._tree([(n, [(-1, 3)] + [(i // 2, 1) for i in range(m)]) for n, m in
                                      ((0, 40), (1, 30), (127, 61), (128, 62), (129, 70), (513, 29), (3001, 61))], 6),
     "tile128_long": lambda: inputs._tree([(n, [(-1, 1)] + [(0, 1)] * 19) for n in (5100, 4900, 130, 5000)], 1),
+    "tile80": lambda: inputs._tree([(n, [(-1, 1)] + [(i // 3, 1) for i in range(19)]) for n in
+                                    (0, 1, 31, 33, 127, 129, 300, 1025)], 3),
     "long_one": lambda: inputs._tree([(5003, [(-1, 1), (0, 1), (1, 1)]), (3, [(-1, 2)])], 2),
     "many": lambda: inputs._tree([(int(n), [(-1, 1 + i % 3), (0, 1), (0, 2), (1, 1)]) for i, n in
                                   enumerate(np.random.default_rng(1).integers(0, 400, 37))], 2),
@@ -59,13 +61,15 @@ def _wide(y, s):
 def _check(tree, x, hist, ds, scale, got, lse, kind):
     d = x[0].shape[2]
     s = [None] * 3 if ds is None else ds
-    o, want, wv, size = dh.attention(tree, _wide(x[0], s[0]), _wide(x[1], s[1]), _wide(x[2], s[2]),
+    o, want, wv, peak, size = dh.attention(tree, _wide(x[0], s[0]), _wide(x[1], s[1]), _wide(x[2], s[2]),
                                      [_wide(h, s[1]) for h in hist[0]], [_wide(h, s[2]) for h in hist[1]], scale)
     keys = int(tree.past_len.max()) + tree.T
     out = torch.float32 if kind == "f32" else torch.bfloat16
-    # weights are rounded to bf16 (half for e4m3 codes) before they multiply v
-    w = {"f32": 0.0, "bf16": 2.0 ** -8, "e4m3": 2.0 ** -11}[kind]
-    tol = dh.attention_tolerance(o, wv, size, d, keys, out, w)
+    # weights are rounded to bf16 before they multiply v; with e4m3 codes to half, or to an e4m3
+    # code and its remainder's: each within half a step (2^-4) of what it stands for, 2^-8 together,
+    # and never closer than half the least step, 2^-10, of weights scaled by 2^6
+    w = {"f32": 0.0, "bf16": 2.0 ** -8, "e4m3": 2.0 ** -8}[kind]
+    tol = dh.attention_tolerance(o, wv, peak, size, d, keys, out, w, 2.0 ** -16 if kind == "e4m3" else 0.0)
     err = (got.double().cpu() - o).abs()
     assert got.dtype == out
     assert bool((err <= tol).all()), float((err / tol).max())
@@ -101,7 +105,7 @@ def test_packed(case, kind):
 
 @pytest.mark.parametrize("kind", ["bf16", "e4m3", "f32"])
 @pytest.mark.parametrize("block_rows", [16, 48, 128, 256])
-@pytest.mark.parametrize("case", ["edges", "odd_requests", "wide", "tile128", "tile256", "many"])
+@pytest.mark.parametrize("case", ["edges", "odd_requests", "wide", "tile128", "tile256", "tile80", "many"])
 def test_paged_with_nan_behind_the_rows(case, block_rows, kind):
     """Rows of a block past a history's end hold NaN, and belong to nobody."""
     tree = TREES[case]()

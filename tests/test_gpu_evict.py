@@ -30,7 +30,7 @@ def test_mass(block_rows, heads, kind):
     scale = 1 / math.sqrt(d)
     wide = [_wide(y, z) for y, z in zip(x, s)]
     pk, pv = [_wide(h, s[1]) for h in hist[0]], [_wide(h, s[2]) for h in hist[1]]
-    _, lse, _, size = dh.attention(tree, *wide, pk, pv, scale)
+    _, lse, _, _, size = dh.attention(tree, *wide, pk, pv, scale)
     lse = lse.float()
     pools, table, slots, width = dh.scatter(hist[:1], block_rows, np.random.default_rng(1), extra=40, fill=math.nan)
     g = torch.Generator().manual_seed(3)

@@ -17,9 +17,8 @@ struct DraftParams {
   int Hq, Hkv, G, d;
   float scale;
   // row tiles of tile_rows query rows (tokens x heads of the group), key units of
-  // `unit` history rows; a slot holds slot_rows partial rows: the tile's, and with
-  // `halves` a second partial of each from row slot_rows / 2 on
-  int workers, tile_rows, slot_rows, halves, unit;
+  // `unit` history rows; a run's slot holds 2^parts_log partials of a tile's rows
+  int workers, tile_rows, parts_log, unit;
   void *out;
   float *lse;
   // workspace: prefix sums of units and items, partial rows and their (max, sum)
@@ -102,7 +101,7 @@ __device__ __forceinline__ int draft_run(const DraftParams &p, const long long *
   return c1 - c0;
 }
 
-// draft_wide.cu: 128- or 256-row tiles on tcgen05 (bf16, d == 128)
-int draft_wide_launch(const DraftParams &p, int past_rows, int dev, cudaStream_t s);
+// draft_wide.cu: tiles of 32, 64, 128 (bf16, e4m3) or 256 rows (bf16) on tcgen05, d == 128
+int draft_wide_launch(const DraftParams &p, int past_rows, bool f8, int dev, cudaStream_t s);
 
 }  // namespace flide

@@ -514,7 +514,7 @@ __global__ void __launch_bounds__(256) draft_join_portable(const DraftParams p) 
     const int W = workers_of(U, p.workers);
     const int w0 = worker_of(U, W, u0), w1 = worker_of(U, W, u0 + per - 1);
     for (int w = w0; w <= w1; ++w) {
-      const size_t pr = (size_t)(w + p.item0[r] + li) * p.slot_rows + row % p.tile_rows;
+      const size_t pr = (size_t)(w + p.item0[r] + li) * p.tile_rows + row % p.tile_rows;
       const float pm = p.part_ml[2 * pr], pl = p.part_ml[2 * pr + 1];
       const float mn = fmaxf(m, pm), ref = mn == -INFINITY ? 0.f : mn;
       const float f = exp2f(m - ref), g = exp2f(pm - ref);
@@ -657,10 +657,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) draft_join_kernel(const Dr
     const long long li = (long long)tile * p.Hkv + hk, u0 = ua + li * per;
     const int W = workers_of(U, p.workers);
     const int w0 = worker_of(U, W, u0), w1 = worker_of(U, W, u0 + per - 1);
-    const int parts = (w1 - w0 + 1) << p.halves;
-    const size_t pr0 = (size_t)(w0 + ia + li) * p.slot_rows + row - tile * p.tile_rows;
+    const int parts = (w1 - w0 + 1) << p.parts_log;
+    const size_t pr0 = ((size_t)(w0 + ia + li) << p.parts_log) * p.tile_rows + row - tile * p.tile_rows;
     auto partial = [&](int i, float2 &ml, float4 (&v)[kE / 4]) {
-      const size_t pr = pr0 + (size_t)(i >> p.halves) * p.slot_rows + ((i & p.halves) ? p.slot_rows / 2 : 0);
+      const size_t pr = pr0 + (size_t)i * p.tile_rows;
       ml = *reinterpret_cast<const float2 *>(p.part_ml + 2 * pr);
 #pragma unroll
       for (int e = 0; e < kE / 4; ++e)
@@ -717,29 +717,26 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) draft_join_kernel(const Dr
 // ---- host ----------------------------------------------------------------------
 
 // Which part kernel, by the query rows of a request on average (the capacities:
-// the host sees no more): up to 16 rows one 16-row tile, up to 32 one of 32, and
-// above that, where the tcgen05 kernel takes the type and head layout, tiles of
-// 128 or 256; elsewhere more 32-row tiles, each a pass over the keys.
-enum Variant { kPortable, kMma16, kMma32, kWide128, kWide256 };
+// the host sees no more): up to 16 rows a 16-row tile, and above that, where the
+// tcgen05 kernel takes the type and head layout, its smallest tile that holds
+// them (bf16 up to 256 rows, e4m3 128); elsewhere 32-row tiles, each a pass over
+// the keys.
+enum Kernel { kPortable, kMma, kWide };
+struct Variant {
+  Kernel kernel;
+  int tile_rows, parts_log;
+};
 
 Variant variant_of(long long R, long long T, int G, int d, int dtype) {
-  if (dtype == FLIDE_F32 || (d != 64 && d != 128)) return kPortable;
+  if (dtype == FLIDE_F32 || (d != 64 && d != 128)) return {kPortable, 16, 0};
   const long long rows = (T * G + R - 1) / (R > 0 ? R : 1);
-  if (rows <= 16) return kMma16;
-  if (rows <= 32 || dtype != FLIDE_BF16 || d != 128 || 128 % G) return kMma32;
-  return rows <= 128 || R > 2048 ? kWide128 : kWide256;  // 256 rows leave less room for the lists
-}
-
-struct Shape {
-  int tile_rows, slot_rows, halves;
-};
-Shape shape_of(Variant v) {
-  switch (v) {
-    case kMma32: return {32, 32, 0};
-    case kWide128: return {128, 256, 1};
-    case kWide256: return {256, 256, 0};
-    default: return {16, 16, 0};
-  }
+  if (rows <= 16) return {kMma, 16, 0};
+  if (d != 128 || 128 % G) return {kMma, 32, 0};
+  if (rows <= 32 && G <= 32) return {kWide, 32, 3};
+  if (rows <= 64 && G <= 64) return {kWide, 64, 2};
+  // 256 rows leave less room for the requests' lists
+  if (rows <= 128 || R > 2048 || dtype == FLIDE_E4M3) return {kWide, 128, 1};
+  return {kWide, 256, 0};
 }
 
 constexpr int kMaxWorkers = 640;  // of any variant: what the workspace allows for
@@ -750,17 +747,17 @@ struct DraftSpace {
 };
 
 // Bytes of the workspace's parts: a slot for every worker and item.
-DraftSpace draft_space(long long R, long long T, int Hkv, int G, int d, Variant v) {
-  const Shape sh = shape_of(v);
-  const long long slots = (v >= kWide128 ? kWideWorkers : kMaxWorkers) +
-                          ((T * G + sh.tile_rows - 1) / sh.tile_rows + R) * Hkv;
+DraftSpace draft_space(long long R, long long T, int Hkv, int G, int d, const Variant &v) {
+  const long long slots = (v.kernel == kWide ? kWideWorkers : kMaxWorkers) +
+                          ((T * G + v.tile_rows - 1) / v.tile_rows + R) * Hkv;
+  const long long rows = (slots << v.parts_log) * v.tile_rows;
   auto up = [](size_t n) { return (n + 255) / 256 * 256; };
   DraftSpace s;
   s.unit0 = 0;
   s.item0 = up((R + 1) * sizeof(long long));
   s.ml = s.item0 + up((R + 1) * sizeof(long long));
-  s.o = s.ml + up((size_t)slots * sh.slot_rows * 2 * sizeof(float));
-  s.total = s.o + up((size_t)slots * sh.slot_rows * d * sizeof(float));
+  s.o = s.ml + up((size_t)rows * 2 * sizeof(float));
+  s.total = s.o + up((size_t)rows * d * sizeof(float));
   return s;
 }
 
@@ -827,7 +824,6 @@ int draft_attn(const void *q, const void *k, const void *v, const void *past_k, 
   if (idx->R > kMaxListR || (long long)idx->T * Hq > 0x3fffffffLL) return FLIDE_ERR_CAPACITY;
   if (idx->R == 0 || idx->T == 0) return FLIDE_OK;
   const Variant var = variant_of(idx->R, idx->T, Hq / Hkv, d, dtype);
-  const Shape sh = shape_of(var);
   const DraftSpace sp = draft_space(idx->R, idx->T, Hkv, Hq / Hkv, d, var);
   if (workspace_bytes < sp.total) return FLIDE_ERR_CAPACITY;
   int dev = 0, sms = 0;
@@ -849,9 +845,8 @@ int draft_attn(const void *q, const void *k, const void *v, const void *past_k, 
   p.G = Hq / Hkv;
   p.d = d;
   p.scale = scale;
-  p.tile_rows = sh.tile_rows;
-  p.slot_rows = sh.slot_rows;
-  p.halves = sh.halves;
+  p.tile_rows = var.tile_rows;
+  p.parts_log = var.parts_log;
   p.out = out;
   p.lse = lse;
   p.unit0 = reinterpret_cast<long long *>(ws + sp.unit0);
@@ -859,25 +854,23 @@ int draft_attn(const void *q, const void *k, const void *v, const void *past_k, 
   p.part_ml = reinterpret_cast<float *>(ws + sp.ml);
   p.part_o = reinterpret_cast<float *>(ws + sp.o);
   int rc;
-  switch (var) {
-    case kPortable:
-      rc = dtype == FLIDE_F32 ? portable_launch<float>(p, dev, sms, s) : portable_launch<__nv_bfloat16>(p, dev, sms, s);
-      if (rc != FLIDE_OK) return rc;
-      return dtype == FLIDE_F32 ? join_portable_launch<float, float>(p, s)
-                                : join_portable_launch<__nv_bfloat16, __nv_bfloat16>(p, s);
-    case kMma16:
-      rc = dtype == FLIDE_E4M3 ? mma_launch<128, true, 1>(p, dev, sms, s)
-           : d == 128          ? mma_launch<128, false, 1>(p, dev, sms, s)
-                               : mma_launch<64, false, 1>(p, dev, sms, s);
-      break;
-    case kMma32:
-      rc = dtype == FLIDE_E4M3 ? mma_launch<128, true, 2>(p, dev, sms, s)
-           : d == 128          ? mma_launch<128, false, 2>(p, dev, sms, s)
-                               : mma_launch<64, false, 2>(p, dev, sms, s);
-      break;
-    default:
-      p.workers = min(kWideWorkers, sms);
-      rc = draft_wide_launch(p, past_rows, dev, s);
+  if (var.kernel == kPortable) {
+    rc = dtype == FLIDE_F32 ? portable_launch<float>(p, dev, sms, s) : portable_launch<__nv_bfloat16>(p, dev, sms, s);
+    if (rc != FLIDE_OK) return rc;
+    return dtype == FLIDE_F32 ? join_portable_launch<float, float>(p, s)
+                              : join_portable_launch<__nv_bfloat16, __nv_bfloat16>(p, s);
+  }
+  if (var.kernel == kWide) {
+    p.workers = min(kWideWorkers, sms);
+    rc = draft_wide_launch(p, past_rows, dtype == FLIDE_E4M3, dev, s);
+  } else if (var.tile_rows == 16) {
+    rc = dtype == FLIDE_E4M3 ? mma_launch<128, true, 1>(p, dev, sms, s)
+         : d == 128          ? mma_launch<128, false, 1>(p, dev, sms, s)
+                             : mma_launch<64, false, 1>(p, dev, sms, s);
+  } else {
+    rc = dtype == FLIDE_E4M3 ? mma_launch<128, true, 2>(p, dev, sms, s)
+         : d == 128          ? mma_launch<128, false, 2>(p, dev, sms, s)
+                             : mma_launch<64, false, 2>(p, dev, sms, s);
   }
   if (rc != FLIDE_OK) return rc;
   if (dtype == FLIDE_E4M3) return join_launch<uint8_t, 128>(p, s);

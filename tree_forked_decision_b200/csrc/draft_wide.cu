@@ -8,7 +8,11 @@
 //   - 256 rows: each warpgroup has its own 128 rows, both see every key tile;
 //   - 128 rows: both have the same rows and take every second key tile; their
 //     (O, max, sum) are two partials for the join.  One operand's softmax alone
-//     would leave the tensor core and the memory idle half the time.
+//     would leave the tensor core and the memory idle half the time;
+//   - 64 or 32 rows: the operand holds them two or four times, and each copy's
+//     threads take a half or quarter of the tile's keys (their weights for the
+//     others are 0): four or eight partials, and a half or quarter of the softmax
+//     in each thread's chain, which is what bounds a tile.
 // A block (one to an SM) takes its share of the batch's key tiles as runs
 // inside one (request, row tile, kv head) item (draft.cuh); barriers count over
 // the block's life, so the next run's loads are in flight while the last tiles
@@ -16,12 +20,20 @@
 // memory before they are multiplied: their weight is 0, but what stands there
 // may be NaN.
 //
+// e4m3: S and O come from the codes (kind::f8f6f4, exact products).  A weight in
+// e4m3 would be 2^-4 off, so it goes in as two codes, its own and its remainder's:
+// two products at twice the rate.  Scaled by 2^6 (its reference is at most 4 below
+// the row's maximum), a weight is off by 2^-8 of itself or 2^-16 of the row's
+// largest.  (Widening V to half in the softmax warps instead took 124 us where
+// this takes the time in the design notes' table.)
+//
 // 256 rows are bound by the two warpgroups' softmax and the MMA issue (see
 // attn_tc.cu), 128 rows by the history's bytes.  Every wait is bounded (2 s);
 // on expiry the block records FLIDE_ERR_TIMEOUT, waits for its own copies and
 // MMAs, frees TMEM and ends.
 #include <cstddef>
 #include <cuda.h>
+#include <cuda_fp16.h>
 
 #include "draft.cuh"
 #include "launch.cuh"
@@ -36,10 +48,10 @@ constexpr int kBM = 128, kBN = 128;
 constexpr int kWThreads = 320;
 constexpr uint64_t kWaitNs = 2000000000ull;
 
-// Shared memory in 32 KB tiles: Q's operands, then the stages of K and of V; the
-// barriers and the block's lists (16 bytes a request) after them.  128 rows leave
-// room for a third stage while the lists are short.
-constexpr int kMaxStages = 3;
+// Shared memory: Q's operands, the stages of K and of V (32 KB a tile, 16 KB of
+// codes), then the barriers and the block's lists (16 bytes a request).  As many
+// stages as fit.
+constexpr int kMaxStages = 4;
 constexpr int kSmemMax = 232448;
 enum {
   bQ = 0,
@@ -60,8 +72,16 @@ struct Misc {
   int abort, stop;
   long long part[32];
 };
-constexpr size_t wide_smem(int halves, int stages, int R) {
-  return (size_t)(halves + 2 * stages) * 32768 + 256 + sizeof(Misc) + (size_t)(R + 1) * 16 + 1024;
+constexpr size_t wide_smem(bool f8, int halves, int stages, int R) {
+  return (size_t)(halves + 2 * stages) * (f8 ? 16384 : 32768) + 256 + sizeof(Misc) +
+         (size_t)(R + 1) * 16 + 1024;
+}
+
+// 32 bytes at once (a whole sector; rows of a warp's lanes lie 512 bytes apart)
+__device__ __forceinline__ void st_sector(float *p, const uint32_t *v) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
 }
 
 // A key tile's stage and how often the ring has been round (its parity is that of
@@ -81,14 +101,17 @@ struct WideMaps {
   CUtensorMap q, k, v;
 };
 
-template <int kHalves>
+template <int kHalves, int kRep, bool F8>
 __global__ void __launch_bounds__(kWThreads, 1)
 draft_part_wide(const __grid_constant__ WideMaps maps, const DraftParams p, int mtok, int box_rows,
                 int stages) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   const uint32_t sb = smem_u32(smem);
-  const int s_k = kHalves * 32768, s_v = s_k + stages * 32768, s_bar = s_v + stages * 32768;
+  static_assert(kHalves == 1 || kRep == 1, "copies are of a tile of one operand");
+  constexpr int kCopy = kBM / kRep, kCols = kBN / kRep;  // rows of a copy, keys of its threads
+  constexpr int kTile = F8 ? 16384 : 32768, kSlabs = F8 ? 1 : 2;  // bytes; 128-byte slabs of a row
+  const int s_k = kHalves * kTile, s_v = s_k + stages * kTile, s_bar = s_v + stages * kTile;
   Misc &ms = *reinterpret_cast<Misc *>(smem + s_bar + 256);
   volatile int *abort_flag = &ms.abort;
   long long *unit0 = reinterpret_cast<long long *>(&ms + 1), *item0 = unit0 + (p.x.R + 1);
@@ -144,11 +167,12 @@ draft_part_wide(const __grid_constant__ WideMaps maps, const DraftParams p, int 
       u += draft_run(p, unit0, item0, u, u_end, w, run);
       if (rc > 0 && !(ok = wait(bQFree, (rc - 1) & 1))) break;
       if (lane == 0) {
-        mbar_arrive_expect_tx(bar(bQ), kHalves * 32768);
+        mbar_arrive_expect_tx(bar(bQ), kHalves * kTile);
         for (int h = 0; h < kHalves; ++h)
-          for (int s = 0; s < 2; ++s)
-            tma_load_3d(sb + h * 32768 + s * 16384, &maps.q, bar(bQ), 64 * s, run.hk * p.G,
-                        run.t0 + (run.tile * kHalves + h) * mtok);
+          for (int s = 0; s < kSlabs; ++s)
+            for (int c = 0; c < kRep; ++c)
+              tma_load_3d(sb + h * kTile + s * 16384 + c * kCopy * 128, &maps.q, bar(bQ), 64 * s, run.hk * p.G,
+                          run.t0 + (run.tile * kHalves + h) * mtok);
       }
       // boxes that hold history rows, a lane each (the rest of the last tile keeps
       // what the stage held, and is masked); looked up a tile ahead
@@ -165,22 +189,22 @@ draft_part_wide(const __grid_constant__ WideMaps maps, const DraftParams p, int 
         const long long row = next;
         next = row_at(k0 + kBN);
         if (kt >= stages && !(ok = wait(bKFree + st, turn))) break;
-        if (lane == 0) mbar_arrive_expect_tx(bar(bK + st), used * box_rows * 256);
+        if (lane == 0) mbar_arrive_expect_tx(bar(bK + st), used * box_rows * 128 * kSlabs);
         __syncwarp();
         if (lane < used)
-          for (int s = 0; s < 2; ++s)
-            tma_load_3d(sb + s_k + st * 32768 + s * 16384 + lane * box_rows * 128, &maps.k, bar(bK + st),
+          for (int s = 0; s < kSlabs; ++s)
+            tma_load_3d(sb + s_k + st * kTile + s * 16384 + lane * box_rows * 128, &maps.k, bar(bK + st),
                         64 * s, run.hk, (int)row);
         if (kt >= stages && !(ok = wait(bVFree + st, turn))) {
           // K of this tile is in flight, V is not
           mbar_wait(bar(bK + st), ring.turn, abort_flag, kWaitNs, false);
           break;
         }
-        if (lane == 0) mbar_arrive_expect_tx(bar(bV + st), used * box_rows * 256);
+        if (lane == 0) mbar_arrive_expect_tx(bar(bV + st), used * box_rows * 128 * kSlabs);
         __syncwarp();
         if (lane < used)
-          for (int s = 0; s < 2; ++s)
-            tma_load_3d(sb + s_v + st * 32768 + s * 16384 + lane * box_rows * 128, &maps.v, bar(bV + st),
+          for (int s = 0; s < kSlabs; ++s)
+            tma_load_3d(sb + s_v + st * kTile + s * 16384 + lane * box_rows * 128, &maps.v, bar(bV + st),
                         64 * s, run.hk, (int)row);
         ring.next(stages);
       }
@@ -194,7 +218,8 @@ draft_part_wide(const __grid_constant__ WideMaps maps, const DraftParams p, int 
   } else if (warp == 9) {
     // -------------------------------------------------------------- MMA
     if (lane == 0) {
-      constexpr uint32_t id_s = idesc_bf16(kBM, kBN, false), id_pv = idesc_bf16(kBM, 128, true);
+      constexpr uint32_t id_s = F8 ? idesc_e4m3(kBM, kBN, false) : idesc_bf16(kBM, kBN, false);
+      constexpr uint32_t id_pv = F8 ? idesc_e4m3(kBM, 128, true) : idesc_bf16(kBM, 128, true);
       auto wait = [&](int b, uint32_t parity) { return mbar_wait(bar(b), parity, abort_flag, kWaitNs); };
       bool ok = true;
       int rc = 0;
@@ -208,12 +233,14 @@ draft_part_wide(const __grid_constant__ WideMaps maps, const DraftParams p, int 
         auto scores = [&](int h) -> bool {
           if ((kHalves == 1 || h == 0) && !wait(bK + rs.st, rs.turn)) return false;
           tc_fence_after();
-          const uint32_t k_at = sb + s_k + rs.st * 32768;
+          const uint32_t k_at = sb + s_k + rs.st * kTile;
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {
+          for (int kk = 0; kk < 4 * kSlabs; ++kk) {  // 32 bytes of a row each
             const uint32_t o = (kk >> 2) * 16384 + (kk & 3) * 32;
-            mma_bf16(tmem + h * 256, sdesc_sw128(sb + (kHalves == 2 ? h : 0) * 32768 + o, 16, 1024),
-                     sdesc_sw128(k_at + o, 16, 1024), id_s, kk > 0 ? 1u : 0u);
+            const uint64_t a = sdesc_sw128(sb + (kHalves == 2 ? h : 0) * kTile + o, 16, 1024);
+            const uint64_t b = sdesc_sw128(k_at + o, 16, 1024);
+            if (F8) mma_f8(tmem + h * 256, a, b, id_s, kk > 0 ? 1u : 0u);
+            else mma_bf16(tmem + h * 256, a, b, id_s, kk > 0 ? 1u : 0u);
           }
           mma_commit(bar(bS + h));
           if (kHalves == 1 || h == 1) {
@@ -229,11 +256,15 @@ draft_part_wide(const __grid_constant__ WideMaps maps, const DraftParams p, int 
           if ((kHalves == 1 || h == 0) && !wait(bV + rv.st, rv.turn)) return false;
           if (i < 2 && rc > 0 && !wait(bOFree + h, (rc - 1) & 1)) return false;
           tc_fence_after();
-          const uint32_t v_at = sb + s_v + rv.st * 32768;
+          const uint32_t v_at = sb + s_v + rv.st * kTile;
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            mma_bf16_ts(tmem + h * 256 + 128, tmem + h * 256 + kk * 8, sdesc_sw128(v_at + kk * 2048, 16384, 1024),
-                        id_pv, (i >= 2 || kk > 0) ? 1u : 0u);
+          for (int kk = 0; kk < 8; ++kk) {
+            // bf16: 16 keys each; codes: 32 keys each, the weights and then their remainders
+            const uint32_t acc = (i >= 2 || kk > 0) ? 1u : 0u;
+            const uint64_t b = sdesc_sw128(v_at + (F8 ? (kk & 3) * 4096 : kk * 2048), 16384, 1024);
+            if (F8) mma_f8_ts(tmem + h * 256 + 128, tmem + h * 256 + kk * 8, b, id_pv, acc);
+            else mma_bf16_ts(tmem + h * 256 + 128, tmem + h * 256 + kk * 8, b, id_pv, acc);
+          }
           if (kHalves == 1 || h == 1) {
             mma_commit(bar(bVFree + rv.st));
             rv.next(stages);
@@ -259,12 +290,14 @@ draft_part_wide(const __grid_constant__ WideMaps maps, const DraftParams p, int 
   } else {
     // -------------------------------------------------------------- softmax
     const int h = warp >> 2, row = (warp & 3) * 32 + lane;  // S buffer; its row = TMEM lane
+    const int col0 = (warp & 3) * 32 / kCopy * kCols;       // the first key of this warp's copy
     const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t t_s = tl + h * 256, t_o = tl + h * 256 + 128;
-    const float c = p.scale * kLog2eD;
+    const float c = p.scale * kLog2eD * (F8 ? p.descale[0] * p.descale[1] : 1.f);
     auto wait = [&](int b, uint32_t parity) {
       return __all_sync(0xffffffffu, mbar_wait(bar(b), parity, abort_flag, kWaitNs));
     };
+    constexpr float kShift = F8 ? 6.f : 0.f;  // weights carry 2^kShift
     bool ok = true;
     uint32_t ns = 0;  // score tiles taken, mod 2
     int rc = 0, kt0 = 0;
@@ -278,20 +311,22 @@ draft_part_wide(const __grid_constant__ WideMaps maps, const DraftParams p, int 
         if (!(ok = wait(bS + h, ns))) break;
         ns ^= 1;
         tc_fence_after();
-        uint32_t sr[128];
-        tmem_ld128(t_s, sr);
+        uint32_t sr[kCols];
+        if constexpr (kCols == 128) tmem_ld128(t_s, sr);
+        else if constexpr (kCols == 64) tmem_ld64(t_s + col0, sr);
+        else tmem_ld32(t_s + col0, sr);
         if (left < kBN) {
 #pragma unroll
-          for (int j = 0; j < kBN; ++j)
-            if (j >= left) sr[j] = 0xff800000u;  // -inf
+          for (int j = 0; j < kCols; ++j)
+            if (col0 + j >= left) sr[j] = 0xff800000u;  // -inf
           if (opens(i)) {
             // V rows behind the history: zero, whatever was there
             const int st = (kt0 + kt) % stages;
             if (!(ok = wait(bV + st, ((kt0 + kt) / stages) & 1))) break;
             for (int e = left * 8 + (tid & 127); e < kBN * 8; e += 128) {
-              uint4 *z = reinterpret_cast<uint4 *>(smem + s_v + st * 32768) + e;
+              uint4 *z = reinterpret_cast<uint4 *>(smem + s_v + st * kTile) + e;
               z[0] = make_uint4(0u, 0u, 0u, 0u);
-              z[1024] = make_uint4(0u, 0u, 0u, 0u);  // the upper 64 elements
+              if (!F8) z[1024] = make_uint4(0u, 0u, 0u, 0u);  // the upper 64 elements
             }
             fence_proxy_async_smem();
           }
@@ -301,16 +336,17 @@ draft_part_wide(const __grid_constant__ WideMaps maps, const DraftParams p, int 
 #pragma unroll
         for (int k = 0; k < 8; ++k) mx[k] = __uint_as_float(sr[k]);
 #pragma unroll
-        for (int j = 8; j < kBN; j += 16) {
+        for (int j = 8; j < kCols; j += 8) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            mx[k] = fmax3f(mx[k], __uint_as_float(sr[j + 2 * k < kBN ? j + 2 * k : 0]),
-                           __uint_as_float(sr[j + 2 * k + 1 < kBN ? j + 2 * k + 1 : 0]));
+          for (int k = 0; k < 8; k += 2) {
+            const int o = (j / 8 & 1) * 4 + k / 2;
+            mx[o] = fmax3f(mx[o], __uint_as_float(sr[j + k]), __uint_as_float(sr[j + k + 1]));
+          }
         }
         const float mt = c * fmaxf(fmax3f(mx[0], mx[1], mx[2]), fmax3f(fmax3f(mx[3], mx[4], mx[5]), mx[6], mx[7]));
         if (i < 2) {
           m = mt;
-        } else if (__any_sync(0xffffffffu, mt > m + 8.f)) {
+        } else if (__any_sync(0xffffffffu, mt > m + (F8 ? 2.f : 8.f))) {
           // this buffer's last PV is complete: it was issued before this S
           const float mn = fmaxf(m, mt), f = mn == -INFINITY ? 1.f : exp2f(m - mn);
 #pragma unroll 1
@@ -324,16 +360,45 @@ draft_part_wide(const __grid_constant__ WideMaps maps, const DraftParams p, int 
           l *= f;
           m = mn;
         }
-        const float ref = m == -INFINITY ? 0.f : m;
+        const float ref = (m == -INFINITY ? 0.f : m) - kShift;
         const uint64_t c2 = f2_pack(c, c), nm2 = f2_pack(-ref, -ref);
         uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
+        uint32_t rem[F8 ? kCols / 4 : 1];
+        constexpr int kWords = F8 ? kCols / 4 : kCols / 2;  // of packed weights (codes: and as many of remainders)
+        if constexpr (F8) {
 #pragma unroll
-        for (int j = 0; j < kBN; j += 2) {
-          float x0, x1;
-          f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[j]), __uint_as_float(sr[j + 1])), c2, nm2), x0, x1);
-          const float e0 = ex2_approx(x0), e1 = ex2_approx(x1);
-          acc[(j >> 1) & 3] = f2_add(acc[(j >> 1) & 3], f2_pack(e0, e1));
-          sr[j >> 1] = pack_bf16x2(e0, e1);
+          for (int j = 0; j < kCols; j += 4) {
+            float e[4];
+#pragma unroll
+            for (int k = 0; k < 4; k += 2) {
+              f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[j + k]), __uint_as_float(sr[j + k + 1])), c2, nm2), e[k],
+                        e[k + 1]);
+              e[k] = ex2_approx(e[k]);
+              e[k + 1] = ex2_approx(e[k + 1]);
+              acc[(j + k) / 2 & 3] = f2_add(acc[(j + k) / 2 & 3], f2_pack(e[k], e[k + 1]));
+            }
+            const uint32_t code = pack_e4m3x4(e[0], e[1], e[2], e[3]);
+#pragma unroll
+            for (int k = 0; k < 4; k += 2) {
+              const uint32_t pair = e4m3x2_to_half2(k ? code >> 16 : code);
+              const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&pair));
+              e[k] -= f.x;
+              e[k + 1] -= f.y;
+            }
+            // words of codes take the places of scores that were read: j / 4 < j
+            const uint32_t rest = pack_e4m3x4(e[0], e[1], e[2], e[3]);
+            sr[j / 4] = code;
+            rem[j / 4] = rest;
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < kCols; j += 2) {
+            float x0, x1;
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[j]), __uint_as_float(sr[j + 1])), c2, nm2), x0, x1);
+            const float e0 = ex2_approx(x0), e1 = ex2_approx(x1);
+            acc[(j >> 1) & 3] = f2_add(acc[(j >> 1) & 3], f2_pack(e0, e1));
+            sr[j >> 1] = pack_bf16x2(e0, e1);
+          }
         }
         {
           float a0, a1, b0, b1;
@@ -341,7 +406,19 @@ draft_part_wide(const __grid_constant__ WideMaps maps, const DraftParams p, int 
           f2_unpack(f2_add(acc[2], acc[3]), b0, b1);
           l += (a0 + a1) + (b0 + b1);
         }
-        tmem_st64(t_s, *reinterpret_cast<uint32_t(*)[64]>(sr));
+        if constexpr (kCols == 128 && !F8) {
+          tmem_st64(t_s, *reinterpret_cast<uint32_t(*)[64]>(sr));
+        } else {  // the other copies' keys: weight 0
+          uint32_t all[64];
+          const int mine = col0 / kCols;
+#pragma unroll
+          for (int j = 0; j < 64; ++j) {
+            const int k = F8 ? j % 32 : j;
+            const uint32_t v = F8 && j >= 32 ? rem[k % kWords] : sr[k % kWords];
+            all[j] = k / kWords == mine ? v : 0u;
+          }
+          tmem_st64(t_s, all);
+        }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(bP + h));
@@ -349,6 +426,7 @@ draft_part_wide(const __grid_constant__ WideMaps maps, const DraftParams p, int 
       if (!ok || !(ok = wait(bO, rc & 1))) break;
       tc_fence_after();
       const size_t at = (size_t)run.slot * 256 + h * 128 + row;
+      const bool real = run.tile * p.tile_rows + (kHalves == 2 ? h * kBM : 0) + row % kCopy < run.tokens * p.G;
       if (h < steps) {
         float *o = p.part_o + at * 128;
 #pragma unroll 1
@@ -356,11 +434,11 @@ draft_part_wide(const __grid_constant__ WideMaps maps, const DraftParams p, int 
           uint32_t r32[32];
           tmem_ld32(t_o + 32 * c4, r32);
 #pragma unroll
-          for (int j = 0; j < 32; j += 4)
-            *reinterpret_cast<uint4 *>(o + 32 * c4 + j) = make_uint4(r32[j], r32[j + 1], r32[j + 2], r32[j + 3]);
+          for (int j = 0; j < 32; j += 8)
+            if (real) st_sector(o + 32 * c4 + j, r32 + j);
         }
       }
-      *reinterpret_cast<float2 *>(p.part_ml + 2 * at) = make_float2(m, l);
+      *reinterpret_cast<float2 *>(p.part_ml + 2 * at) = make_float2(m - kShift, l);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(bOFree + h));
@@ -396,48 +474,62 @@ EncodeFn encode_tiled() {
   return fn;
 }
 
-// [rows, heads, 128] bf16 as (element, head, row); box of 64 elements (128
-// swizzled bytes) x box_heads x box_rows
-bool wide_map(CUtensorMap *m, const void *base, int heads, long rows, int box_heads, int box_rows) {
+// [rows, heads, 128] bf16 or codes as (element, head, row); box of 128 swizzled
+// bytes x box_heads x box_rows
+bool wide_map(CUtensorMap *m, const void *base, int esz, int heads, long rows, int box_heads, int box_rows) {
   EncodeFn enc = encode_tiled();
   if (!enc || rows <= 0) return false;
   const cuuint64_t dims[3] = {128, (cuuint64_t)heads, (cuuint64_t)rows};
-  const cuuint64_t strides[2] = {256, (cuuint64_t)heads * 256};
-  const cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_rows}, step[3] = {1, 1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, step,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  const cuuint64_t strides[2] = {(cuuint64_t)128 * esz, (cuuint64_t)heads * 128 * esz};
+  const cuuint32_t box[3] = {(cuuint32_t)(128 / esz), (cuuint32_t)box_heads, (cuuint32_t)box_rows};
+  const cuuint32_t step[3] = {1, 1, 1};
+  return enc(m, esz == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+             const_cast<void *>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int kHalves>
+template <int kHalves, int kRep, bool F8>
 int wide_launch(const DraftParams &p, const WideMaps &maps, int mtok, int box_rows, int dev, cudaStream_t s) {
-  int stages = kHalves == 2 ? 2 : kMaxStages;
-  while (wide_smem(kHalves, stages, p.x.R) > kSmemMax) --stages;
+  int stages = kMaxStages;
+  while (wide_smem(F8, kHalves, stages, p.x.R) > kSmemMax) --stages;
   if (stages < 2) return FLIDE_ERR_CAPACITY;
-  const size_t smem = wide_smem(kHalves, stages, p.x.R);
-  if (!allow_smem<draft_part_wide<kHalves>>(dev)) return FLIDE_ERR_CUDA;
-  draft_part_wide<kHalves><<<p.workers, kWThreads, smem, s>>>(maps, p, mtok, box_rows, stages);
+  const size_t smem = wide_smem(F8, kHalves, stages, p.x.R);
+  if (!allow_smem<draft_part_wide<kHalves, kRep, F8>>(dev)) return FLIDE_ERR_CUDA;
+  draft_part_wide<kHalves, kRep, F8><<<p.workers, kWThreads, smem, s>>>(maps, p, mtok, box_rows, stages);
   FLIDE_LAUNCH_CHECK();
   return FLIDE_OK;
 }
 
 }  // namespace
 
-int draft_wide_launch(const DraftParams &p0, int past_rows, int dev, cudaStream_t s) {
+int draft_wide_launch(const DraftParams &p0, int past_rows, bool f8, int dev, cudaStream_t s) {
   DraftParams p = p0;
   p.unit = kBN;
-  const int mtok = kBM / p.G;
+  const int rep = p.tile_rows < kBM ? kBM / p.tile_rows : 1;
+  const int mtok = kBM / rep / p.G, esz = f8 ? 1 : 2;
   // rows of a box: a tile's, or the most that divides both it and a block
   int box_rows = kBN;
   if (p.hist.block_table)
     while (p.hist.block_rows % box_rows) box_rows /= 2;
   WideMaps maps;
   const bool past = p.past_k != nullptr && past_rows > 0;  // without: no unit, no load
-  if (!wide_map(&maps.q, p.q, p.Hq, p.x.T, p.G, mtok) ||
-      !wide_map(&maps.k, past ? p.past_k : p.k, p.Hkv, past ? past_rows : p.x.T, 1, box_rows) ||
-      !wide_map(&maps.v, past ? p.past_v : p.v, p.Hkv, past ? past_rows : p.x.T, 1, box_rows))
+  if (!wide_map(&maps.q, p.q, esz, p.Hq, p.x.T, p.G, mtok) ||
+      !wide_map(&maps.k, past ? p.past_k : p.k, esz, p.Hkv, past ? past_rows : p.x.T, 1, box_rows) ||
+      !wide_map(&maps.v, past ? p.past_v : p.v, esz, p.Hkv, past ? past_rows : p.x.T, 1, box_rows))
     return FLIDE_ERR_CUDA;
-  return p.halves ? wide_launch<1>(p, maps, mtok, box_rows, dev, s) : wide_launch<2>(p, maps, mtok, box_rows, dev, s);
+  if (p.tile_rows == 2 * kBM) return wide_launch<2, 1, false>(p, maps, mtok, box_rows, dev, s);
+  switch (rep) {
+    case 4:
+      return f8 ? wide_launch<1, 4, true>(p, maps, mtok, box_rows, dev, s)
+                : wide_launch<1, 4, false>(p, maps, mtok, box_rows, dev, s);
+    case 2:
+      return f8 ? wide_launch<1, 2, true>(p, maps, mtok, box_rows, dev, s)
+                : wide_launch<1, 2, false>(p, maps, mtok, box_rows, dev, s);
+    default:
+      return f8 ? wide_launch<1, 1, true>(p, maps, mtok, box_rows, dev, s)
+                : wide_launch<1, 1, false>(p, maps, mtok, box_rows, dev, s);
+  }
 }
 
 }  // namespace flide
