@@ -571,7 +571,7 @@ size_t flide_draft_attn_workspace_bytes(int32_t R, int32_t T, int32_t Hq, int32_
  * relative error <= 2^-8, absolute <= 2^-16 of the row's largest weight); their
  * sum is not.
  * Host errors: FLIDE_ERR_SHAPE, FLIDE_ERR_CAPACITY (workspace too small, more
- * than 4096 requests, T * Hq past 2^30), FLIDE_ERR_CUDA; device errors as
+ * than 2048 requests, T * Hq past 2^30), FLIDE_ERR_CUDA; device errors as
  * flide_fork_attn. */
 int flide_draft_attn(const void *q, const void *k, const void *v, const void *past_k,
                      const void *past_v, int32_t past_rows, const flide_tree_index *idx, int32_t Hq,

@@ -1,5 +1,8 @@
 // draft.cuh -- what the draft attention kernels share: their parameters and the
 // division of a batch's (request, row tile, kv head, key unit) list over workers.
+// A run of a worker inside one item costs what `extra` units cost (its queries,
+// its partial's store, an emptied pipeline), so each item begins with that many
+// units without keys: a worker with many short histories gets fewer keys.
 #pragma once
 
 #include "common.cuh"
@@ -8,6 +11,14 @@
 namespace flide {
 
 constexpr float kLog2eD = 1.4426950408889634f;
+
+// A request in the work list: its first unit and item, the units of one item, its
+// stream tokens from t0, its history rows and (history_rows) their base.  Entry R
+// holds the totals.
+struct __align__(16) DraftReq {
+  long long unit0;
+  int item0, units, t0, tokens, hist, base;
+};
 
 struct DraftParams {
   flide_tree_index x;
@@ -18,11 +29,11 @@ struct DraftParams {
   float scale;
   // row tiles of tile_rows query rows (tokens x heads of the group), key units of
   // `unit` history rows; a run's slot holds 2^parts_log partials of a tile's rows
-  int workers, tile_rows, parts_log, unit;
+  int workers, tile_rows, parts_log, unit, extra;
   void *out;
   float *lse;
-  // workspace: prefix sums of units and items, partial rows and their (max, sum)
-  long long *unit0, *item0;
+  // workspace: the work list, partial rows and their (max, sum)
+  DraftReq *list;
   float *part_o, *part_ml;
 };
 
@@ -52,56 +63,94 @@ __device__ __forceinline__ int worker_of(long long U, int W, long long u) {
   return w;
 }
 
+// The batch's work list, in shared memory and, for the join kernel, in the
+// workspace.  part: 64 entries.  Ends with a barrier.
+__device__ __forceinline__ void draft_list(const DraftParams &p, DraftReq *list, long long *part) {
+  const flide_tree_index &x = p.x;
+  const int R = x.R, nt = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (R + nt - 1) / nt, lo = min(R, tid * per), hi = min(R, lo + per);
+  long long units = 0, items = 0;
+  for (int r = lo; r < hi; ++r) {
+    DraftReq q;
+    long long base;
+    q.hist = history_rows(x, p.hist, r, blockIdx.x == 0, &base);
+    q.base = (int)base;
+    q.tokens = request_tokens(x, r, &q.t0);
+    q.unit0 = units;
+    q.item0 = (int)items;
+    q.units = q.hist > 0 ? (q.hist + p.unit - 1) / p.unit + p.extra : 0;
+    const long long n = (long long)tiles_of(p, q.tokens) * p.Hkv;
+    items += n;
+    units += n * q.units;
+    list[r] = q;
+  }
+  long long iu = units, ii = items;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long yu = __shfl_up_sync(0xffffffffu, iu, o), yi = __shfl_up_sync(0xffffffffu, ii, o);
+    if (lane >= o) {
+      iu += yu;
+      ii += yi;
+    }
+  }
+  if (lane == 31) {
+    part[warp] = iu;
+    part[32 + warp] = ii;
+  }
+  __syncthreads();
+  long long bu = iu - units, bi = ii - items;
+  for (int w = 0; w < warp; ++w) {
+    bu += part[w];
+    bi += part[32 + w];
+  }
+  for (int r = lo; r < hi; ++r) {
+    list[r].unit0 += bu;
+    list[r].item0 += (int)bi;
+    if (blockIdx.x == 0) p.list[r] = list[r];
+  }
+  if (tid == nt - 1) {
+    const DraftReq end{bu + units, (int)(bi + items), 0, 0, 0, 0, 0};
+    list[R] = end;
+    if (blockIdx.x == 0) p.list[R] = end;
+  }
+  __syncthreads();
+}
+
 // A worker's run: history rows [k0, k1) of one item (row tile `tile`, kv head
 // hk of a request of `tokens` tokens from t0); base: history_rows.
 struct Run {
-  int tile, hk, t0, tokens, k0, k1;
-  long long base, slot;
+  int tile, hk, t0, tokens, k0, k1, base;
+  long long slot;
 };
 
-// Prefix sums over the requests of their units and items, in
-// shared memory, and for the join kernel in the workspace.
-__device__ __forceinline__ void draft_lists(const DraftParams &p, long long *unit0, long long *item0,
-                                            long long *part) {
-  const flide_tree_index &x = p.x;
-  const int unit = p.unit;
-  request_prefix(x.R, [&](int r) -> long long {
-    int t0;
-    return (long long)tiles_of(p, request_tokens(x, r, &t0)) * p.Hkv;
-  }, item0, part);
-  request_prefix(x.R, [&](int r) -> long long {
-    long long base;
-    const long long n = history_rows(x, p.hist, r, blockIdx.x == 0, &base);
-    return (item0[r + 1] - item0[r]) * ((n + unit - 1) / unit);
-  }, unit0, part);
-  if (blockIdx.x == 0)
-    for (int r = threadIdx.x; r <= x.R; r += blockDim.x) {
-      p.unit0[r] = unit0[r];
-      p.item0[r] = item0[r];
+// The next run of worker w from unit u on, which moves past it; false at the end.
+__device__ __forceinline__ bool draft_run(const DraftParams &p, const DraftReq *list, long long &u,
+                                          long long u_end, int w, Run &run) {
+  while (u < u_end) {
+    int lo = 0, hi = p.x.R;  // the request with unit0 <= u < the next one's
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (list[mid + 1].unit0 > u) hi = mid; else lo = mid + 1;
     }
+    const DraftReq q = list[lo];
+    const long long at = u - q.unit0;
+    const int li = (int)(at / q.units), c0 = (int)(at - (long long)li * q.units);
+    const int c1 = (int)min((long long)q.units, c0 + (u_end - u));
+    u += c1 - c0;
+    run.tile = li / p.Hkv;
+    run.hk = li - run.tile * p.Hkv;
+    run.t0 = q.t0;
+    run.tokens = q.tokens;
+    run.base = q.base;
+    run.k0 = max(c0 - p.extra, 0) * p.unit;
+    run.k1 = min(q.hist, (c1 - p.extra) * p.unit);
+    run.slot = (long long)w + q.item0 + li;
+    if (run.k1 > run.k0) return true;
+  }
+  return false;
 }
 
-// The run that starts at unit u of worker w; returns its units.
-__device__ __forceinline__ int draft_run(const DraftParams &p, const long long *unit0,
-                                         const long long *item0, long long u, long long u_end,
-                                         int w, Run &run) {
-  const int unit = p.unit;
-  const int r = request_of(unit0, p.x.R, u);
-  run.tokens = request_tokens(p.x, r, &run.t0);
-  const int n = history_rows(p.x, p.hist, r, false, &run.base);
-  const int units = (n + unit - 1) / unit;
-  const long long li = (u - unit0[r]) / units;
-  const int c0 = (int)(u - unit0[r] - li * units);
-  const int c1 = (int)min((long long)units, c0 + (u_end - u));
-  run.tile = (int)(li / p.Hkv);
-  run.hk = (int)(li % p.Hkv);
-  run.k0 = c0 * unit;
-  run.k1 = min(n, c1 * unit);
-  run.slot = w + item0[r] + li;
-  return c1 - c0;
-}
-
-// draft_wide.cu: tiles of 32, 64, 128 (bf16, e4m3) or 256 rows (bf16) on tcgen05, d == 128
-int draft_wide_launch(const DraftParams &p, int past_rows, bool f8, int dev, cudaStream_t s);
+// draft_wide.cu (sets p's unit and extra): tiles of 32, 64, 128 (bf16, e4m3) or 256 rows (bf16) on tcgen05, d == 128
+int draft_wide_launch(DraftParams &p, int past_rows, bool f8, int dev, cudaStream_t s);
 
 }  // namespace flide

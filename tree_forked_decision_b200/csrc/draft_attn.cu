@@ -51,16 +51,16 @@ constexpr int kPKeys = 32; // keys of a unit
 template <typename T>
 __global__ void __launch_bounds__(kPT) draft_part_portable(const DraftParams p) {
   extern __shared__ float smem[];
-  __shared__ long long part[32];
+  __shared__ long long part[64];
   const flide_tree_index &x = p.x;
   if (failed(x.status)) return;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int d = p.d, ld = d + 4, R = x.R;
-  long long *unit0 = reinterpret_cast<long long *>(smem), *item0 = unit0 + (R + 1);
-  float *sq = smem + 4 * (R + 1) + (4 - (4 * (R + 1)) % 4) % 4, *sk = sq + kPRows * ld, *sv = sk + kPKeys * ld;
+  DraftReq *list = reinterpret_cast<DraftReq *>(smem);
+  float *sq = smem + 8 * (R + 1), *sk = sq + kPRows * ld, *sv = sk + kPKeys * ld;
   float *sp = sv + kPKeys * ld;
-  draft_lists(p, unit0, item0, part);
-  const long long U = unit0[R];
+  draft_list(p, list, part);
+  const long long U = list[R].unit0;
   const int w = blockIdx.x, W = workers_of(U, p.workers);
   if (w >= W) return;
   long long u = worker_start(U, W, w);
@@ -69,9 +69,8 @@ __global__ void __launch_bounds__(kPT) draft_part_portable(const DraftParams p) 
           *Vp = static_cast<const T *>(p.past_v);
   const float qk_scale = p.scale * kLog2eD * (p.descale ? p.descale[0] * p.descale[1] : 1.f);
   const int nd = d / 32;
-  while (u < u_end) {
-    Run run;
-    u += draft_run(p, unit0, item0, u, u_end, w, run);
+  Run run;
+  while (draft_run(p, list, u, u_end, w, run)) {
     __syncthreads();
     for (int e = tid; e < kPRows * d; e += kPT) {
       const int row = e / d, i = e - row * d, g = run.tile * kPRows + row;
@@ -192,18 +191,18 @@ draft_part_mma(const DraftParams p) {
   using S = MmaShape<D, F8, kMT>;
   constexpr int kMW = S::kMW, kRows = S::kRows;
   extern __shared__ float smem[];
-  __shared__ long long part[32];
+  __shared__ long long part[64];
   __shared__ uint4 qfrag[kMT * S::kSteps * 32];
   const flide_tree_index &x = p.x;
   asm volatile("griddepcontrol.launch_dependents;");
   if (failed(x.status)) return;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
   const int R = x.R;
-  // O [warp][rows][D], then max and sum [warp][rows]; the prefix arrays after them
+  // O [warp][rows][D], then max and sum [warp][rows]; the work list after them
   float *so = smem, *sm = smem + kMW * kRows * D, *sl = sm + kMW * kRows;
-  long long *unit0 = reinterpret_cast<long long *>(sl + kMW * kRows), *item0 = unit0 + (R + 1);
-  draft_lists(p, unit0, item0, part);
-  const long long U = unit0[R];
+  DraftReq *list = reinterpret_cast<DraftReq *>(sl + kMW * kRows);
+  draft_list(p, list, part);
+  const long long U = list[R].unit0;
   const int w = blockIdx.x, W = workers_of(U, p.workers);
   if (w >= W) return;
   long long u = worker_start(U, W, w);
@@ -211,9 +210,8 @@ draft_part_mma(const DraftParams p) {
   const float qk_scale = p.scale * kLog2eD * (F8 ? p.descale[0] * p.descale[1] : 1.f);
   const char *Kp = static_cast<const char *>(p.past_k), *Vp = static_cast<const char *>(p.past_v);
   const size_t stride = (size_t)p.Hkv * S::kRow;
-  while (u < u_end) {
-    Run run;
-    u += draft_run(p, unit0, item0, u, u_end, w, run);
+  Run run;
+  while (draft_run(p, list, u, u_end, w, run)) {
     __syncthreads();  // the last run's shared memory is free
     // Q fragments: lane (g, c) of step s holds rows g, g + 8 at the elements its K loads give
     for (int e = tid; e < kMT * S::kCj * 32; e += kMW * 32) {
@@ -503,18 +501,16 @@ __global__ void __launch_bounds__(256) draft_join_portable(const DraftParams p) 
         if (i < nd) acc[i] = fmaf(w, value_of(Vs + at + 32 * i), acc[i] * f);
     }
   }
-  const int r = x.node_req[n];
-  const long long U = p.unit0[x.R], ua = p.unit0[r];
-  const long long items = p.item0[r + 1] - p.item0[r];
-  const long long per = items > 0 ? (p.unit0[r + 1] - ua) / items : 0;  // units of one item
-  if (per > 0) {
-    const int row = (t - x.node_start[x.req_node[r]]) * p.G + h % p.G;
-    const long long li = (long long)(row / p.tile_rows) * p.Hkv + hk;
-    const long long u0 = ua + li * per;
+  const DraftReq q = p.list[x.node_req[n]];
+  if (q.units > 0) {
+    const long long U = p.list[x.R].unit0;
+    const int row = (t - q.t0) * p.G + h % p.G;
+    const int li = row / p.tile_rows * p.Hkv + hk;
+    const long long u0 = q.unit0 + (long long)li * q.units;
     const int W = workers_of(U, p.workers);
-    const int w0 = worker_of(U, W, u0), w1 = worker_of(U, W, u0 + per - 1);
+    const int w0 = worker_of(U, W, u0 + p.extra), w1 = worker_of(U, W, u0 + q.units - 1);
     for (int w = w0; w <= w1; ++w) {
-      const size_t pr = (size_t)(w + p.item0[r] + li) * p.tile_rows + row % p.tile_rows;
+      const size_t pr = (size_t)(w + q.item0 + li) * p.tile_rows + row % p.tile_rows;
       const float pm = p.part_ml[2 * pr], pl = p.part_ml[2 * pr + 1];
       const float mn = fmaxf(m, pm), ref = mn == -INFINITY ? 0.f : mn;
       const float f = exp2f(m - ref), g = exp2f(pm - ref);
@@ -649,16 +645,17 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) draft_join_kernel(const Dr
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the part kernel's results
   if (!live || failed(x.status)) return;
-  const long long U = p.unit0[x.R], ua = p.unit0[r], ub = p.unit0[r + 1], ia = p.item0[r];
-  if (ub > ua) {
-    const long long per = (ub - ua) / (p.item0[r + 1] - ia);  // units of one item
-    const int row = (t - x.node_start[x.req_node[r]]) * p.G + h - hk * p.G;
-    const int tile = row / p.tile_rows;
-    const long long li = (long long)tile * p.Hkv + hk, u0 = ua + li * per;
+  const DraftReq q = p.list[r];
+  if (q.units > 0) {
+    const long long U = p.list[x.R].unit0;
+    const int row = (t - q.t0) * p.G + h - hk * p.G;
+    const int tile = row / p.tile_rows, li = tile * p.Hkv + hk;
+    const long long u0 = q.unit0 + (long long)li * q.units;
     const int W = workers_of(U, p.workers);
-    const int w0 = worker_of(U, W, u0), w1 = worker_of(U, W, u0 + per - 1);
+    // the workers of the item's units with keys
+    const int w0 = worker_of(U, W, u0 + p.extra), w1 = worker_of(U, W, u0 + q.units - 1);
     const int parts = (w1 - w0 + 1) << p.parts_log;
-    const size_t pr0 = ((size_t)(w0 + ia + li) << p.parts_log) * p.tile_rows + row - tile * p.tile_rows;
+    const size_t pr0 = ((size_t)(w0 + q.item0 + li) << p.parts_log) * p.tile_rows + row - tile * p.tile_rows;
     auto partial = [&](int i, float2 &ml, float4 (&v)[kE / 4]) {
       const size_t pr = pr0 + (size_t)i * p.tile_rows;
       ml = *reinterpret_cast<const float2 *>(p.part_ml + 2 * pr);
@@ -731,11 +728,10 @@ Variant variant_of(long long R, long long T, int G, int d, int dtype) {
   if (dtype == FLIDE_F32 || (d != 64 && d != 128)) return {kPortable, 16, 0};
   const long long rows = (T * G + R - 1) / (R > 0 ? R : 1);
   if (rows <= 16) return {kMma, 16, 0};
-  if (d != 128 || 128 % G) return {kMma, 32, 0};
+  if (d != 128 || 128 % G || R > 1024) return {kMma, 32, 0};  // (the tiles leave room for 1024 list entries)
   if (rows <= 32 && G <= 32) return {kWide, 32, 3};
   if (rows <= 64 && G <= 64) return {kWide, 64, 2};
-  // 256 rows leave less room for the requests' lists
-  if (rows <= 128 || R > 2048 || dtype == FLIDE_E4M3) return {kWide, 128, 1};
+  if (rows <= 128 || dtype == FLIDE_E4M3) return {kWide, 128, 1};
   return {kWide, 256, 0};
 }
 
@@ -743,7 +739,7 @@ constexpr int kMaxWorkers = 640;  // of any variant: what the workspace allows f
 constexpr int kWideWorkers = 160; // of the wide ones, one to an SM
 
 struct DraftSpace {
-  size_t unit0, item0, ml, o, total;
+  size_t list, ml, o, total;
 };
 
 // Bytes of the workspace's parts: a slot for every worker and item.
@@ -753,9 +749,8 @@ DraftSpace draft_space(long long R, long long T, int Hkv, int G, int d, const Va
   const long long rows = (slots << v.parts_log) * v.tile_rows;
   auto up = [](size_t n) { return (n + 255) / 256 * 256; };
   DraftSpace s;
-  s.unit0 = 0;
-  s.item0 = up((R + 1) * sizeof(long long));
-  s.ml = s.item0 + up((R + 1) * sizeof(long long));
+  s.list = 0;
+  s.ml = up((R + 1) * sizeof(DraftReq));
   s.o = s.ml + up((size_t)rows * 2 * sizeof(float));
   s.total = s.o + up((size_t)rows * d * sizeof(float));
   return s;
@@ -774,8 +769,9 @@ template <typename T>
 int portable_launch(DraftParams &p, int dev, int sms, cudaStream_t s) {
   p.workers = min(kMaxWorkers, 4 * sms);
   p.unit = kPKeys;
+  p.extra = 0;
   return part_launch<draft_part_portable<T>>(
-      p, dev, kPT, (size_t)(p.x.R + 1) * 16 + 16 +
+      p, dev, kPT, (size_t)(p.x.R + 1) * sizeof(DraftReq) +
                        sizeof(float) * ((size_t)(kPRows + 2 * kPKeys) * (p.d + 4) + kPRows * kPKeys), s);
 }
 
@@ -784,7 +780,8 @@ int mma_launch(DraftParams &p, int dev, int sms, cudaStream_t s) {
   using S = MmaShape<D, F8, kMT>;
   p.workers = min(kMaxWorkers, S::kBlocks * sms);
   p.unit = S::kUnit;
-  return part_launch<draft_part_mma<D, F8, kMT>>(p, dev, S::kMW * 32, S::kSmem + (size_t)(p.x.R + 1) * 16, s);
+  p.extra = 0;
+  return part_launch<draft_part_mma<D, F8, kMT>>(p, dev, S::kMW * 32, S::kSmem + (size_t)(p.x.R + 1) * sizeof(DraftReq), s);
 }
 
 template <typename T, typename TOut>
@@ -849,8 +846,7 @@ int draft_attn(const void *q, const void *k, const void *v, const void *past_k, 
   p.parts_log = var.parts_log;
   p.out = out;
   p.lse = lse;
-  p.unit0 = reinterpret_cast<long long *>(ws + sp.unit0);
-  p.item0 = reinterpret_cast<long long *>(ws + sp.item0);
+  p.list = reinterpret_cast<DraftReq *>(ws + sp.list);
   p.part_ml = reinterpret_cast<float *>(ws + sp.ml);
   p.part_o = reinterpret_cast<float *>(ws + sp.o);
   int rc;

@@ -45,13 +45,14 @@ namespace {
 using namespace sm100;
 
 constexpr int kBM = 128, kBN = 128;
-constexpr int kWThreads = 320;
+constexpr int kWThreads = 352;  // two softmax warpgroups, K and Q loads, MMA, V loads
 constexpr uint64_t kWaitNs = 2000000000ull;
 
 // Shared memory: Q's operands, the stages of K and of V (32 KB a tile, 16 KB of
-// codes), then the barriers and the block's lists (16 bytes a request).  As many
+// codes), then the barriers and the block's work list (32 bytes a request).  As many
 // stages as fit.
 constexpr int kMaxStages = 4;
+constexpr int kRunTiles = 3;  // key tiles that a run costs beside its own
 constexpr int kSmemMax = 232448;
 enum {
   bQ = 0,
@@ -67,21 +68,14 @@ enum {
   bDrain = bO + 1,
   kBars = bDrain + 1
 };
-struct Misc {
+struct __align__(16) Misc {
   uint32_t tmem;
   int abort, stop;
-  long long part[32];
+  long long part[64];
 };
 constexpr size_t wide_smem(bool f8, int halves, int stages, int R) {
   return (size_t)(halves + 2 * stages) * (f8 ? 16384 : 32768) + 256 + sizeof(Misc) +
-         (size_t)(R + 1) * 16 + 1024;
-}
-
-// 32 bytes at once (a whole sector; rows of a warp's lanes lie 512 bytes apart)
-__device__ __forceinline__ void st_sector(float *p, const uint32_t *v) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]),
-               "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-               : "memory");
+         (size_t)(R + 1) * sizeof(DraftReq) + 1024;
 }
 
 // A key tile's stage and how often the ring has been round (its parity is that of
@@ -114,7 +108,7 @@ draft_part_wide(const __grid_constant__ WideMaps maps, const DraftParams p, int 
   const int s_k = kHalves * kTile, s_v = s_k + stages * kTile, s_bar = s_v + stages * kTile;
   Misc &ms = *reinterpret_cast<Misc *>(smem + s_bar + 256);
   volatile int *abort_flag = &ms.abort;
-  long long *unit0 = reinterpret_cast<long long *>(&ms + 1), *item0 = unit0 + (p.x.R + 1);
+  DraftReq *list = reinterpret_cast<DraftReq *>(&ms + 1);
   const flide_tree_index &x = p.x;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   auto bar = [&](int i) -> uint32_t { return sb + s_bar + 8 * i; };
@@ -129,8 +123,8 @@ draft_part_wide(const __grid_constant__ WideMaps maps, const DraftParams p, int 
   }
   __syncthreads();
   if (ms.stop) return;
-  draft_lists(p, unit0, item0, ms.part);
-  const long long U = unit0[x.R];
+  draft_list(p, list, ms.part);
+  const long long U = list[x.R].unit0;
   const int w = blockIdx.x, W = workers_of(U, p.workers);
   if (w >= W) return;
   if (warp == 9) {
@@ -148,12 +142,15 @@ draft_part_wide(const __grid_constant__ WideMaps maps, const DraftParams p, int 
   // first step that a key tile is used by
   auto opens = [](int i) { return kHalves == 1 || !(i & 1); };
 
-  if (warp == 8) {
-    // -------------------------------------------------------------- producer
+  if (warp == 8 || warp == 10) {
+    // -------------------------------------------------------------- producers
+    // warp 8 loads Q and K, warp 10 V: K's next tile does not wait behind V's
+    const bool is_v = warp == 10;
+    const CUtensorMap *map = is_v ? &maps.v : &maps.k;
+    const int b_full = is_v ? bV : bK, b_free = is_v ? bVFree : bKFree, s_at = is_v ? s_v : s_k;
     if (lane == 0) {
-      prefetch_tmap(&maps.q);
-      prefetch_tmap(&maps.k);
-      prefetch_tmap(&maps.v);
+      if (!is_v) prefetch_tmap(&maps.q);
+      prefetch_tmap(map);
     }
     const int boxes = kBN / box_rows;
     auto wait = [&](int b, uint32_t parity) {
@@ -162,18 +159,8 @@ draft_part_wide(const __grid_constant__ WideMaps maps, const DraftParams p, int 
     bool ok = true;
     int rc = 0, kt = 0;  // runs, key tiles so far
     Ring ring;
-    for (; u < u_end && ok; ++rc) {
-      Run run;
-      u += draft_run(p, unit0, item0, u, u_end, w, run);
-      if (rc > 0 && !(ok = wait(bQFree, (rc - 1) & 1))) break;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(bar(bQ), kHalves * kTile);
-        for (int h = 0; h < kHalves; ++h)
-          for (int s = 0; s < kSlabs; ++s)
-            for (int c = 0; c < kRep; ++c)
-              tma_load_3d(sb + h * kTile + s * 16384 + c * kCopy * 128, &maps.q, bar(bQ), 64 * s, run.hk * p.G,
-                          run.t0 + (run.tile * kHalves + h) * mtok);
-      }
+    Run run;
+    for (; ok && draft_run(p, list, u, u_end, w, run); ++rc) {
       // boxes that hold history rows, a lane each (the rest of the last tile keeps
       // what the stage held, and is masked); looked up a tile ahead
       auto row_at = [&](int k0) -> long long {
@@ -182,39 +169,36 @@ draft_part_wide(const __grid_constant__ WideMaps maps, const DraftParams p, int 
         return max(history_row(x, p.hist, run.base, k), 0ll);  // no block: row 0, the call is flagged
       };
       long long next = row_at(run.k0);
+      if (!is_v) {
+        if (rc > 0 && !(ok = wait(bQFree, (rc - 1) & 1))) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar(bQ), kHalves * kTile);
+          for (int h = 0; h < kHalves; ++h)
+            for (int s = 0; s < kSlabs; ++s)
+              for (int c = 0; c < kRep; ++c)
+                tma_load_3d(sb + h * kTile + s * 16384 + c * kCopy * 128, &maps.q, bar(bQ), 64 * s, run.hk * p.G,
+                            run.t0 + (run.tile * kHalves + h) * mtok);
+        }
+      }
       for (int k0 = run.k0; k0 < run.k1; k0 += kBN, ++kt) {
         const int st = ring.st;
-        const uint32_t turn = ring.turn ^ 1;  // the stage's last use
         const int used = min(boxes, (run.k1 - k0 + box_rows - 1) / box_rows);
         const long long row = next;
         next = row_at(k0 + kBN);
-        if (kt >= stages && !(ok = wait(bKFree + st, turn))) break;
-        if (lane == 0) mbar_arrive_expect_tx(bar(bK + st), used * box_rows * 128 * kSlabs);
+        if (kt >= stages && !(ok = wait(b_free + st, ring.turn ^ 1))) break;
+        if (lane == 0) mbar_arrive_expect_tx(bar(b_full + st), used * box_rows * 128 * kSlabs);
         __syncwarp();
         if (lane < used)
           for (int s = 0; s < kSlabs; ++s)
-            tma_load_3d(sb + s_k + st * kTile + s * 16384 + lane * box_rows * 128, &maps.k, bar(bK + st),
-                        64 * s, run.hk, (int)row);
-        if (kt >= stages && !(ok = wait(bVFree + st, turn))) {
-          // K of this tile is in flight, V is not
-          mbar_wait(bar(bK + st), ring.turn, abort_flag, kWaitNs, false);
-          break;
-        }
-        if (lane == 0) mbar_arrive_expect_tx(bar(bV + st), used * box_rows * 128 * kSlabs);
-        __syncwarp();
-        if (lane < used)
-          for (int s = 0; s < kSlabs; ++s)
-            tma_load_3d(sb + s_v + st * kTile + s * 16384 + lane * box_rows * 128, &maps.v, bar(bV + st),
-                        64 * s, run.hk, (int)row);
+            tma_load_3d(sb + s_at + st * kTile + s * 16384 + lane * box_rows * 128, map, bar(b_full + st), 64 * s,
+                        run.hk, (int)row);
         ring.next(stages);
       }
     }
     // no copy may be in flight when the block ends
-    if (rc > 0) mbar_wait(bar(bQ), (rc - 1) & 1, abort_flag, kWaitNs, false);
-    for (int t = max(0, kt - stages); t < kt; ++t) {
-      mbar_wait(bar(bK + t % stages), (t / stages) & 1, abort_flag, kWaitNs, false);
-      mbar_wait(bar(bV + t % stages), (t / stages) & 1, abort_flag, kWaitNs, false);
-    }
+    if (!is_v && rc > 0) mbar_wait(bar(bQ), (rc - 1) & 1, abort_flag, kWaitNs, false);
+    for (int t = max(0, kt - stages); t < kt; ++t)
+      mbar_wait(bar(b_full + t % stages), (t / stages) & 1, abort_flag, kWaitNs, false);
   } else if (warp == 9) {
     // -------------------------------------------------------------- MMA
     if (lane == 0) {
@@ -225,9 +209,8 @@ draft_part_wide(const __grid_constant__ WideMaps maps, const DraftParams p, int 
       int rc = 0;
       uint32_t np[2] = {0, 0};  // weights taken per S buffer, mod 2
       Ring rs, rv;              // key tiles of the scores and of the products with V
-      for (; u < u_end && ok; ++rc) {
-        Run run;
-        u += draft_run(p, unit0, item0, u, u_end, w, run);
+      Run run;
+      for (; ok && draft_run(p, list, u, u_end, w, run); ++rc) {
         const int steps = (run.k1 - run.k0 + kBN - 1) / kBN * kHalves;
         // S of the next step, in S buffer h
         auto scores = [&](int h) -> bool {
@@ -301,9 +284,8 @@ draft_part_wide(const __grid_constant__ WideMaps maps, const DraftParams p, int 
     bool ok = true;
     uint32_t ns = 0;  // score tiles taken, mod 2
     int rc = 0, kt0 = 0;
-    for (; u < u_end && ok; ++rc) {
-      Run run;
-      u += draft_run(p, unit0, item0, u, u_end, w, run);
+    Run run;
+    for (; ok && draft_run(p, list, u, u_end, w, run); ++rc) {
       const int tiles = (run.k1 - run.k0 + kBN - 1) / kBN, steps = tiles * kHalves;
       float m = -INFINITY, l = 0.f;
       for (int i = h; i < steps; i += 2) {
@@ -425,20 +407,39 @@ draft_part_wide(const __grid_constant__ WideMaps maps, const DraftParams p, int 
       }
       if (!ok || !(ok = wait(bO, rc & 1))) break;
       tc_fence_after();
-      const size_t at = (size_t)run.slot * 256 + h * 128 + row;
-      const bool real = run.tile * p.tile_rows + (kHalves == 2 ? h * kBM : 0) + row % kCopy < run.tokens * p.G;
-      if (h < steps) {
-        float *o = p.part_o + at * 128;
+      // the partial's rows, 128 bytes of four rows a store: eight lanes exchange
+      // their rows' 16-byte words (lane j takes word j of each), because a lane
+      // writing its own row touches 32 lines a store (6.4K cycles a run)
+      const size_t at = (size_t)run.slot * 256 + h * 128;
+      const int limit = run.tokens * p.G - run.tile * p.tile_rows - (kHalves == 2 ? h * kBM : 0);  // real rows
+      const int l8 = lane & 7;
 #pragma unroll 1
-        for (int c4 = 0; c4 < 4; ++c4) {
-          uint32_t r32[32];
-          tmem_ld32(t_o + 32 * c4, r32);
+      for (int c4 = 0; c4 < 4 && h < steps; ++c4) {
+        uint32_t r32[32];
+        tmem_ld32(t_o + 32 * c4, r32);
 #pragma unroll
-          for (int j = 0; j < 32; j += 8)
-            if (real) st_sector(o + 32 * c4 + j, r32 + j);
+        for (int s = 4; s > 0; s >>= 1) {
+          const bool up = l8 & s;
+#pragma unroll
+          for (int a = 0; a < 8; ++a) {
+            if (a & s) continue;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              uint32_t &lo = r32[4 * a + k], &hi = r32[4 * (a | s) + k];
+              const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? lo : hi, s);
+              if (up) lo = got; else hi = got;
+            }
+          }
+        }
+#pragma unroll
+        for (int a = 0; a < 8; ++a) {
+          const int r = row - l8 + a;
+          if (r % kCopy < limit)
+            *reinterpret_cast<uint4 *>(p.part_o + (at + r) * 128 + 32 * c4 + 4 * l8) =
+                make_uint4(r32[4 * a], r32[4 * a + 1], r32[4 * a + 2], r32[4 * a + 3]);
         }
       }
-      *reinterpret_cast<float2 *>(p.part_ml + 2 * at) = make_float2(m - kShift, l);
+      if (row % kCopy < limit) *reinterpret_cast<float2 *>(p.part_ml + 2 * (at + row)) = make_float2(m - kShift, l);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(bOFree + h));
@@ -503,9 +504,9 @@ int wide_launch(const DraftParams &p, const WideMaps &maps, int mtok, int box_ro
 
 }  // namespace
 
-int draft_wide_launch(const DraftParams &p0, int past_rows, bool f8, int dev, cudaStream_t s) {
-  DraftParams p = p0;
+int draft_wide_launch(DraftParams &p, int past_rows, bool f8, int dev, cudaStream_t s) {
   p.unit = kBN;
+  p.extra = kRunTiles;
   const int rep = p.tile_rows < kBM ? kBM / p.tile_rows : 1;
   const int mtok = kBM / rep / p.G, esz = f8 ? 1 : 2;
   // rows of a box: a tile's, or the most that divides both it and a block

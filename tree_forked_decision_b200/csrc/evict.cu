@@ -312,6 +312,7 @@ __device__ __forceinline__ int evict_length(const EvictParams &p, int r, bool re
   return len;
 }
 
+constexpr int kMaxEvictR = 4096;  // each request looks through the others' slots
 constexpr int kSelThreads = 1024;
 constexpr int kBits = 11;  // 3 passes over 32-bit codes
 constexpr int kBins = 1 << kBits;
@@ -571,7 +572,7 @@ int flide_history_evict(int32_t R, const int32_t *req_slot, int32_t n_slots, con
   if (!es) return FLIDE_ERR_SHAPE;
   const int64_t row_bytes = (int64_t)Hkv * d * es;
   if (row_bytes % 16 || row_bytes > (1 << 20)) return FLIDE_ERR_SHAPE;
-  if (R > kMaxListR || (int64_t)max_blocks * block_rows > INT32_MAX) return FLIDE_ERR_CAPACITY;
+  if (R > kMaxEvictR || (int64_t)max_blocks * block_rows > INT32_MAX) return FLIDE_ERR_CAPACITY;
   if (R == 0) return FLIDE_OK;
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||

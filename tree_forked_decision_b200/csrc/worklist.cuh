@@ -6,7 +6,7 @@
 
 namespace flide {
 
-constexpr int kMaxListR = 4096;  // requests of a work list
+constexpr int kMaxListR = 2048;  // requests of a work list
 
 // pref[r] = sum of count(0 .. r-1), pref[R] = the total; 64 bits, because a
 // long history's units times its heads pass 2^31.  `part` holds a block's
