@@ -729,8 +729,8 @@ Variant variant_of(long long R, long long T, int G, int d, int dtype) {
   const long long rows = (T * G + R - 1) / (R > 0 ? R : 1);
   if (rows <= 16) return {kMma, 16, 0};
   if (d != 128 || 128 % G || R > 1024) return {kMma, 32, 0};  // (the tiles leave room for 1024 list entries)
-  if (rows <= 32 && G <= 32) return {kWide, 32, 3};
-  if (rows <= 64 && G <= 64) return {kWide, 64, 2};
+  if (rows <= 32 && G <= 32) return {kWide, 32, 0};
+  if (rows <= 64 && G <= 64) return {kWide, 64, 0};
   if (rows <= 128 || dtype == FLIDE_E4M3) return {kWide, 128, 1};
   return {kWide, 256, 0};
 }

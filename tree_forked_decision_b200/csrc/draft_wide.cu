@@ -11,8 +11,8 @@
 //     would leave the tensor core and the memory idle half the time;
 //   - 64 or 32 rows: the operand holds them two or four times, and each copy's
 //     threads take a half or quarter of the tile's keys (their weights for the
-//     others are 0): four or eight partials, and a half or quarter of the softmax
-//     in each thread's chain, which is what bounds a tile.
+//     others are 0): a half or quarter of the softmax in each thread's chain, which
+//     is what bounds a tile.  The four or eight results are joined in the block.
 // A block (one to an SM) takes its share of the batch's key tiles as runs
 // inside one (request, row tile, kv head) item (draft.cuh); barriers count over
 // the block's life, so the next run's loads are in flight while the last tiles
@@ -65,7 +65,8 @@ enum {
   bP = bS + 2,                // [2], 4 warps
   bOFree = bP + 2,            // [2], 4 warps
   bO = bOFree + 2,
-  bDrain = bO + 1,
+  bMerge = bO + 1,            // 8 warps
+  bDrain = bMerge + 1,
   kBars = bDrain + 1
 };
 struct __align__(16) Misc {
@@ -73,8 +74,11 @@ struct __align__(16) Misc {
   int abort, stop;
   long long part[64];
 };
-constexpr size_t wide_smem(bool f8, int halves, int stages, int R) {
-  return (size_t)(halves + 2 * stages) * (f8 ? 16384 : 32768) + 256 + sizeof(Misc) +
+// Where copies' results are joined: their rows (132 floats: eight lanes' words in
+// 32 banks), and a warp's (max, sum) for each of its rows.
+constexpr int merge_bytes(int rep) { return rep > 1 ? kBM / rep * 132 * 4 + 2 * 8 * 32 * 4 : 0; }
+constexpr size_t wide_smem(bool f8, int halves, int rep, int tiles, int R) {
+  return (size_t)(halves + tiles) * (f8 ? 16384 : 32768) + merge_bytes(rep) + 256 + sizeof(Misc) +
          (size_t)(R + 1) * sizeof(DraftReq) + 1024;
 }
 
@@ -98,14 +102,15 @@ struct WideMaps {
 template <int kHalves, int kRep, bool F8>
 __global__ void __launch_bounds__(kWThreads, 1)
 draft_part_wide(const __grid_constant__ WideMaps maps, const DraftParams p, int mtok, int box_rows,
-                int stages) {
+                int stages_k, int stages_v) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   const uint32_t sb = smem_u32(smem);
   static_assert(kHalves == 1 || kRep == 1, "copies are of a tile of one operand");
   constexpr int kCopy = kBM / kRep, kCols = kBN / kRep;  // rows of a copy, keys of its threads
   constexpr int kTile = F8 ? 16384 : 32768, kSlabs = F8 ? 1 : 2;  // bytes; 128-byte slabs of a row
-  const int s_k = kHalves * kTile, s_v = s_k + stages * kTile, s_bar = s_v + stages * kTile;
+  const int s_k = kHalves * kTile, s_v = s_k + stages_k * kTile, s_m = s_v + stages_v * kTile;
+  const int s_bar = s_m + merge_bytes(kRep);
   Misc &ms = *reinterpret_cast<Misc *>(smem + s_bar + 256);
   volatile int *abort_flag = &ms.abort;
   DraftReq *list = reinterpret_cast<DraftReq *>(&ms + 1);
@@ -116,7 +121,7 @@ draft_part_wide(const __grid_constant__ WideMaps maps, const DraftParams p, int 
   // the status word may change while the grid runs: one thread's reading counts
   if (tid == 0) {
     for (int i = 0; i < kBars; ++i)
-      mbar_init(bar(i), (i >= bP && i < bP + 2) || (i >= bOFree && i < bOFree + 2) ? 4u : 1u);
+      mbar_init(bar(i), (i >= bP && i < bP + 2) || (i >= bOFree && i < bOFree + 2) ? 4u : i == bMerge ? 8u : 1u);
     fence_mbar_init();
     ms.abort = 0;
     ms.stop = failed(x.status);
@@ -147,6 +152,7 @@ draft_part_wide(const __grid_constant__ WideMaps maps, const DraftParams p, int 
     // warp 8 loads Q and K, warp 10 V: K's next tile does not wait behind V's
     const bool is_v = warp == 10;
     const CUtensorMap *map = is_v ? &maps.v : &maps.k;
+    const int stages = is_v ? stages_v : stages_k;
     const int b_full = is_v ? bV : bK, b_free = is_v ? bVFree : bKFree, s_at = is_v ? s_v : s_k;
     if (lane == 0) {
       if (!is_v) prefetch_tmap(&maps.q);
@@ -228,7 +234,7 @@ draft_part_wide(const __grid_constant__ WideMaps maps, const DraftParams p, int 
           mma_commit(bar(bS + h));
           if (kHalves == 1 || h == 1) {
             mma_commit(bar(bKFree + rs.st));
-            rs.next(stages);
+            rs.next(stages_k);
           }
           return true;
         };
@@ -250,7 +256,7 @@ draft_part_wide(const __grid_constant__ WideMaps maps, const DraftParams p, int 
           }
           if (kHalves == 1 || h == 1) {
             mma_commit(bar(bVFree + rv.st));
-            rv.next(stages);
+            rv.next(stages_v);
           }
           return true;
         };
@@ -282,6 +288,14 @@ draft_part_wide(const __grid_constant__ WideMaps maps, const DraftParams p, int 
     };
     constexpr float kShift = F8 ? 6.f : 0.f;  // weights carry 2^kShift
     bool ok = true;
+    uint32_t met = 0;
+    auto meet = [&]() -> bool {  // all softmax warps
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(bMerge));
+      const uint32_t phase = met;
+      met ^= 1;
+      return wait(bMerge, phase);
+    };
     uint32_t ns = 0;  // score tiles taken, mod 2
     int rc = 0, kt0 = 0;
     Run run;
@@ -303,8 +317,8 @@ draft_part_wide(const __grid_constant__ WideMaps maps, const DraftParams p, int 
             if (col0 + j >= left) sr[j] = 0xff800000u;  // -inf
           if (opens(i)) {
             // V rows behind the history: zero, whatever was there
-            const int st = (kt0 + kt) % stages;
-            if (!(ok = wait(bV + st, ((kt0 + kt) / stages) & 1))) break;
+            const int st = (kt0 + kt) % stages_v;
+            if (!(ok = wait(bV + st, ((kt0 + kt) / stages_v) & 1))) break;
             for (int e = left * 8 + (tid & 127); e < kBN * 8; e += 128) {
               uint4 *z = reinterpret_cast<uint4 *>(smem + s_v + st * kTile) + e;
               z[0] = make_uint4(0u, 0u, 0u, 0u);
@@ -407,42 +421,97 @@ draft_part_wide(const __grid_constant__ WideMaps maps, const DraftParams p, int 
       }
       if (!ok || !(ok = wait(bO, rc & 1))) break;
       tc_fence_after();
-      // the partial's rows, 128 bytes of four rows a store: eight lanes exchange
-      // their rows' 16-byte words (lane j takes word j of each), because a lane
-      // writing its own row touches 32 lines a store (6.4K cycles a run)
-      const size_t at = (size_t)run.slot * 256 + h * 128;
       const int limit = run.tokens * p.G - run.tile * p.tile_rows - (kHalves == 2 ? h * kBM : 0);  // real rows
-      const int l8 = lane & 7;
+      if constexpr (kRep == 1) {
+        // the partial's rows, 128 bytes of four rows a store: eight lanes exchange
+        // their rows' 16-byte words (lane j takes word j of each), because a lane
+        // writing its own row touches 32 lines a store (6.4K cycles a run)
+        const size_t at = (size_t)run.slot * 256 + h * 128;
+        const int l8 = lane & 7;
 #pragma unroll 1
-      for (int c4 = 0; c4 < 4 && h < steps; ++c4) {
-        uint32_t r32[32];
-        tmem_ld32(t_o + 32 * c4, r32);
+        for (int c4 = 0; c4 < 4 && h < steps; ++c4) {
+          uint32_t r32[32];
+          tmem_ld32(t_o + 32 * c4, r32);
 #pragma unroll
-        for (int s = 4; s > 0; s >>= 1) {
-          const bool up = l8 & s;
+          for (int s = 4; s > 0; s >>= 1) {
+            const bool up = l8 & s;
 #pragma unroll
-          for (int a = 0; a < 8; ++a) {
-            if (a & s) continue;
+            for (int a = 0; a < 8; ++a) {
+              if (a & s) continue;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              uint32_t &lo = r32[4 * a + k], &hi = r32[4 * (a | s) + k];
-              const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? lo : hi, s);
-              if (up) lo = got; else hi = got;
+              for (int k = 0; k < 4; ++k) {
+                uint32_t &lo = r32[4 * a + k], &hi = r32[4 * (a | s) + k];
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? lo : hi, s);
+                if (up) lo = got; else hi = got;
+              }
             }
           }
+#pragma unroll
+          for (int a = 0; a < 8; ++a) {
+            const int r = row - l8 + a;
+            if (r % kCopy < limit)
+              *reinterpret_cast<uint4 *>(p.part_o + (at + r) * 128 + 32 * c4 + 4 * l8) =
+                  make_uint4(r32[4 * a], r32[4 * a + 1], r32[4 * a + 2], r32[4 * a + 3]);
+          }
+        }
+        if (row % kCopy < limit) *reinterpret_cast<float2 *>(p.part_ml + 2 * (at + row)) = make_float2(m - kShift, l);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(bOFree + h));
+      } else {
+        // The copies' results become one.  A row's sharers are kRep warps of each S
+        // buffer; they add a chunk of columns each to the buffer in shared memory
+        // and move on to the next, so every sum has one order.
+        constexpr int kShare = 2 * kRep, kChunk = 128 / kShare;
+        const int mine = h * kRep + row / kCopy, r = row % kCopy, wid = warp;
+        float *buf = reinterpret_cast<float *>(smem + s_m), *st_m = buf + kCopy * 132, *st_l = st_m + 256;
+        if (h >= steps) m = -INFINITY;
+        st_m[wid * 32 + lane] = m - kShift;
+        st_l[wid * 32 + lane] = l;
+        if (!(ok = meet())) break;
+        float top = -INFINITY, all = 0.f;
+#pragma unroll
+        for (int k = 0; k < kShare; ++k) {  // sharer k's warp: S buffer k / kRep, this row's quadrant of copy k % kRep
+          const int wk = (k / kRep) * 4 + (k % kRep) * (4 / kRep) + (warp & 3) % (4 / kRep);
+          top = fmaxf(top, st_m[wk * 32 + lane]);
         }
 #pragma unroll
-        for (int a = 0; a < 8; ++a) {
-          const int r = row - l8 + a;
-          if (r % kCopy < limit)
-            *reinterpret_cast<uint4 *>(p.part_o + (at + r) * 128 + 32 * c4 + 4 * l8) =
-                make_uint4(r32[4 * a], r32[4 * a + 1], r32[4 * a + 2], r32[4 * a + 3]);
+        for (int k = 0; k < kShare; ++k) {
+          const int wk = (k / kRep) * 4 + (k % kRep) * (4 / kRep) + (warp & 3) % (4 / kRep);
+          all += st_l[wk * 32 + lane] * (top == -INFINITY ? 0.f : ex2_approx(st_m[wk * 32 + lane] - top));
         }
+        const float f = m == -INFINITY ? 0.f : ex2_approx(m - kShift - top);
+#pragma unroll 1
+        for (int k = 0; k < kShare && ok; ++k) {
+          const int c0 = (mine + k) % kShare * kChunk;
+          uint32_t v[kChunk];
+          if constexpr (kChunk == 16) tmem_ld16(t_o + c0, v);
+          else tmem_ld32(t_o + c0, v);
+          float4 *to = reinterpret_cast<float4 *>(buf + r * 132 + c0);
+#pragma unroll
+          for (int j = 0; j < kChunk / 4; ++j) {
+            float4 o = k > 0 ? to[j] : make_float4(0.f, 0.f, 0.f, 0.f);
+            if (h < steps) {
+              o.x = fmaf(f, __uint_as_float(v[4 * j]), o.x);
+              o.y = fmaf(f, __uint_as_float(v[4 * j + 1]), o.y);
+              o.z = fmaf(f, __uint_as_float(v[4 * j + 2]), o.z);
+              o.w = fmaf(f, __uint_as_float(v[4 * j + 3]), o.w);
+            }
+            to[j] = o;
+          }
+          ok = meet();
+        }
+        if (!ok) break;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(bOFree + h));
+        const size_t at = (size_t)run.slot * kCopy;
+        for (int e = tid; e < kCopy * 32; e += 256)
+          if (e / 32 < limit)
+            *reinterpret_cast<float4 *>(p.part_o + (at + e / 32) * 128 + 4 * (e & 31)) =
+                *reinterpret_cast<const float4 *>(buf + e / 32 * 132 + 4 * (e & 31));
+        if (mine == 0 && r < limit) *reinterpret_cast<float2 *>(p.part_ml + 2 * (at + r)) = make_float2(top, all);
       }
-      if (row % kCopy < limit) *reinterpret_cast<float2 *>(p.part_ml + 2 * (at + row)) = make_float2(m - kShift, l);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(bOFree + h));
       kt0 += tiles;
     }
   }
@@ -492,12 +561,12 @@ bool wide_map(CUtensorMap *m, const void *base, int esz, int heads, long rows, i
 
 template <int kHalves, int kRep, bool F8>
 int wide_launch(const DraftParams &p, const WideMaps &maps, int mtok, int box_rows, int dev, cudaStream_t s) {
-  int stages = kMaxStages;
-  while (wide_smem(F8, kHalves, stages, p.x.R) > kSmemMax) --stages;
-  if (stages < 2) return FLIDE_ERR_CAPACITY;
-  const size_t smem = wide_smem(F8, kHalves, stages, p.x.R);
+  int k = kMaxStages, v = kMaxStages;  // as many as fit, K's first
+  while (k > 1 && wide_smem(F8, kHalves, kRep, k + v, p.x.R) > kSmemMax) (k > v ? k : v)--;
+  if (k < 2 || v < 2) return FLIDE_ERR_CAPACITY;
+  const size_t smem = wide_smem(F8, kHalves, kRep, k + v, p.x.R);
   if (!allow_smem<draft_part_wide<kHalves, kRep, F8>>(dev)) return FLIDE_ERR_CUDA;
-  draft_part_wide<kHalves, kRep, F8><<<p.workers, kWThreads, smem, s>>>(maps, p, mtok, box_rows, stages);
+  draft_part_wide<kHalves, kRep, F8><<<p.workers, kWThreads, smem, s>>>(maps, p, mtok, box_rows, k, v);
   FLIDE_LAUNCH_CHECK();
   return FLIDE_OK;
 }
