@@ -37,13 +37,6 @@ struct DraftParams {
   float *part_o, *part_ml;
 };
 
-// tokens of request r's stream region
-__device__ __forceinline__ int request_tokens(const flide_tree_index &x, int r, int *t0) {
-  const int n0 = x.req_node[r], n1 = x.req_node[r + 1];
-  *t0 = n1 > n0 ? x.node_start[n0] : 0;
-  return n1 > n0 ? x.node_start[n1] - *t0 : 0;
-}
-
 __device__ __forceinline__ int tiles_of(const DraftParams &p, int tokens) {
   return (int)(((long long)tokens * p.G + p.tile_rows - 1) / p.tile_rows);
 }
@@ -64,18 +57,35 @@ __device__ __forceinline__ int worker_of(long long U, int W, long long u) {
 }
 
 // The batch's work list, in shared memory and, for the join kernel, in the
-// workspace.  part: 64 entries.  Ends with a barrier.
-__device__ __forceinline__ void draft_list(const DraftParams &p, DraftReq *list, long long *part) {
+// workspace; false (and no list) where the status word says that the batch failed:
+// one thread's reading, since it may change while the grid runs.  part: 64 entries.
+// Ends with a barrier.  What a request's number alone addresses is loaded before
+// anything is waited for: after a long history nothing of it is left in L2, and
+// every dependent load takes a microsecond.
+__device__ __forceinline__ bool draft_list(const DraftParams &p, DraftReq *list, long long *part) {
   const flide_tree_index &x = p.x;
   const int R = x.R, nt = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (R + nt - 1) / nt, lo = min(R, tid * per), hi = min(R, lo + per);
+  const int stop = tid == 0 ? failed(x.status) : 0;
+  int n0 = 0, n1 = 0, p0 = 0, p1 = 0, slot = 0;
+  auto first = [&](int r) {
+    n0 = x.req_node[r];
+    n1 = x.req_node[r + 1];
+    p0 = x.past_start[r];
+    p1 = x.past_start[r + 1];
+    if (p.hist.block_table) slot = p.hist.req_slot[r];
+  };
+  if (lo < hi) first(lo);
+  if (__syncthreads_or(stop)) return false;
   long long units = 0, items = 0;
   for (int r = lo; r < hi; ++r) {
+    if (r > lo) first(r);
     DraftReq q;
-    long long base;
-    q.hist = history_rows(x, p.hist, r, blockIdx.x == 0, &base);
-    q.base = (int)base;
-    q.tokens = request_tokens(x, r, &q.t0);
+    q.t0 = n1 > n0 ? x.node_start[n0] : 0;
+    q.tokens = n1 > n0 ? x.node_start[n1] - q.t0 : 0;
+    int code = 0;
+    q.hist = history_length(p.hist, p0, p1 - p0, slot, &q.base, &code);
+    if (code && blockIdx.x == 0) set_status(x.status, code);
     q.unit0 = units;
     q.item0 = (int)items;
     q.units = q.hist > 0 ? (q.hist + p.unit - 1) / p.unit + p.extra : 0;
@@ -114,6 +124,7 @@ __device__ __forceinline__ void draft_list(const DraftParams &p, DraftReq *list,
     if (blockIdx.x == 0) p.list[R] = end;
   }
   __syncthreads();
+  return true;
 }
 
 // A worker's run: history rows [k0, k1) of one item (row tile `tile`, kv head
@@ -134,7 +145,8 @@ __device__ __forceinline__ bool draft_run(const DraftParams &p, const DraftReq *
     }
     const DraftReq q = list[lo];
     const long long at = u - q.unit0;
-    const int li = (int)(at / q.units), c0 = (int)(at - (long long)li * q.units);
+    const int li = at >> 31 ? (int)(at / q.units) : (int)at / q.units;  // (a 64-bit quotient is slow)
+    const int c0 = (int)(at - (long long)li * q.units);
     const int c1 = (int)min((long long)q.units, c0 + (u_end - u));
     u += c1 - c0;
     run.tile = li / p.Hkv;

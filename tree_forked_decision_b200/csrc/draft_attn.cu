@@ -53,13 +53,12 @@ __global__ void __launch_bounds__(kPT) draft_part_portable(const DraftParams p) 
   extern __shared__ float smem[];
   __shared__ long long part[64];
   const flide_tree_index &x = p.x;
-  if (failed(x.status)) return;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int d = p.d, ld = d + 4, R = x.R;
   DraftReq *list = reinterpret_cast<DraftReq *>(smem);
   float *sq = smem + 8 * (R + 1), *sk = sq + kPRows * ld, *sv = sk + kPKeys * ld;
   float *sp = sv + kPKeys * ld;
-  draft_list(p, list, part);
+  if (!draft_list(p, list, part)) return;
   const long long U = list[R].unit0;
   const int w = blockIdx.x, W = workers_of(U, p.workers);
   if (w >= W) return;
@@ -195,13 +194,12 @@ draft_part_mma(const DraftParams p) {
   __shared__ uint4 qfrag[kMT * S::kSteps * 32];
   const flide_tree_index &x = p.x;
   asm volatile("griddepcontrol.launch_dependents;");
-  if (failed(x.status)) return;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
   const int R = x.R;
   // O [warp][rows][D], then max and sum [warp][rows]; the work list after them
   float *so = smem, *sm = smem + kMW * kRows * D, *sl = sm + kMW * kRows;
   DraftReq *list = reinterpret_cast<DraftReq *>(sl + kMW * kRows);
-  draft_list(p, list, part);
+  if (!draft_list(p, list, part)) return;
   const long long U = list[R].unit0;
   const int w = blockIdx.x, W = workers_of(U, p.workers);
   if (w >= W) return;

@@ -52,7 +52,6 @@ constexpr uint64_t kWaitNs = 2000000000ull;
 // codes), then the barriers and the block's work list (32 bytes a request).  As many
 // stages as fit.
 constexpr int kMaxStages = 4;
-constexpr int kRunTiles = 3;  // key tiles that a run costs beside its own
 constexpr int kSmemMax = 232448;
 enum {
   bQ = 0,
@@ -71,7 +70,7 @@ enum {
 };
 struct __align__(16) Misc {
   uint32_t tmem;
-  int abort, stop;
+  int abort;
   long long part[64];
 };
 // Where copies' results are joined: their rows (132 floats: eight lanes' words in
@@ -118,17 +117,13 @@ draft_part_wide(const __grid_constant__ WideMaps maps, const DraftParams p, int 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   auto bar = [&](int i) -> uint32_t { return sb + s_bar + 8 * i; };
   asm volatile("griddepcontrol.launch_dependents;");
-  // the status word may change while the grid runs: one thread's reading counts
   if (tid == 0) {
     for (int i = 0; i < kBars; ++i)
       mbar_init(bar(i), (i >= bP && i < bP + 2) || (i >= bOFree && i < bOFree + 2) ? 4u : i == bMerge ? 8u : 1u);
     fence_mbar_init();
     ms.abort = 0;
-    ms.stop = failed(x.status);
   }
-  __syncthreads();
-  if (ms.stop) return;
-  draft_list(p, list, ms.part);
+  if (!draft_list(p, list, ms.part)) return;
   const long long U = list[x.R].unit0;
   const int w = blockIdx.x, W = workers_of(U, p.workers);
   if (w >= W) return;
@@ -575,7 +570,9 @@ int wide_launch(const DraftParams &p, const WideMaps &maps, int mtok, int box_ro
 
 int draft_wide_launch(DraftParams &p, int past_rows, bool f8, int dev, cudaStream_t s) {
   p.unit = kBN;
-  p.extra = kRunTiles;
+  // key tiles that a run costs beside its own: about 11K cycles of 1.5K (codes),
+  // 2.2K and (256 rows) 3.9K a tile
+  p.extra = f8 ? 6 : p.tile_rows == 2 * kBM ? 3 : 5;
   const int rep = p.tile_rows < kBM ? kBM / p.tile_rows : 1;
   const int mtok = kBM / rep / p.G, esz = f8 ? 1 : 2;
   // rows of a box: a tile's, or the most that divides both it and a block

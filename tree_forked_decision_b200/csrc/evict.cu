@@ -49,8 +49,7 @@ __device__ __forceinline__ long long mass_units(const MassParams &p, int r, int 
   const flide_tree_index &x = p.x;
   const int slot = p.hist.req_slot[r];
   if (slot < 0) return 0;
-  int t0;
-  long long base;
+  int t0, base;
   const int root = root_tokens(x, r, &t0);
   const int n = history_rows(x, p.hist, r, report, &base);
   if (root == 0) return 0;
@@ -78,8 +77,7 @@ __global__ void __launch_bounds__(kMThreads) mass_kernel_portable(const MassPara
           *Pk = static_cast<const T *>(p.pool_k);
   for (long long u = blockIdx.x; u < unit0[R]; u += gridDim.x) {
     const int r = request_of(unit0, R, u);
-    int t0;
-    long long slot;
+    int t0, slot;
     const int root = root_tokens(x, r, &t0);
     const int n = history_rows(x, p.hist, r, false, &slot);
     slot = p.hist.req_slot[r];
@@ -157,8 +155,7 @@ __global__ void __launch_bounds__(kMassWarps * 32, 2) mass_kernel_mma(const Mass
   int held_r = -1, held_b = -1;  // request and batch of query tiles in shared memory
   for (long long u = blockIdx.x * U / gridDim.x; u < u_end; ++u) {
     const int r = request_of(unit0, R, u);
-    int t0;
-    long long slot;
+    int t0, slot;
     const int root = root_tokens(x, r, &t0);
     const int n = history_rows(x, p.hist, r, false, &slot);
     slot = p.hist.req_slot[r];

@@ -59,24 +59,32 @@ struct HistoryView {
   long long rows;  // rows of the packed arrays
 };
 
-// History rows of request r that can be read (0 with the status set where the
-// slot or the lengths are bad); first packed row or slot in *base.
-__device__ __forceinline__ int history_rows(const flide_tree_index &x, const HistoryView &h, int r,
-                                            bool report, long long *base) {
-  const int p0 = x.past_start[r], len = x.past_start[r + 1] - p0;
-  *base = p0;
+// Rows that can be read of a history of `len` rows, packed from row p0 or in pool
+// slot `slot`: 0 and a status code where the slot or the lengths are bad.  *base:
+// its first packed row, or its slot.
+__device__ __forceinline__ int history_length(const HistoryView &h, int p0, int len, int slot, int *base,
+                                              int *code) {
+  *base = h.block_table ? slot : p0;
   if (len <= 0) return 0;
   if (h.block_table) {
-    const int slot = h.req_slot[r];
     if (slot < 0 || slot >= h.n_slots || len > (long long)h.max_blocks * h.block_rows) {
-      if (report) set_status(x.status, FLIDE_ERR_INVALID);
+      *code = FLIDE_ERR_INVALID;
       return 0;
     }
-    *base = slot;
   } else if (p0 < 0 || (long long)p0 + len > h.rows) {
-    if (report) set_status(x.status, h.rows ? FLIDE_ERR_CAPACITY : FLIDE_ERR_SHAPE);
+    *code = h.rows ? FLIDE_ERR_CAPACITY : FLIDE_ERR_SHAPE;
     return 0;
   }
+  return len;
+}
+
+// The same of request r, with the status set where `report`.
+__device__ __forceinline__ int history_rows(const flide_tree_index &x, const HistoryView &h, int r,
+                                            bool report, int *base) {
+  int code = 0;
+  const int p0 = x.past_start[r];
+  const int len = history_length(h, p0, x.past_start[r + 1] - p0, h.block_table ? h.req_slot[r] : 0, base, &code);
+  if (code && report) set_status(x.status, code);
   return len;
 }
 
