@@ -22,6 +22,8 @@
 namespace flide {
 namespace {
 
+using namespace sm100;
+
 constexpr float kLog2eM = 1.4426950408889634f;
 
 struct MassParams {
@@ -32,6 +34,7 @@ struct MassParams {
   float *mass_out;
   int Hq, Hkv, G, d;
   float scale;
+  int held;  // query tiles in shared memory at a time (tensor-core kernel)
 };
 
 // Units of a request: its history rows and its root's rows, `unit` at a time
@@ -120,149 +123,228 @@ __global__ void __launch_bounds__(kMThreads) mass_kernel_portable(const MassPara
 // bf16 rows of 64 or 128 elements and e4m3 rows of 128, on the tensor cores.  A
 // warp takes 16 history rows over all heads, so a row's sum over heads and
 // tokens stays in one lane quad's registers: S^T = K Q^T with the 16 rows as the
-// m16 operand, loaded from global memory straight into its registers, and 8
-// query rows (tokens x heads of the group) as the n8 one, kept in shared memory
-// as the raw 16-byte words that the lanes' k order asks for (see draft_attn.cu).
-// exp(score - lse) of a padding row is exp(-inf) = 0.  The next head's rows are
-// loaded before the current head's are used.  Bound by K's bytes.
-constexpr int kMassWarps = 8;
-constexpr int kMassUnit = 16 * kMassWarps;  // history rows of a unit
+// m16 operand and 8 query rows (tokens x heads of the group) as the n8 one, kept
+// in shared memory as the raw 16-byte words that the lanes' k order asks for (see
+// draft_attn.cu).  exp(score - lse) of a padding row is exp(-inf) = 0.
+//
+// Bound by K's bytes, and so by what is on its way: each lane copies the very
+// words it will need to its own places in shared memory (8 KB a warp), a head or
+// more ahead and past the end of a group of rows; no lane reads another's words,
+// so nothing but the copies is waited for.  After that by the latency of a head's
+// 260 instructions: 16 histories of 1024 to 16384 rows, 4 root tokens of 32 heads
+// took 73 us with 8 warps an SM, 63 with 12, 59 with 16.  Blocks share the batch's
+// groups of 16 rows evenly: a warp has about three.
+constexpr int kMassWarps = 16;
+constexpr int kRing = 8192;  // bytes of a warp's ring
 
 template <int D, bool F8>
 struct MassShape {
   static constexpr int kRow = D * (F8 ? 1 : 2);
   static constexpr int kCj = kRow / 64;                     // a lane's 16-byte loads of a row
-  static constexpr int kWords = kCj * (F8 ? 2 : 1);         // its 16-byte words of an 8-row query tile
+  static constexpr int kStages = kRing / (2 * kCj * 512);   // steps (16 rows of a head) of the ring
+  static constexpr int kWords = kCj * (F8 ? 2 : 1);         // a lane's 16-byte words of an 8-row query tile
   static constexpr int kTileBytes = kWords * 32 * 16 + 32;  // and the tile's 8 lse
-  static constexpr int kTiles = 65536 / kTileBytes;         // query tiles held at a time
 };
 
+// A request in the list: its first group, its root's tokens, its history.
+struct __align__(16) MassReq {
+  long long group0;
+  int t0, root, hist, slot;
+};
+
+__device__ __forceinline__ void copy_async16(uint32_t dst, const void *src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+
 template <int D, bool F8>
-__global__ void __launch_bounds__(kMassWarps * 32, 2) mass_kernel_mma(const MassParams p) {
+__global__ void __launch_bounds__(kMassWarps * 32, 1) mass_kernel_mma(const MassParams p) {
   using S = MassShape<D, F8>;
-  extern __shared__ uint4 qs[];  // [kTiles][kWords][32], then lse [kTiles][8], then the unit prefix
+  extern __shared__ uint4 qs[];  // [held][kWords][32], lse [held][8], the warps' rings, the list
   __shared__ long long part[32];
-  float *ls = reinterpret_cast<float *>(qs + S::kTiles * S::kWords * 32);
-  long long *unit0 = reinterpret_cast<long long *>(ls + S::kTiles * 8);
+  float *ls = reinterpret_cast<float *>(qs + p.held * S::kWords * 32);
+  uint4 *rings = reinterpret_cast<uint4 *>(ls + p.held * 8);
+  MassReq *list = reinterpret_cast<MassReq *>(rings + kMassWarps * (kRing / 16));
   const flide_tree_index &x = p.x;
-  if (failed(x.status)) return;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3, R = x.R;
-  request_prefix(R, [&](int r) { return mass_units(p, r, kMassUnit, blockIdx.x == 0); }, unit0, part);
-  const long long U = unit0[R];
-  const float sk = F8 ? p.descale[0] * p.descale[1] : 1.f;
-  const float qk_scale = p.scale * sk * kLog2eM;
-  const long long u_end = (blockIdx.x + 1) * U / gridDim.x;
-  int held_r = -1, held_b = -1;  // request and batch of query tiles in shared memory
-  for (long long u = blockIdx.x * U / gridDim.x; u < u_end; ++u) {
-    const int r = request_of(unit0, R, u);
-    int t0, slot;
-    const int root = root_tokens(x, r, &t0);
-    const int n = history_rows(x, p.hist, r, false, &slot);
-    slot = p.hist.req_slot[r];
-    const int past_units = (n + kMassUnit - 1) / kMassUnit, cu = (int)(u - unit0[r]);
-    const bool fresh = cu >= past_units;
-    const int len = fresh ? root : n;
-    const int k0 = (fresh ? cu - past_units : cu) * kMassUnit + 16 * warp;
-    const int rows = root * p.G, per = (rows + 7) / 8, tiles = p.Hkv * per;  // tile = head * per + row tile
-    long long row = -1;
-    if (k0 < len) row = fresh ? (long long)t0 + k0 : history_row(x, p.hist, slot, k0);
-    const char *base = static_cast<const char *>(fresh ? p.k : p.pool_k) + 16 * c;
-    const bool ok[2] = {row >= 0 && k0 + g < len, row >= 0 && k0 + g + 8 < len};
-    auto load = [&](int h, uint4 (&kr)[2][S::kCj]) {
+  if (__syncthreads_or(tid == 0 && failed(x.status))) return;
+  {
+    long long *group0 = &list[0].group0;  // every fourth 8-byte word of the list
+    request_prefix(R, [&](int r) -> long long {
+      MassReq &q = list[r];
+      const long long n = mass_units(p, r, 16, blockIdx.x == 0);
+      q.root = root_tokens(x, r, &q.t0);
+      int base;
+      q.hist = history_rows(x, p.hist, r, false, &base);
+      q.slot = p.hist.req_slot[r];
+      return n;
+    }, group0, part, sizeof(MassReq) / sizeof(long long));
+  }
+  const long long N = list[R].group0;
+  const float qk_scale = p.scale * (F8 ? p.descale[0] * p.descale[1] : 1.f) * kLog2eM;
+  uint4 *ring = rings + warp * (kRing / 16) + lane;
+  long long u = blockIdx.x * N / gridDim.x;
+  const long long u_end = (blockIdx.x + 1) * N / gridDim.x;
+  while (u < u_end) {
+    int r = 0;
+    for (int hi = R; r < hi;) {
+      const int mid = (r + hi) >> 1;
+      if (list[mid + 1].group0 > u) hi = mid; else r = mid + 1;
+    }
+    const MassReq q = list[r];
+    const int ga = (int)(u - q.group0), gb = (int)min(list[r + 1].group0 - q.group0, ga + (u_end - u));
+    u += gb - ga;
+    const int past_groups = (q.hist + 15) / 16;
+    const int rows = q.root * p.G, per = (rows + 7) / 8, tiles = p.Hkv * per;  // tile = head * per + row tile
+    float *out = p.mass_out + (size_t)q.slot * p.hist.max_blocks * p.hist.block_rows;
+    const float *in = p.mass + (size_t)q.slot * p.hist.max_blocks * p.hist.block_rows;
+    for (int b0 = 0; b0 < tiles; b0 += p.held) {
+      const int b1 = min(tiles, b0 + p.held), h0 = b0 / per, heads = (b1 - 1) / per - h0 + 1;
+      // this warp's groups ga + warp, ga + warp + kMassWarps, ...; steps (group, head) go into
+      // the ring in order.  Row of a group's first history row, or -1: its first stream row.
+      auto row_of = [&](int grp) -> long long {
+        if (grp >= gb) return -1;
+        return grp < past_groups ? history_row(x, p.hist, q.slot, 16 * grp) : q.t0 + 16 * (grp - past_groups);
+      };
+      int ig = ga + warp, ih = 0;  // the next step to copy: group, head (from h0)
+      long long inext = row_of(ig);
+      const char *src[2];          // its rows g and g + 8 (on: history or root has them)
+      bool on[2];
+      auto group = [&]() {
+        const bool fresh = ig >= past_groups;
+        const int left = (fresh ? q.root : q.hist) - 16 * (fresh ? ig - past_groups : ig);
+        const char *base = static_cast<const char *>(fresh ? p.k : p.pool_k) + 16 * c + (size_t)h0 * S::kRow;
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int j = 0; j < S::kCj; ++j)
-          kr[t][j] = ok[t] ? sm100::ld_stream(base + ((size_t)(row + g + 8 * t) * p.Hkv + h) * S::kRow + 64 * j)
-                           : make_uint4(0u, 0u, 0u, 0u);
-    };
-    uint4 kr[2][S::kCj], nx[2][S::kCj];
-    load(0, nx);
-    float acc[2] = {0.f, 0.f};  // rows k0 + g, k0 + g + 8
-    int head = -1;
-    for (int b0 = 0; b0 < tiles; b0 += S::kTiles) {
-      const int b1 = min(tiles, b0 + S::kTiles);
-      if (held_r != r || held_b != b0) {
-        __syncthreads();
-        for (int e = tid; e < (b1 - b0) * S::kCj * 32; e += kMassWarps * 32) {
-          const int q = e / (S::kCj * 32), j = e / 32 % S::kCj, l = e & 31;
-          const int h = (b0 + q) / per, qr = (b0 + q) % per * 8 + (l >> 2);
-          uint4 v = make_uint4(0u, 0u, 0u, 0u);
-          const size_t at = (size_t)(t0 + qr / p.G) * p.Hq + h * p.G + qr % p.G;
-          if (qr < rows)
-            v = *reinterpret_cast<const uint4 *>(static_cast<const char *>(p.q) + at * S::kRow + 64 * j + 16 * (l & 3));
-          if (F8) {
-            qs[(q * S::kWords + 2 * j) * 32 + l] = make_uint4(sm100::e4m3x2_to_half2(v.x), sm100::e4m3x2_to_half2(v.x >> 16),
-                                                              sm100::e4m3x2_to_half2(v.y), sm100::e4m3x2_to_half2(v.y >> 16));
-            qs[(q * S::kWords + 2 * j + 1) * 32 + l] = make_uint4(sm100::e4m3x2_to_half2(v.z), sm100::e4m3x2_to_half2(v.z >> 16),
-                                                                  sm100::e4m3x2_to_half2(v.w), sm100::e4m3x2_to_half2(v.w >> 16));
-          } else {
-            qs[(q * S::kWords + j) * 32 + l] = v;
-          }
-          if (j == 0 && (l & 3) == 0) ls[q * 8 + (l >> 2)] = qr < rows ? p.lse[at] * kLog2eM : INFINITY;
+        for (int t = 0; t < 2; ++t) {
+          on[t] = inext >= 0 && g + 8 * t < left;
+          src[t] = base + (size_t)(on[t] ? inext + g + 8 * t : 0) * p.Hkv * S::kRow;
         }
-        __syncthreads();
-        held_r = r;
-        held_b = b0;
-      }
-      for (int q = b0; q < b1; ++q) {
-        const int h = q / per;
-        if (h != head) {
-          head = h;
+        inext = row_of(ig + kMassWarps);  // looked up a group ahead
+      };
+      group();
+      const uint32_t ring0 = smem_u32(ring);
+      uint32_t to = ring0;         // the next stage
+      auto copy = [&]() {
+        if (ig < gb) {
 #pragma unroll
           for (int t = 0; t < 2; ++t)
 #pragma unroll
-            for (int j = 0; j < S::kCj; ++j) kr[t][j] = nx[t][j];
-          if (h + 1 < p.Hkv) load(h + 1, nx);
-        }
-        float s[4] = {0.f, 0.f, 0.f, 0.f};
-        const uint4 *qt = qs + (q - b0) * S::kWords * 32 + lane;
-#pragma unroll
-        for (int j = 0; j < S::kWords; ++j) {
-          const uint4 b = qt[j * 32];
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            uint32_t a[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              if (F8) {  // word 2 (j % 2) + i of load j / 2: its low and high code pairs
-                const uint32_t v = sm100::word_of(kr[k & 1][j / 2], 2 * (j % 2) + i);
-                a[k] = sm100::e4m3x2_to_half2(k >> 1 ? v >> 16 : v);
-              } else {
-                a[k] = sm100::word_of(kr[k & 1][j], 2 * i + (k >> 1));
-              }
-            }
-            sm100::mma16816<F8>(s, a[0], a[1], a[2], a[3], i ? b.z : b.x, i ? b.w : b.y);
+            for (int j = 0; j < S::kCj; ++j)
+              copy_async16(to + (t * S::kCj + j) * 512, src[t] + 64 * j, on[t]);
+          src[0] += S::kRow;
+          src[1] += S::kRow;
+          to += 2 * S::kCj * 512;
+          if (to == ring0 + S::kStages * 2 * S::kCj * 512) to = ring0;
+          if (++ih == heads) {
+            ih = 0;
+            ig += kMassWarps;
+            group();
           }
         }
-        const int r0 = q % per * 8 + 2 * c;
-        const float2 l2 = *reinterpret_cast<const float2 *>(ls + (q - b0) * 8 + 2 * c);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+      };
+#pragma unroll 1
+      for (int k = 0; k < S::kStages - 1; ++k) copy();  // on their way while the queries come
+      __syncthreads();  // the tiles held before are done with
+      for (int e = tid; e < (b1 - b0) * S::kCj * 32; e += kMassWarps * 32) {
+        const int t = e / (S::kCj * 32), j = e / 32 % S::kCj, l = e & 31;
+        const int h = (b0 + t) / per, qr = (b0 + t) % per * 8 + (l >> 2);
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        const size_t at = (size_t)(q.t0 + qr / p.G) * p.Hq + h * p.G + qr % p.G;
+        if (qr < rows)
+          v = *reinterpret_cast<const uint4 *>(static_cast<const char *>(p.q) + at * S::kRow + 64 * j + 16 * (l & 3));
+        uint4 *to = qs + t * S::kWords * 32 + l;
+        if (F8) {
+          to[2 * j * 32] = make_uint4(e4m3x2_to_half2(v.x), e4m3x2_to_half2(v.x >> 16), e4m3x2_to_half2(v.y),
+                                      e4m3x2_to_half2(v.y >> 16));
+          to[(2 * j + 1) * 32] = make_uint4(e4m3x2_to_half2(v.z), e4m3x2_to_half2(v.z >> 16), e4m3x2_to_half2(v.w),
+                                            e4m3x2_to_half2(v.w >> 16));
+        } else {
+          to[j * 32] = v;
+        }
+        if (j == 0 && (l & 3) == 0) ls[t * 8 + (l >> 2)] = qr < rows ? p.lse[at] * kLog2eM : INFINITY;
+      }
+      __syncthreads();
+      int st = 0;
+      for (int grp = ga + warp; grp < gb; grp += kMassWarps) {
+        const bool fresh = grp >= past_groups;
+        const int i0 = 16 * (fresh ? grp - past_groups : grp), len = fresh ? q.root : q.hist;
+        float acc[2] = {0.f, 0.f};  // rows i0 + g, i0 + g + 8
+        for (int hh = 0; hh < heads; ++hh) {
+          asm volatile("cp.async.wait_group %0;" ::"n"(S::kStages - 2) : "memory");
+          uint4 kr[2][S::kCj];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float e = sm100::ex2_approx(fmaf(s[i], qk_scale, -(i & 1 ? l2.y : l2.x)));
-          // a root row is seen by its own token and later ones
-          if (fresh && (r0 + (i & 1)) / p.G < k0 + g + 8 * (i >> 1)) e = 0.f;
-          acc[i >> 1] += e;
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int j = 0; j < S::kCj; ++j) kr[t][j] = ring[((st * 2 + t) * S::kCj + j) * 32];
+          if (++st == S::kStages) st = 0;
+          copy();  // into the stage taken one step ago
+          const int h = h0 + hh;
+          // query tiles two at a time: two chains of products over the same rows
+          const int t1 = min(b1, (h + 1) * per);
+          for (int t = max(b0, h * per); t < t1; t += 2) {
+            float s[2][4] = {};
+            const uint4 *qt = qs + (t - b0) * S::kWords * 32 + lane;
+            const int two = t + 1 < t1 ? S::kWords * 32 : 0;  // (a last odd tile twice, its second sum unused)
+#pragma unroll
+            for (int j = 0; j < S::kWords; ++j) {
+              const uint4 q0 = qt[j * 32], q1 = qt[j * 32 + two];
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                uint32_t a[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  if (F8) {  // word 2 (j % 2) + i of load j / 2: its low and high code pairs
+                    const uint32_t v = word_of(kr[k & 1][j / 2], 2 * (j % 2) + i);
+                    a[k] = e4m3x2_to_half2(k >> 1 ? v >> 16 : v);
+                  } else {
+                    a[k] = word_of(kr[k & 1][j], 2 * i + (k >> 1));
+                  }
+                }
+                mma16816<F8>(s[0], a[0], a[1], a[2], a[3], i ? q0.z : q0.x, i ? q0.w : q0.y);
+                mma16816<F8>(s[1], a[0], a[1], a[2], a[3], i ? q1.z : q1.x, i ? q1.w : q1.y);
+              }
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              if (k && !two) break;
+              const int r0 = (t + k - h * per) * 8 + 2 * c;
+              const float2 l2 = *reinterpret_cast<const float2 *>(ls + (t + k - b0) * 8 + 2 * c);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                float e = ex2_approx(fmaf(s[k][i], qk_scale, -(i & 1 ? l2.y : l2.x)));
+                // a root row is seen by its own token and later ones
+                if (fresh && (r0 + (i & 1)) / p.G < i0 + g + 8 * (i >> 1)) e = 0.f;
+                acc[i >> 1] += e;
+              }
+            }
+          }
+        }
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          acc[t] += __shfl_xor_sync(0xffffffffu, acc[t], 1);
+          acc[t] += __shfl_xor_sync(0xffffffffu, acc[t], 2);
+          const int i = i0 + g + 8 * t;
+          if (c == 0 && i < len) {
+            const int at = (fresh ? q.hist : 0) + i;
+            // (a later batch of query tiles adds to the first one's sum)
+            out[at] = b0 > 0 ? out[at] + acc[t] : fresh ? acc[t] : in[at] + acc[t];
+          }
         }
       }
-    }
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      acc[t] += __shfl_xor_sync(0xffffffffu, acc[t], 1);
-      acc[t] += __shfl_xor_sync(0xffffffffu, acc[t], 2);
-      if (c == 0 && ok[t]) {
-        const size_t at = (size_t)slot * p.hist.max_blocks * p.hist.block_rows + (fresh ? n : 0) + k0 + g + 8 * t;
-        p.mass_out[at] = fresh ? acc[t] : p.mass[at] + acc[t];
-      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
     }
   }
 }
 
 template <int D, bool F8>
-int mass_mma_launch(const MassParams &p, int dev, int sms, cudaStream_t s) {
-  const size_t smem = (size_t)MassShape<D, F8>::kTiles * MassShape<D, F8>::kTileBytes + (size_t)(p.x.R + 1) * 8;
+int mass_mma_launch(MassParams &p, int dev, int sms, cudaStream_t s) {
+  using S = MassShape<D, F8>;
   if (!allow_smem<mass_kernel_mma<D, F8>>(dev)) return FLIDE_ERR_CUDA;
-  mass_kernel_mma<D, F8><<<2 * sms, kMassWarps * 32, smem, s>>>(p);
+  // what the rings and the list (2048 requests: 64 KB) leave, for all query tiles
+  // that a request may have if they fit
+  const int fixed = kMassWarps * kRing + (p.x.R + 1) * (int)sizeof(MassReq);
+  p.held = min((231000 - fixed) / S::kTileBytes, p.Hkv * (((int)min((long long)p.x.T * p.G, 1ll << 20) + 7) / 8));
+  mass_kernel_mma<D, F8><<<sms, kMassWarps * 32, (size_t)fixed + p.held * S::kTileBytes, s>>>(p);
   FLIDE_LAUNCH_CHECK();
   return FLIDE_OK;
 }
@@ -488,7 +570,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_copy_kernel(const EvictPar
       for (int k = 0; k < kUnroll; ++k) {
         const int w = w0 + 32 * k;
         if (w < 2 * words)
-          v[k] = sm100::ld_stream((w < words ? p.pool_k : p.pool_v) + a + 16 * (size_t)(w < words ? w : w - words));
+          v[k] = ld_stream((w < words ? p.pool_k : p.pool_v) + a + 16 * (size_t)(w < words ? w : w - words));
       }
 #pragma unroll
       for (int k = 0; k < kUnroll; ++k) {

@@ -8,17 +8,18 @@ namespace flide {
 
 constexpr int kMaxListR = 2048;  // requests of a work list
 
-// pref[r] = sum of count(0 .. r-1), pref[R] = the total; 64 bits, because a
-// long history's units times its heads pass 2^31.  `part` holds a block's
-// thread sums (blockDim.x <= 1024 entries); ends with a barrier.
+// pref[r * step] = sum of count(0 .. r-1), pref[R * step] = the total; 64 bits,
+// because a long history's units times its heads pass 2^31.  `part` holds the
+// warps' sums (32 entries); ends with a barrier.
 template <typename F>
-__device__ __forceinline__ void request_prefix(int R, F count, long long *pref, long long *part) {
+__device__ __forceinline__ void request_prefix(int R, F count, long long *pref, long long *part,
+                                               int step = 1) {
   const int nt = blockDim.x, per = (R + nt - 1) / nt, tid = threadIdx.x;
   const int lo = min(R, tid * per), hi = min(R, lo + per);
   long long sum = 0;
   for (int r = lo; r < hi; ++r) {
     const long long c = count(r);
-    pref[r] = c;
+    pref[(size_t)r * step] = c;
     sum += c;
   }
   const int lane = tid & 31, warp = tid >> 5;
@@ -33,11 +34,11 @@ __device__ __forceinline__ void request_prefix(int R, F count, long long *pref, 
   long long base = incl - sum;
   for (int w = 0; w < warp; ++w) base += part[w];
   for (int r = lo; r < hi; ++r) {
-    const long long c = pref[r];
-    pref[r] = base;
+    const long long c = pref[(size_t)r * step];
+    pref[(size_t)r * step] = base;
     base += c;
   }
-  if (tid == nt - 1) pref[R] = base;
+  if (tid == nt - 1) pref[(size_t)R * step] = base;
   __syncthreads();
 }
 
