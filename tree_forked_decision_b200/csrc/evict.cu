@@ -397,8 +397,17 @@ constexpr int kBits = 11;  // 3 passes over 32-bit codes
 constexpr int kBins = 1 << kBits;
 
 // One block per request: the code of the smallest kept mass by radix selection
-// over the rows between sinks and recent, then the kept rows in order.
+// over the rows between sinks and recent, then the kept rows in order.  A thread
+// has kEach neighbouring rows of a chunk, so one scan places a whole chunk; the
+// first chunk is read once and stays in registers for all passes (longer histories
+// read the others again).  The kept rows are gathered in shared memory and stored
+// from there: a thread's own stores lie kEach rows apart, a line each, and took
+// most of 21 us for 16384 rows.
+template <int kEach>
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictParams p) {
+  constexpr int kChunk = kEach * kSelThreads;
+  extern __shared__ int kept_s[];  // [kChunk], then their masses
+  float *mass_s = reinterpret_cast<float *>(kept_s + kChunk);
   __shared__ int hist[kBins];
   __shared__ int scratch[40];
   __shared__ int s_dup, s_bin, s_left;
@@ -420,19 +429,36 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
   const size_t at = (size_t)p.req_slot[r] * p.max_blocks * p.block_rows;
   const float *mass = p.mass + at;
   float *mass_out = p.mass_out + at;
-  const bool all = len <= p.budget;
+  float v[kEach];
+  auto load = [&](int base) {
+    const int i0 = base + kEach * tid;
+    if (i0 + kEach <= len && (at & 3) == 0 && ((uintptr_t)p.mass & 15) == 0) {
+#pragma unroll
+      for (int k = 0; k < kEach; k += 4) *reinterpret_cast<float4 *>(v + k) = *reinterpret_cast<const float4 *>(mass + i0 + k);
+    } else {
+#pragma unroll
+      for (int k = 0; k < kEach; ++k) v[k] = i0 + k < len ? mass[i0 + k] : 0.f;
+    }
+  };
+  load(0);
+  const bool one = len <= kChunk, all = len <= p.budget;
   const int lo = all ? 0 : p.sinks, hi = all ? 0 : len - p.recent;  // candidates
   int want = all ? 0 : p.budget - p.sinks - p.recent;
   const bool any = want > 0;
   uint32_t prefix = 0, mask = 0;  // codes still in question: (code & mask) == prefix
-  if (want > 0) {
+  if (any) {
     for (int shift = 32 - kBits; ; shift = max(0, shift - kBits)) {
       const uint32_t bins = mask == 0 || shift > 0 ? kBins : 1u << (32 - 2 * kBits);
       for (int b = tid; b < kBins; b += kSelThreads) hist[b] = 0;
       __syncthreads();
-      for (int i = lo + tid; i < hi; i += kSelThreads) {
-        const uint32_t c = mass_code(mass[i]);
-        if ((c & mask) == prefix) atomicAdd(&hist[(c >> shift) & (bins - 1)], 1);
+      for (int base = 0; base < len; base += kChunk) {
+        if (!one) load(base);
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+          const int i = base + kEach * tid + k;
+          const uint32_t c = mass_code(v[k]);
+          if (i >= lo && i < hi && (c & mask) == prefix) atomicAdd(&hist[(c >> shift) & (bins - 1)], 1);
+        }
       }
       __syncthreads();
       // bins from the top: thread b holds bins kBins-1-2b and kBins-2-2b
@@ -450,43 +476,50 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
       want = s_left;  // of the chosen bin's rows
       prefix |= (uint32_t)s_bin << shift;
       mask |= (bins - 1) << shift;
-      __syncthreads();
       if (shift == 0) break;
     }
   }
   // rows above the threshold, the first `want` at it, and the fixed ones: row i
   // goes to (sure rows before it) + min(ties before it, want), so one scan of
-  // both counts places four rows a thread.  The masses of a chunk are read
-  // before its scan and written after it, to places not past them: in place works.
+  // both counts places a chunk.  A chunk's masses are read before its scan and
+  // written after it, to places not past them: in place works.
   int out = 0, ties = 0;
-  for (int i0 = 0; i0 < len; i0 += 4 * kSelThreads) {
-    const int i = i0 + 4 * tid;
-    float v[4];
-    int sure = 0, tie = 0;  // bit k: row i + k
+  for (int base = 0; base < len; base += kChunk) {
+    if (!one) load(base);
+    const int i0 = base + kEach * tid;
+    uint32_t sure = 0, tie = 0;  // bit k: row i0 + k
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      v[k] = i + k < len ? mass[i + k] : 0.f;
-      if (i + k >= len) continue;
+    for (int k = 0; k < kEach; ++k) {
+      const int i = i0 + k;
+      if (i >= len) continue;
       const uint32_t c = mass_code(v[k]);
-      if (all || i + k < lo || i + k >= hi || (any && c > prefix)) sure |= 1 << k;
-      else if (any && c == prefix) tie |= 1 << k;
+      if (all || i < lo || i >= hi || (any && c > prefix)) sure |= 1u << k;
+      else if (any && c == prefix) tie |= 1u << k;
     }
     int tot;
     const int before = block_excl_scan(__popc(sure) | __popc(tie) << 16, scratch, &tot);
+    const int first = out + min(ties, want);  // the chunk's first place
     int s = out + (before & 0xffff), e = ties + (before >> 16);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const bool at = tie >> k & 1;
-      if ((sure >> k & 1) || (at && e < want)) {
-        const int j = s + min(e, want);
-        kept[j] = i + k;
-        mass_out[j] = v[k];
+    for (int k = 0; k < kEach; ++k) {
+      const bool even = tie >> k & 1;
+      if ((sure >> k & 1) || (even && e < want)) {
+        const int j = s + min(e, want) - first;
+        kept_s[j] = i0 + k;
+        mass_s[j] = v[k];
       }
       s += sure >> k & 1;
-      e += at;
+      e += even;
     }
     out += tot & 0xffff;
     ties += tot >> 16;
+    const int n = out + min(ties, want) - first;
+    __syncthreads();
+    for (int j = tid; j < n; j += kSelThreads) {
+      kept[first + j] = kept_s[j];
+      mass_out[first + j] = mass_s[j];
+    }
+    __syncthreads();
   }
   out += min(ties, want);
   for (int j = out + tid; j < p.budget; j += kSelThreads) kept[j] = -1;
@@ -681,7 +714,14 @@ int flide_history_evict(int32_t R, const int32_t *req_slot, int32_t n_slots, con
   p.status = status;
   p.row_bytes = (int)row_bytes;
   cudaStream_t s = (cudaStream_t)stream;
-  evict_select_kernel<<<R, kSelThreads, 0, s>>>(p);
+  // few rows a thread for short histories: 4 of 4096 (2304 rows: 8 us, with 16 of
+  // 16384 13 us)
+  if ((int64_t)max_blocks * block_rows <= 4 * kSelThreads) {
+    evict_select_kernel<4><<<R, kSelThreads, 8 * 4 * kSelThreads, s>>>(p);
+  } else {
+    if (!allow_smem<evict_select_kernel<16>>(dev)) return FLIDE_ERR_CUDA;
+    evict_select_kernel<16><<<R, kSelThreads, 8 * 16 * kSelThreads, s>>>(p);
+  }
   FLIDE_LAUNCH_CHECK();
   if (dst_k != pool_k && dst_v != pool_v) {
     const unsigned blocks = (unsigned)min(((int64_t)budget + 7) / 8, max((int64_t)1, (int64_t)16 * sms / R));
