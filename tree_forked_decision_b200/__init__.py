@@ -37,8 +37,17 @@ Further calls: ``fork_attn_fp8`` and
 ``branch_logprob`` / ``option_probs`` (decision probabilities over the
 options), ``schedule.BoundedGdn`` (GDN under a node-state memory budget) and
 ``graphs.GraphBuckets`` (captured CUDA graphs per shape bucket).
+
+Decoding with drafted tokens over a long history (a root of committed tokens and
+a small tree below it per request): ``rope`` (rotary positions of the tree),
+``draft_attn`` / ``draft_attn_paged`` (its few tokens over the whole history),
+``verify_draft`` (accepted tokens and the next one, from the target's
+probabilities and given random numbers), ``history_mass`` and ``history_evict``
+(a bound on the history by the attention weight its rows gathered);
+``history.HistoryStore`` has the step in its docstring.
 """
 from .flide import (DeviceTree, FlideError, TreeIndex, amax, branch_logprob,  # noqa: F401
-                    fork_attn, fork_attn_fp8, fork_attn_paged, fork_gdn, fork_gdn_fp8, load,
-                    option_probs,
-                    quantize_e4m3, state_resume, state_save, state_slots, tree_build)
+                    draft_attn, draft_attn_paged, draft_attn_workspace, fork_attn, fork_attn_fp8,
+                    fork_attn_paged, fork_gdn, fork_gdn_fp8, history_evict, history_mass, load,
+                    option_probs, quantize_e4m3, rope, rope_freqs, state_resume, state_save,
+                    state_slots, tree_build, verify_draft)

@@ -81,8 +81,12 @@ __device__ __forceinline__ bool draft_list(const DraftParams &p, DraftReq *list,
   for (int r = lo; r < hi; ++r) {
     if (r > lo) first(r);
     DraftReq q;
+    // debug build: the request's nodes lie among the tree's, its tokens in the stream
+    const int N = x.counts[FLIDE_CNT_N];
+    if (!in_bounds(x.status, x.counts, n0, N + 1, 802) || !in_bounds(x.status, x.counts, n1, N + 1, 802)) n0 = n1 = 0;
     q.t0 = n1 > n0 ? x.node_start[n0] : 0;
     q.tokens = n1 > n0 ? x.node_start[n1] - q.t0 : 0;
+    if (!in_bounds(x.status, x.counts, (long long)q.t0 + q.tokens, x.counts[FLIDE_CNT_T] + 1ll, 803)) q.tokens = 0;
     int code = 0;
     q.hist = history_length(p.hist, p0, p1 - p0, slot, &q.base, &code);
     if (code && blockIdx.x == 0) set_status(x.status, code);

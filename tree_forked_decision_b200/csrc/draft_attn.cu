@@ -481,7 +481,7 @@ __global__ void __launch_bounds__(256) draft_join_portable(const DraftParams p) 
   }
   float m = -INFINITY, l = 0.f;
   for (int a = x.anc_ptr[n]; a < x.anc_ptr[n + 1]; ++a) {
-    const int node = x.anc_node[a];
+    const int node = (int)checked(x.status, x.counts, x.anc_node[a], x.counts[FLIDE_CNT_N], 804);
     const int e = node == n ? t + 1 : x.node_start[node + 1];
     for (int j = x.node_start[node]; j < e; ++j) {
       const size_t at = ((size_t)j * p.Hkv + hk) * d + lane;
@@ -601,7 +601,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) draft_join_kernel(const Dr
     for (int a0 = x.anc_ptr[n]; a0 < a1; a0 += 32) {
       int first = 0, len = 0;  // this lane's ancestor: its keys
       if (a0 + lane < a1) {
-        const int node = x.anc_node[a0 + lane];
+        const int node = (int)checked(x.status, x.counts, x.anc_node[a0 + lane], x.counts[FLIDE_CNT_N], 804);
         first = x.node_start[node];
         len = (node == n ? t + 1 : x.node_start[node + 1]) - first;
       }
@@ -613,7 +613,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) draft_join_kernel(const Dr
         const int cnt = min(kPath, total - b0);
         for (int k0 = 0; k0 < cnt; k0 += 4) {
           const bool on = k0 + grp < cnt;
-          const size_t at = ((size_t)path[on ? k0 + grp : 0] * p.Hkv + hk) * D;
+          const int key = (int)checked(x.status, x.counts, path[on ? k0 + grp : 0], x.counts[FLIDE_CNT_T], 805);
+          const size_t at = ((size_t)key * p.Hkv + hk) * D;
           uint4 kw[Row::kWords], vw[Row::kWords];
           Row::load(K + at, l8, kw);
           Row::load(Vs + at, l8, vw);

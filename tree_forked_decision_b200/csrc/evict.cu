@@ -43,9 +43,14 @@ constexpr int kMKeys = 32;
 constexpr int kMThreads = 128;
 
 __device__ __forceinline__ int root_tokens(const flide_tree_index &x, int r, int *t0) {
-  const int n0 = x.req_node[r], n1 = x.req_node[r + 1];
-  *t0 = n1 > n0 ? x.node_start[n0] : 0;
-  return n1 > n0 ? x.node_start[n0 + 1] - *t0 : 0;
+  const int n0 = x.req_node[r], n1 = x.req_node[r + 1], N = x.counts[FLIDE_CNT_N];
+  *t0 = 0;
+  // debug build: the root lies among the tree's nodes, its tokens in the stream
+  if (n1 <= n0 || !in_bounds(x.status, x.counts, n0, N, 811)) return 0;
+  const int end = x.node_start[n0 + 1];
+  if (!in_bounds(x.status, x.counts, end, x.counts[FLIDE_CNT_T] + 1ll, 812)) return 0;
+  *t0 = x.node_start[n0];
+  return end - *t0;
 }
 
 __device__ __forceinline__ long long mass_units(const MassParams &p, int r, int unit, bool report) {

@@ -103,8 +103,11 @@ verify_kernel(const VerifyParams p) {
   // token), so one block's reading decides for its whole cluster
   if (tid == 0) sh.stop = failed(x.status);
   cluster.sync();
-  const bool stop = *cluster.map_shared_rank(&sh.stop, 0) != 0;
-  const int n0 = x.req_node[r], n1 = x.req_node[r + 1];
+  bool stop = *cluster.map_shared_rank(&sh.stop, 0) != 0;
+  // debug build: the request's nodes lie among the tree's (the same finding in every block)
+  const int N = stop ? 0 : x.counts[FLIDE_CNT_N];
+  int n0 = stop ? 0 : x.req_node[r], n1 = stop ? 0 : x.req_node[r + 1];
+  if (!in_bounds(x.status, x.counts, n0, N + 1, 901) || !in_bounds(x.status, x.counts, n1, N + 1, 901)) n0 = n1 = 0;
   const int first = n1 > n0 ? x.node_start[n0] : 0, end = n1 > n0 ? x.node_start[n1] : 0;
   const int nn = n1 - n0;
   if (rank == 0 && !stop)
@@ -120,7 +123,8 @@ verify_kernel(const VerifyParams p) {
   }
   for (int i = tid; i <= nn; i += kVThreads) {
     sh.start[i] = x.node_start[n0 + i];
-    if (i < nn) sh.parent[i] = (int16_t)(i == 0 ? -1 : x.anc_node[x.anc_ptr[n0 + i + 1] - 2] - n0);
+    if (i < nn)
+      sh.parent[i] = (int16_t)(i == 0 ? -1 : checked(x.status, x.counts, x.anc_node[x.anc_ptr[n0 + i + 1] - 2] - n0, i, 902));
   }
   __syncthreads();
 
@@ -149,7 +153,7 @@ verify_kernel(const VerifyParams p) {
     return k;
   };
   for (int i = tid; i < min(kHeld, end - branch); i += kVThreads) {
-    const int row = branch + i, m = x.token_node[row] - n0;
+    const int row = branch + i, m = (int)checked(x.status, x.counts, x.token_node[row] - n0, nn, 903);
     const Candidate k = look_up(row, row > sh.start[m] ? row - 1 : sh.start[sh.parent[m] + 1] - 1);
     sh.tok[i] = k.tok;
     sh.u[i] = k.u;
