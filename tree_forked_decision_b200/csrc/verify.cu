@@ -71,7 +71,7 @@ struct VerifyShared {
   int kid_token[kMaxKids];
   double seg[kMaxSegs];
   double warp[kVWarps];
-  double total[2];        // this block's part of a sum, by parity of the exchange
+  double total[2][16];    // the blocks' parts of a sum, by parity of the exchange
   int stop;
 };
 
@@ -214,7 +214,7 @@ verify_kernel(const VerifyParams p) {
     }
   };
   // sum of the weights over the vocabulary, the same bits in every block;
-  // leaves each segment's sum in sh.seg and each block's in its sh.total
+  // leaves each segment's sum in sh.seg and the blocks' in sh.total
   auto sum_weights = [&](const T *prow, const T *qrow) -> double {
     __syncthreads();
     if (sampled && c > 0.) sum_segments(prow, qrow, Kind<1>{});
@@ -225,11 +225,12 @@ verify_kernel(const VerifyParams p) {
       double acc = 0.;
       for (int s = lane; s < n_seg; s += 32) acc += sh.seg[s];
       acc = warp_sum_d(acc);
-      if (lane == 0) sh.total[flip] = acc;
+      // every block gets a copy: nothing remote is read after the barrier
+      if (lane < blocks) cluster.map_shared_rank(&sh.total[flip][0], lane)[rank] = acc;
     }
     cluster.sync();
     double all = 0.;
-    for (int b = 0; b < blocks; ++b) all += cluster.map_shared_rank(sh.total, b)[flip];
+    for (int b = 0; b < blocks; ++b) all += sh.total[flip][b];
     flip ^= 1;
     return all;
   };
@@ -320,14 +321,13 @@ verify_kernel(const VerifyParams p) {
   double before = 0.;
   int owner = -1, last = -1;
   for (int b = 0; b < blocks; ++b) {
-    const double t = cluster.map_shared_rank(sh.total, b)[flip];
+    const double t = sh.total[flip][b];
     if (t > 0.) last = b;
     if (owner < 0) {
       if (before + t > aim) owner = b;
       else before += t;
     }
   }
-  cluster.sync();  // every block has read the totals
   const bool fell = owner < 0;  // rounding put the aim past the end
   if (fell) owner = last;
   if (rank == 0 && tid == 0) {
