@@ -670,7 +670,8 @@ int flide_history_mass(const void *q, const void *k, const float *lse, const voi
  * n_slots or listed twice, a length outside [0, max_blocks * block_rows] (those
  * requests are left as they are) or a row without a block.  Host errors:
  * FLIDE_ERR_SHAPE (also budget <= 0, sinks + recent > budget),
- * FLIDE_ERR_CAPACITY (more than 4096 requests), FLIDE_ERR_CUDA. */
+ * FLIDE_ERR_CAPACITY (more than 4096 requests, a pool or a history of more than
+ * 2^31 - 1 rows), FLIDE_ERR_CUDA. */
 int flide_history_evict(int32_t R, const int32_t *req_slot, int32_t n_slots, const int32_t *hist_len,
                         const int32_t *block_table, int32_t max_blocks, int32_t block_rows,
                         const void *pool_k, const void *pool_v, int32_t n_blocks, int32_t Hkv,
