@@ -116,6 +116,8 @@ def test_episode(block_rows):
             at = table[s][torch.arange(n) // block_rows].long() * block_rows + torch.arange(n) % block_rows
             assert torch.equal(store.pool_k.cpu()[at], past_k[r]) and torch.equal(store.pool_v.cpu()[at], past_v[r])
             assert np.allclose(store.mass.cpu()[s, :n].numpy(), mass[r], rtol=1e-5)
+            if len([i for i in kept[r].tolist() if i >= 0]) == budget:  # rows to come start without weight
+                assert not bool(store.mass[s, budget:].any())
         assert store.pos_offset(slots).tolist() == gone
         assert store.free_blocks() == R * width + 1 - sum(-(-store.length(s) // block_rows) for s in slots)
         roots = new_roots

@@ -87,6 +87,8 @@ class HistoryStore:
     def release(self, slot: int):
         flide._check(self._lib.flide_pool_release(self._pool, slot), "flide_pool_release")
         self.evicted_h[slot] = 0
+        if self.mass is not None:
+            self.mass[slot].zero_()
         self._sync_table()
 
     def _sync_table(self):
@@ -185,6 +187,7 @@ class HistoryStore:
         for s in slots:
             if s >= 0 and self.length(s) > budget:
                 self.evicted_h[s] += self.length(s) - budget
+                self.mass[s, budget:].zero_()  # rows to come start without weight
                 flide._check(self._lib.flide_pool_truncate(self._pool, s, int(budget)),
                              "flide_pool_truncate")
         self._sync_table()
