@@ -565,14 +565,14 @@ size_t flide_draft_attn_workspace_bytes(int32_t R, int32_t T, int32_t Hq, int32_
  *   workspace  device, 256-byte aligned, flide_draft_attn_workspace_bytes(idx->R,
  *          idx->T, Hq, Hkv, d) bytes; one call at a time
  * Rows past the stream's last token are left as they were.  A key that a row
- * does not see takes no part in its result, whatever its value.  q, k, v and
- * the past 16-byte aligned.  The softmax weights are rounded to bf16 before they
- * multiply v (not for FLIDE_F32; e4m3: to half, or to the sum of two e4m3 values:
- * relative error <= 2^-8, absolute <= 2^-16 of the row's largest weight); their
- * sum is not.
+ * does not see takes no part in its result, whatever its value.  q, k, v, the
+ * past and out 16-byte aligned; scale finite and >= 0 (FLIDE_ERR_INVALID).
+ * The softmax weights are rounded to bf16 before they multiply v (not for
+ * FLIDE_F32; e4m3: to half, or to the sum of two e4m3 values: relative error
+ * <= 2^-8, absolute <= 2^-16 of the row's largest weight); their sum is not.
  * Host errors: FLIDE_ERR_SHAPE, FLIDE_ERR_CAPACITY (workspace too small, more
  * than 2048 requests, T * Hq past 2^30), FLIDE_ERR_CUDA; device errors as
- * flide_fork_attn. */
+ * flide_fork_attn, and FLIDE_ERR_CAPACITY for a past of more than 2^30 rows. */
 int flide_draft_attn(const void *q, const void *k, const void *v, const void *past_k,
                      const void *past_v, int32_t past_rows, const flide_tree_index *idx, int32_t Hq,
                      int32_t Hkv, int32_t d, int32_t dtype, const float *descale, float scale,
@@ -634,14 +634,14 @@ int flide_verify_draft(const flide_tree_index *idx, const int32_t *tokens, const
  *     t >= j (the rows flide_history_append gives the history after the step).
  * Only root tokens count: drafted ones may be rejected, and an accepted token
  * is a root token of a later step, so each token counts once.
- *   q [T, Hq, d], k [T, Hkv, d], pool_k, block_table, req_slot, idx and descale
- *     as given to flide_draft_attn_paged, lse as written by it
+ *   q [T, Hq, d], k [T, Hkv, d], pool_k (16-byte aligned), block_table, req_slot,
+ *     idx and descale as given to flide_draft_attn_paged, lse as written by it
  *   mass, mass_out float [n_slots][max_blocks * block_rows]; mass_out may be
  *     mass (in place), else entries not named above are left as they were.
  * Each slot at most once per call (two requests would race for its sums).
  * Device errors: FLIDE_ERR_INVALID for a bad slot or block,
- * FLIDE_ERR_CAPACITY where P + n passes max_blocks * block_rows (that request
- * is skipped).  Host errors as flide_draft_attn_paged. */
+ * FLIDE_ERR_CAPACITY where P + n passes max_blocks * block_rows or P 2^30 (that
+ * request is skipped).  Host errors as flide_draft_attn_paged. */
 int flide_history_mass(const void *q, const void *k, const float *lse, const void *pool_k,
                        int32_t n_blocks, int32_t block_rows, const int32_t *block_table,
                        int32_t max_blocks, const int32_t *req_slot, int32_t n_slots,
@@ -659,8 +659,8 @@ int flide_history_mass(const void *q, const void *k, const float *lse, const voi
  *             min(length, budget): flide_pool_truncate)
  *   block_table, dst_table  device int32 [n_slots * max_blocks]
  *   pool_k, pool_v [n_blocks * block_rows, Hkv, d], dst_k, dst_v [dst_blocks *
- *             block_rows, Hkv, d] dtype; row bytes a multiple of 16 and at most
- *             2^20
+ *             block_rows, Hkv, d] dtype, 16-byte aligned; row bytes a multiple
+ *             of 16 and at most 2^20
  *   mass, mass_out float [n_slots][max_blocks * block_rows]
  *   kept      int32 [R][budget]: the rows kept, ascending, then -1
  * In place (dst_k == pool_k, dst_v == pool_v, dst_table == block_table,
@@ -670,8 +670,8 @@ int flide_history_mass(const void *q, const void *k, const float *lse, const voi
  * n_slots or listed twice, a length outside [0, max_blocks * block_rows] (those
  * requests are left as they are) or a row without a block.  Host errors:
  * FLIDE_ERR_SHAPE (also budget <= 0, sinks + recent > budget),
- * FLIDE_ERR_CAPACITY (more than 4096 requests, a pool or a history of more than
- * 2^31 - 1 rows), FLIDE_ERR_CUDA. */
+ * FLIDE_ERR_CAPACITY (more than 4096 requests, a pool of more than 2^31 - 1 rows,
+ * max_blocks * block_rows past 2^30), FLIDE_ERR_CUDA. */
 int flide_history_evict(int32_t R, const int32_t *req_slot, int32_t n_slots, const int32_t *hist_len,
                         const int32_t *block_table, int32_t max_blocks, int32_t block_rows,
                         const void *pool_k, const void *pool_v, int32_t n_blocks, int32_t Hkv,

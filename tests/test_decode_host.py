@@ -101,10 +101,12 @@ def test_store_bookkeeping():
         store.evict([0, 0], 4)
     with pytest.raises(ValueError):
         store.accumulate_mass(None, None, None, None, 1.0, [1, 1])
+    store.mass = torch.ones(2, 48)
     store.evicted_h[1] = 7
     assert store.pos_offset([1, -1]).tolist() == [7, 0]
     store.release(1)
     assert store.pos_offset([1]).tolist() == [0]
+    assert bool((store.mass[0] == 1).all()) and bool((store.mass[1] == 0).all())  # the slot starts over
 
 
 # ---- refusals of the device entry points ----
@@ -137,7 +139,8 @@ DRAFT = [
     (dict(Hq=12, Hkv=8), S), (dict(d=16), S), (dict(d=100), S), (dict(d=288), S), (dict(dtype=7), S),
     (dict(dtype=flide.E4M3), S), (dict(dtype=flide.E4M3, descale=A, d=64), S), (dict(idx=_idx(R=-1)), S),
     (dict(idx=_idx(T=-1)), S), (dict(idx=_idx(R=4097)), C), (dict(idx=_idx(T=1 << 28)), C), (dict(ws_bytes=100), C),
-    (dict(ws=A + 16), S), (dict(q=A + 8), S), (dict(idx=_idx(T=0)), flide.OK), (dict(idx=_idx(R=0)), flide.OK),
+    (dict(ws=A + 16), S), (dict(q=A + 8), S), (dict(out=B + 8), S), (dict(scale=-0.1), I),
+    (dict(scale=math.nan), I), (dict(scale=math.inf), I), (dict(idx=_idx(T=0)), flide.OK), (dict(idx=_idx(R=0)), flide.OK),
 ]
 
 
@@ -145,10 +148,10 @@ DRAFT = [
 @pytest.mark.parametrize("kw,code", DRAFT + [(dict(past=NUL), S), (dict(past_rows=-1), S)])
 def test_draft_attn_refusals(lib, kw, code):
     a = dict(idx=_idx(), q=A, past=A, past_rows=10, Hq=16, Hkv=4, d=128, dtype=flide.BF16, descale=NUL, out=B, ws=A,
-             ws_bytes=1 << 40)
+             ws_bytes=1 << 40, scale=0.1)
     a.update(kw)
     assert lib.flide_draft_attn(a["q"], A, A, a["past"], A, a["past_rows"], a["idx"], a["Hq"], a["Hkv"], a["d"],
-                                a["dtype"], a["descale"], 0.1, a["out"], NUL, a["ws"], a["ws_bytes"], NUL) == code
+                                a["dtype"], a["descale"], a["scale"], a["out"], NUL, a["ws"], a["ws_bytes"], NUL) == code
 
 
 PAGED = [(dict(pool=NUL), S), (dict(table=NUL), S), (dict(slot=NUL), S), (dict(n_blocks=0), S), (dict(max_blocks=0), S),
@@ -159,15 +162,15 @@ PAGED = [(dict(pool=NUL), S), (dict(table=NUL), S), (dict(slot=NUL), S), (dict(n
 @pytest.mark.parametrize("kw,code", DRAFT + PAGED)
 def test_draft_attn_paged_refusals(lib, kw, code):
     a = dict(idx=_idx(), q=A, pool=A, table=A, slot=A, n_blocks=4, block_rows=16, max_blocks=2, n_slots=2, Hq=16, Hkv=4,
-             d=128, dtype=flide.BF16, descale=NUL, out=B, ws=A, ws_bytes=1 << 40)
+             d=128, dtype=flide.BF16, descale=NUL, out=B, ws=A, ws_bytes=1 << 40, scale=0.1)
     a.update(kw)
     assert lib.flide_draft_attn_paged(a["q"], A, A, a["pool"], A, a["n_blocks"], a["block_rows"], a["table"],
                                       a["max_blocks"], a["slot"], a["n_slots"], a["idx"], a["Hq"], a["Hkv"], a["d"],
-                                      a["dtype"], a["descale"], 0.1, a["out"], NUL, a["ws"], a["ws_bytes"], NUL) == code
+                                      a["dtype"], a["descale"], a["scale"], a["out"], NUL, a["ws"], a["ws_bytes"], NUL) == code
 
 
 @fake
-@pytest.mark.parametrize("kw,code", [x for x in DRAFT if not {"out", "ws", "ws_bytes"} & set(x[0])
+@pytest.mark.parametrize("kw,code", [x for x in DRAFT if not {"out", "ws", "ws_bytes", "scale"} & set(x[0])
                                      and "q" not in x[0] and x[1] != C] + PAGED
                          + [(dict(q=NUL), S), (dict(lse=NUL), S), (dict(mass=NUL), S), (dict(idx=_idx(R=4097)), C)])
 def test_history_mass_refusals(lib, kw, code):
@@ -185,7 +188,7 @@ def test_history_mass_refusals(lib, kw, code):
     (dict(n_slots=0), S), (dict(block_rows=0), S), (dict(n_blocks=0), S), (dict(dst_blocks=0), S), (dict(Hkv=0), S),
     (dict(budget=0), S), (dict(sinks=-1), S), (dict(recent=-1), S), (dict(sinks=60, recent=41), S),
     (dict(sinks=2 ** 31 - 1, recent=2 ** 31 - 1), S), (dict(dtype=5), S), (dict(Hkv=1, d=4), S),
-    (dict(Hkv=1 << 13, d=128), S), (dict(R=4097), C), (dict(max_blocks=1 << 20, block_rows=1 << 12), C),
+    (dict(Hkv=1 << 13, d=128), S), (dict(pool=A + 8), S), (dict(n_blocks=1 << 26), C), (dict(R=4097), C), (dict(max_blocks=1 << 20, block_rows=1 << 12), C),
     (dict(R=0), flide.OK),
 ])
 def test_history_evict_refusals(lib, kw, code):

@@ -190,6 +190,56 @@ def test_device_errors():
     assert idx.status() == flide.ERR_SHAPE
 
 
+def test_a_past_that_is_too_long_is_refused():
+    rows = (1 << 30) + 1
+    tree = inputs._tree([(rows, [(-1, 1)]), (16, [(-1, 1)])], 0)
+    g = torch.Generator(device="cuda").manual_seed(0)
+    q, k, v, pk, pv = (torch.randn(n, h, 64, generator=g, device="cuda").bfloat16()
+                       for n, h in ((2, 2), (2, 1), (2, 1), (16, 1), (16, 1)))
+    width = (1 << 26) + 1
+    table = torch.zeros(2 * width, dtype=torch.int32, device="cuda")
+    _, idx = build(tree)
+    flide.draft_attn_paged(q, k, v, idx, 0.1, pk, pv, table, torch.arange(2, dtype=torch.int32, device="cuda"), 16,
+                           width)
+    torch.cuda.synchronize()
+    assert idx.status() == flide.ERR_CAPACITY
+
+
+@pytest.mark.parametrize("tokens", [1, 30])
+def test_rows_past_32_bit_offsets(tokens):
+    """The history's blocks behind 2^31 elements of a pool give the bits that they give at its start."""
+    Hq, Hkv, d, bl, n_blocks = 32, 8, 128, 128, 16500
+    assert n_blocks * bl * Hkv * d > 2 ** 31 + 8 * bl * Hkv * d
+    tree = inputs._tree([(470, [(-1, tokens)]), (129, [(-1, tokens)])], 0)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    T = tree.T
+    q, k, v, hk, hv = (torch.randn(n, h, d, generator=g, device="cuda").bfloat16()
+                       for n, h in ((T, Hq), (T, Hkv), (T, Hkv), (6 * bl, Hkv), (6 * bl, Hkv)))
+    pk, pv = (torch.empty(n_blocks * bl, Hkv, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    slots = torch.tensor([1, 0], dtype=torch.int32, device="cuda")
+    got = []
+    for first in (0, n_blocks - 6):
+        for pool, rows in ((pk, hk), (pv, hv)):
+            pool[first * bl:(first + 6) * bl] = rows
+        table = torch.tensor([4, 5, -1, -1, 0, 1, 2, 3], dtype=torch.int32, device="cuda")
+        table = torch.where(table >= 0, table + first, table)
+        _, idx = build(tree)
+        out, lse = flide.draft_attn_paged(q, k, v, idx, 0.1, pk, pv, table, slots, bl, 4)
+        mass = torch.zeros(2, 4 * bl, device="cuda")
+        flide.history_mass(q, k, lse, idx, 0.1, pk, table, slots, bl, 4, mass)
+        m1, status = mass.clone(), torch.zeros(1, dtype=torch.int32, device="cuda")
+        ln = torch.tensor([129 + tokens, 470 + tokens], dtype=torch.int32, device="cuda")
+        kept = flide.history_evict(slots, ln, table, bl, 4, pk, pv, mass, 100, status, sinks=3, recent=9)
+        torch.cuda.synchronize()
+        assert idx.status() == 0 and int(status) == 0
+        rows = [pool[(first + b) * bl:(first + b) * bl + 100].clone() for pool in (pk, pv) for b in (0, 4)]
+        got.append([out, lse, m1, kept, mass] + rows)
+        for i, r in enumerate(rows):  # the kept rows, moved to the front
+            src = (hk, hv)[i // 2][(4 * bl if i % 2 else 0):]
+            assert torch.equal(r, src[kept[i % 2].long()])
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
 def test_two_streams_with_their_own_workspaces():
     tree = TREES["many"]()
     x, hist, _ = _inputs(tree, 16, 4, 128, "bf16", 8)

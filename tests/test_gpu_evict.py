@@ -122,6 +122,14 @@ def test_mass_errors():
                        torch.zeros((n_slots, width * 64), device="cuda"))
     torch.cuda.synchronize()
     assert idx.status() == flide.ERR_CAPACITY
+    past = inputs._tree([(200, [(-1, 1)]), (300, [(-1, 60)])], 0)  # nor does the past alone: no weight is written
+    _, idx = build(past)
+    before = torch.rand((n_slots, width * 64), device="cuda")
+    mass = before.clone()
+    flide.history_mass(q, k, lse, idx, 0.1, pools[0].cuda(), full.view(-1).cuda(), slots.cuda(), 64, width, mass)
+    torch.cuda.synchronize()
+    assert idx.status() == flide.ERR_CAPACITY
+    assert torch.equal(mass[int(slots[1])], before[int(slots[1])])
 
 
 # ---- eviction ----

@@ -22,6 +22,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <cmath>
 
 #include "draft.cuh"
 #include "launch.cuh"
@@ -803,7 +804,7 @@ int join_launch(const DraftParams &p, cudaStream_t s) {
   cfg.stream = s;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, draft_join_kernel<T, D>, p) == cudaSuccess ? FLIDE_OK : FLIDE_ERR_CUDA;
+  return launched(cudaLaunchKernelEx(&cfg, draft_join_kernel<T, D>, p));
 }
 
 int draft_attn(const void *q, const void *k, const void *v, const void *past_k, const void *past_v,
@@ -816,7 +817,10 @@ int draft_attn(const void *q, const void *k, const void *v, const void *past_k, 
   if (dtype == FLIDE_E4M3 && (!descale || d != 128)) return FLIDE_ERR_SHAPE;
   if (idx->R < 0 || idx->T < 0) return FLIDE_ERR_SHAPE;
   if ((uintptr_t)workspace % 256) return FLIDE_ERR_SHAPE;
-  if (((uintptr_t)q | (uintptr_t)k | (uintptr_t)v | (uintptr_t)past_k | (uintptr_t)past_v) % 16) return FLIDE_ERR_SHAPE;
+  if (((uintptr_t)q | (uintptr_t)k | (uintptr_t)v | (uintptr_t)past_k | (uintptr_t)past_v | (uintptr_t)out) % 16)
+    return FLIDE_ERR_SHAPE;
+  // a tile's largest score is scale times the largest product
+  if (!(scale >= 0.f) || std::isinf(scale)) return FLIDE_ERR_INVALID;
   if (idx->R > kMaxListR || (long long)idx->T * Hq > 0x3fffffffLL) return FLIDE_ERR_CAPACITY;
   if (idx->R == 0 || idx->T == 0) return FLIDE_OK;
   const Variant var = variant_of(idx->R, idx->T, Hq / Hkv, d, dtype);

@@ -57,11 +57,11 @@ __device__ __forceinline__ long long mass_units(const MassParams &p, int r, int 
   const flide_tree_index &x = p.x;
   const int slot = p.hist.req_slot[r];
   if (slot < 0) return 0;
-  int t0, base;
-  const int root = root_tokens(x, r, &t0);
-  const int n = history_rows(x, p.hist, r, report, &base);
+  int t0;
+  const int root = root_tokens(x, r, &t0), n = x.past_start[r + 1] - x.past_start[r];
   if (root == 0) return 0;
-  if (slot >= p.hist.n_slots || n + (long long)root > (long long)p.hist.max_blocks * p.hist.block_rows) {
+  if (slot >= p.hist.n_slots || n > kMaxHistory ||
+      n + (long long)root > (long long)p.hist.max_blocks * p.hist.block_rows) {
     if (report) set_status(x.status, slot >= p.hist.n_slots ? FLIDE_ERR_INVALID : FLIDE_ERR_CAPACITY);
     return 0;
   }
@@ -732,7 +732,8 @@ int flide_history_evict(int32_t R, const int32_t *req_slot, int32_t n_slots, con
   if (!es) return FLIDE_ERR_SHAPE;
   const int64_t row_bytes = (int64_t)Hkv * d * es;
   if (row_bytes % 16 || row_bytes > (1 << 20)) return FLIDE_ERR_SHAPE;
-  if (R > kMaxEvictR || (int64_t)max_blocks * block_rows > INT32_MAX ||
+  if (((uintptr_t)pool_k | (uintptr_t)pool_v | (uintptr_t)dst_k | (uintptr_t)dst_v) % 16) return FLIDE_ERR_SHAPE;
+  if (R > kMaxEvictR || (int64_t)max_blocks * block_rows > kMaxHistory ||
       (int64_t)n_blocks * block_rows > INT32_MAX || (int64_t)dst_blocks * block_rows > INT32_MAX)
     return FLIDE_ERR_CAPACITY;
   if (R == 0) return FLIDE_OK;

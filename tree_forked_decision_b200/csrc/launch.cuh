@@ -1,4 +1,5 @@
-// launch.cuh -- host side of a kernel's shared-memory opt-in.
+// launch.cuh -- host side of launches: a kernel's shared-memory opt-in, the code
+// of a launch with attributes.
 #pragma once
 
 #include "common.cuh"
@@ -20,6 +21,13 @@ bool allow_smem(int dev) {
     return false;
   if (dev >= 0 && dev < 64) done[dev].store(true, std::memory_order_release);
   return true;
+}
+
+// The code of a cudaLaunchKernelEx; its error does not stay behind for the next call.
+inline int launched(cudaError_t e) {
+  if (e == cudaSuccess) return FLIDE_OK;
+  cudaGetLastError();
+  return FLIDE_ERR_CUDA;
 }
 
 }  // namespace flide

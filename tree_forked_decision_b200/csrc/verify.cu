@@ -25,6 +25,7 @@
 #include <cooperative_groups.h>
 
 #include "common.cuh"
+#include "launch.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -408,7 +409,7 @@ int verify_launch(const VerifyParams &p, bool wide, int dev, cudaStream_t s) {
   cfg.stream = s;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, verify_kernel<T, kVec>, p) == cudaSuccess ? FLIDE_OK : FLIDE_ERR_CUDA;
+  return launched(cudaLaunchKernelEx(&cfg, verify_kernel<T, kVec>, p));
 }
 
 }  // namespace

@@ -52,6 +52,9 @@ __device__ __forceinline__ int request_of(const long long *pref, int R, long lon
   return lo;
 }
 
+// A history's rows are counted in 32 bits, tile ends past the last row included.
+constexpr int kMaxHistory = 1 << 30;
+
 // A request's history rows: packed rows [base, base + len), or rows of pool
 // slot `slot` through its block table.
 struct HistoryView {
@@ -67,6 +70,10 @@ __device__ __forceinline__ int history_length(const HistoryView &h, int p0, int 
                                               int *code) {
   *base = h.block_table ? slot : p0;
   if (len <= 0) return 0;
+  if (len > kMaxHistory) {
+    *code = FLIDE_ERR_CAPACITY;
+    return 0;
+  }
   if (h.block_table) {
     if (slot < 0 || slot >= h.n_slots || len > (long long)h.max_blocks * h.block_rows) {
       *code = FLIDE_ERR_INVALID;
