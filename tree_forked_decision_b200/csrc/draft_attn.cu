@@ -586,7 +586,13 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) draft_join_kernel(const Dr
   const long long job = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
   const int t = (int)(job / p.Hq), h = (int)(job - (long long)t * p.Hq), hk = h / p.G;
   const size_t head = (size_t)t * p.Hq + h;
-  const bool live = !failed(x.status) && t < x.counts[FLIDE_CNT_T];
+  // what t alone addresses is loaded at once (the last block's rows past the capacity
+  // take its last token's); a token past the stream's has no node
+  const int tc = min(t, x.T - 1), node_of_t = x.token_node[tc];
+  uint4 qw[Row::kWords];
+  Row::load(static_cast<const T *>(p.q) + ((size_t)tc * p.Hq + h) * D, l8, qw);
+  const int n_tokens = x.counts[FLIDE_CNT_T];
+  const bool live = !failed(x.status) && t < n_tokens;
   float m = -INFINITY, l = 0.f, acc[kE];
 #pragma unroll
   for (int e = 0; e < kE; ++e) acc[e] = 0.f;
@@ -594,9 +600,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) draft_join_kernel(const Dr
   if (live) {
     const T *K = static_cast<const T *>(p.k), *Vs = static_cast<const T *>(p.v);
     const float qk_scale = p.scale * kLog2eD * (p.descale ? p.descale[0] * p.descale[1] : 1.f);
-    uint4 qw[Row::kWords];
-    Row::load(static_cast<const T *>(p.q) + head * D, l8, qw);
-    const int n = (int)checked(x.status, x.counts, x.token_node[t], x.counts[FLIDE_CNT_N], 801);
+    const int n = (int)checked(x.status, x.counts, node_of_t, x.counts[FLIDE_CNT_N], 801);
     r = x.node_req[n];
     const int a1 = x.anc_ptr[n + 1];
     for (int a0 = x.anc_ptr[n]; a0 < a1; a0 += 32) {
@@ -644,10 +648,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) draft_join_kernel(const Dr
     }
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the part kernel's results
+  const DraftReq q = p.list[r];  // (loaded beside the status word: a failed call's is not used)
+  const long long U = p.list[x.R].unit0;
   if (!live || failed(x.status)) return;
-  const DraftReq q = p.list[r];
   if (q.units > 0) {
-    const long long U = p.list[x.R].unit0;
     const int row = (t - q.t0) * p.G + h - hk * p.G;
     const int tile = row / p.tile_rows, li = tile * p.Hkv + hk;
     const long long u0 = q.unit0 + (long long)li * q.units;

@@ -68,6 +68,7 @@ enum {
   bDrain = bMerge + 1,
   kBars = bDrain + 1
 };
+constexpr int kBarBytes = (8 * kBars + 15) / 16 * 16;
 struct __align__(16) Misc {
   uint32_t tmem;
   int abort;
@@ -77,7 +78,7 @@ struct __align__(16) Misc {
 // 32 banks), and a warp's (max, sum) for each of its rows.
 constexpr int merge_bytes(int rep) { return rep > 1 ? kBM / rep * 132 * 4 + 2 * 8 * 32 * 4 : 0; }
 constexpr size_t wide_smem(bool f8, int halves, int rep, int tiles, int R) {
-  return (size_t)(halves + tiles) * (f8 ? 16384 : 32768) + merge_bytes(rep) + 256 + sizeof(Misc) +
+  return (size_t)(halves + tiles) * (f8 ? 16384 : 32768) + merge_bytes(rep) + kBarBytes + sizeof(Misc) +
          (size_t)(R + 1) * sizeof(DraftReq) + 1024;
 }
 
@@ -110,7 +111,7 @@ draft_part_wide(const __grid_constant__ WideMaps maps, const DraftParams p, int 
   constexpr int kTile = F8 ? 16384 : 32768, kSlabs = F8 ? 1 : 2;  // bytes; 128-byte slabs of a row
   const int s_k = kHalves * kTile, s_v = s_k + stages_k * kTile, s_m = s_v + stages_v * kTile;
   const int s_bar = s_m + merge_bytes(kRep);
-  Misc &ms = *reinterpret_cast<Misc *>(smem + s_bar + 256);
+  Misc &ms = *reinterpret_cast<Misc *>(smem + s_bar + kBarBytes);
   volatile int *abort_flag = &ms.abort;
   DraftReq *list = reinterpret_cast<DraftReq *>(&ms + 1);
   const flide_tree_index &x = p.x;
@@ -128,7 +129,7 @@ draft_part_wide(const __grid_constant__ WideMaps maps, const DraftParams p, int 
   const int w = blockIdx.x, W = workers_of(U, p.workers);
   if (w >= W) return;
   if (warp == 9) {
-    tmem_alloc(sb + s_bar + 256 + (uint32_t)offsetof(Misc, tmem), 512);
+    tmem_alloc(sb + s_bar + kBarBytes + (uint32_t)offsetof(Misc, tmem), 512);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -161,7 +162,9 @@ draft_part_wide(const __grid_constant__ WideMaps maps, const DraftParams p, int 
     int rc = 0, kt = 0;  // runs, key tiles so far
     Ring ring;
     Run run;
+    const uint64_t once = policy_evict_first(), again = policy_evict_normal();
     for (; ok && draft_run(p, list, u, u_end, w, run); ++rc) {
+      const uint64_t policy = tiles_of(p, run.tokens) > 1 ? again : once;
       // boxes that hold history rows, a lane each (the rest of the last tile keeps
       // what the stage held, and is masked); looked up a tile ahead
       auto row_at = [&](int k0) -> long long {
@@ -192,7 +195,7 @@ draft_part_wide(const __grid_constant__ WideMaps maps, const DraftParams p, int 
         if (lane < used)
           for (int s = 0; s < kSlabs; ++s)
             tma_load_3d(sb + s_at + st * kTile + s * 16384 + lane * box_rows * 128, map, bar(b_full + st), 64 * s,
-                        run.hk, (int)row);
+                        run.hk, (int)row, policy);
         ring.next(stages);
       }
     }

@@ -157,8 +157,10 @@ struct __align__(16) MassReq {
   int t0, root, hist, slot;
 };
 
-__device__ __forceinline__ void copy_async16(uint32_t dst, const void *src, bool on) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+__device__ __forceinline__ void copy_async16(uint32_t dst, const void *src, bool on, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst), "l"(src),
+               "r"(on ? 16 : 0), "l"(policy)
+               : "memory");
 }
 
 template <int D, bool F8>
@@ -166,6 +168,7 @@ __global__ void __launch_bounds__(kMassWarps * 32, 1) mass_kernel_mma(const Mass
   using S = MassShape<D, F8>;
   extern __shared__ uint4 qs[];  // [held][kWords][32], lse [held][8], the warps' rings, the list
   __shared__ long long part[32];
+  __shared__ float edge[kMassWarps][2][16];  // sums of a warp's first and last group, where it has a part of it
   float *ls = reinterpret_cast<float *>(qs + p.held * S::kWords * 32);
   uint4 *rings = reinterpret_cast<uint4 *>(ls + p.held * 8);
   MassReq *list = reinterpret_cast<MassReq *>(rings + kMassWarps * (kRing / 16));
@@ -187,6 +190,7 @@ __global__ void __launch_bounds__(kMassWarps * 32, 1) mass_kernel_mma(const Mass
   const long long N = list[R].group0;
   const float qk_scale = p.scale * (F8 ? p.descale[0] * p.descale[1] : 1.f) * kLog2eM;
   uint4 *ring = rings + warp * (kRing / 16) + lane;
+  const uint64_t once = policy_evict_first(), again = policy_evict_normal();
   long long u = blockIdx.x * N / gridDim.x;
   const long long u_end = (blockIdx.x + 1) * N / gridDim.x;
   while (u < u_end) {
@@ -200,17 +204,24 @@ __global__ void __launch_bounds__(kMassWarps * 32, 1) mass_kernel_mma(const Mass
     u += gb - ga;
     const int past_groups = (q.hist + 15) / 16;
     const int rows = q.root * p.G, per = (rows + 7) / 8, tiles = p.Hkv * per;  // tile = head * per + row tile
+    const uint64_t policy = tiles > p.held ? again : once;
     float *out = p.mass_out + (size_t)q.slot * p.hist.max_blocks * p.hist.block_rows;
     const float *in = p.mass + (size_t)q.slot * p.hist.max_blocks * p.hist.block_rows;
     for (int b0 = 0; b0 < tiles; b0 += p.held) {
       const int b1 = min(tiles, b0 + p.held), h0 = b0 / per, heads = (b1 - 1) / per - h0 + 1;
-      // this warp's groups ga + warp, ga + warp + kMassWarps, ...; steps (group, head) go into
-      // the ring in order.  Row of a group's first history row, or -1: its first stream row.
+      // the pass's steps (group, head) are cut evenly over the warps; warp w takes
+      // [step0(w), step0(w + 1)), and they go into its ring in order
+      const long long steps = (long long)(gb - ga) * heads;
+      auto step0 = [&](int w) -> long long { return steps * w / kMassWarps; };
+      const long long s0 = step0(warp), s1 = step0(warp + 1);
+      const int grp0 = ga + (int)(s0 / heads), hh0 = (int)(s0 % heads);
+      // row of a group's first history row, or its first stream row; -1: no group
       auto row_of = [&](int grp) -> long long {
         if (grp >= gb) return -1;
         return grp < past_groups ? history_row(x, p.hist, q.slot, 16 * grp) : q.t0 + 16 * (grp - past_groups);
       };
-      int ig = ga + warp, ih = 0;  // the next step to copy: group, head (from h0)
+      int ig = grp0, ih = hh0;  // the next step to copy: group, head (from h0)
+      long long to_copy = s1 - s0;
       long long inext = row_of(ig);
       const char *src[2];          // its rows g and g + 8 (on: history or root has them)
       bool on[2];
@@ -223,25 +234,28 @@ __global__ void __launch_bounds__(kMassWarps * 32, 1) mass_kernel_mma(const Mass
           on[t] = inext >= 0 && g + 8 * t < left;
           src[t] = base + (size_t)(on[t] ? inext + g + 8 * t : 0) * p.Hkv * S::kRow;
         }
-        inext = row_of(ig + kMassWarps);  // looked up a group ahead
+        inext = row_of(ig + 1);  // looked up a group ahead
       };
       group();
+      src[0] += (size_t)ih * S::kRow;
+      src[1] += (size_t)ih * S::kRow;
       const uint32_t ring0 = smem_u32(ring);
       uint32_t to = ring0;         // the next stage
       auto copy = [&]() {
-        if (ig < gb) {
+        if (to_copy > 0) {
+          --to_copy;
 #pragma unroll
           for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int j = 0; j < S::kCj; ++j)
-              copy_async16(to + (t * S::kCj + j) * 512, src[t] + 64 * j, on[t]);
+              copy_async16(to + (t * S::kCj + j) * 512, src[t] + 64 * j, on[t], policy);
           src[0] += S::kRow;
           src[1] += S::kRow;
           to += 2 * S::kCj * 512;
           if (to == ring0 + S::kStages * 2 * S::kCj * 512) to = ring0;
           if (++ih == heads) {
             ih = 0;
-            ig += kMassWarps;
+            ++ig;
             group();
           }
         }
@@ -269,12 +283,23 @@ __global__ void __launch_bounds__(kMassWarps * 32, 1) mass_kernel_mma(const Mass
         if (j == 0 && (l & 3) == 0) ls[t * 8 + (l >> 2)] = qr < rows ? p.lse[at] * kLog2eM : INFINITY;
       }
       __syncthreads();
-      int st = 0;
-      for (int grp = ga + warp; grp < gb; grp += kMassWarps) {
+      // row i of a group's 16 gets `sum` from this pass's heads
+      auto store = [&](int grp, int i, float sum) {
         const bool fresh = grp >= past_groups;
-        const int i0 = 16 * (fresh ? grp - past_groups : grp), len = fresh ? q.root : q.hist;
+        i += 16 * (fresh ? grp - past_groups : grp);
+        if (i >= (fresh ? q.root : q.hist)) return;
+        const int at = (fresh ? q.hist : 0) + i;
+        // (a later batch of query tiles adds to the first one's sum)
+        out[at] = b0 > 0 ? out[at] + sum : fresh ? sum : in[at] + sum;
+      };
+      int st = 0, grp = grp0, first = hh0;
+      for (long long s = s0; s < s1; ++grp, first = 0) {
+        const bool fresh = grp >= past_groups;
+        const int i0 = 16 * (fresh ? grp - past_groups : grp);
+        const int last = (int)min((long long)heads, first + (s1 - s));
+        s += last - first;
         float acc[2] = {0.f, 0.f};  // rows i0 + g, i0 + g + 8
-        for (int hh = 0; hh < heads; ++hh) {
+        for (int hh = first; hh < last; ++hh) {
           asm volatile("cp.async.wait_group %0;" ::"n"(S::kStages - 2) : "memory");
           uint4 kr[2][S::kCj];
 #pragma unroll
@@ -328,15 +353,24 @@ __global__ void __launch_bounds__(kMassWarps * 32, 1) mass_kernel_mma(const Mass
         for (int t = 0; t < 2; ++t) {
           acc[t] += __shfl_xor_sync(0xffffffffu, acc[t], 1);
           acc[t] += __shfl_xor_sync(0xffffffffu, acc[t], 2);
-          const int i = i0 + g + 8 * t;
-          if (c == 0 && i < len) {
-            const int at = (fresh ? q.hist : 0) + i;
-            // (a later batch of query tiles adds to the first one's sum)
-            out[at] = b0 > 0 ? out[at] + acc[t] : fresh ? acc[t] : in[at] + acc[t];
+          if (c == 0) {
+            if (last - first == heads) store(grp, g + 8 * t, acc[t]);
+            else edge[warp][first == 0][g + 8 * t] = acc[t];
           }
         }
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
+      // a group that several warps share: the warp with its first head adds their
+      // sums, in order
+      __syncthreads();
+      const int cut = ga + (int)((s1 - 1) / heads);  // the warp's last group
+      const long long end = (long long)(cut + 1 - ga) * heads;
+      if (s1 > s0 && end > s1 && end - heads >= s0 && lane < 16) {
+        float sum = edge[warp][1][lane];
+        for (int w = warp + 1; w < kMassWarps && step0(w) < end; ++w)
+          if (step0(w + 1) > step0(w)) sum += edge[w][0][lane];
+        store(cut, lane, sum);
+      }
     }
   }
 }
@@ -348,7 +382,7 @@ int mass_mma_launch(MassParams &p, int dev, int sms, cudaStream_t s) {
   // what the rings and the list (2048 requests: 64 KB) leave, for all query tiles
   // that a request may have if they fit
   const int fixed = kMassWarps * kRing + (p.x.R + 1) * (int)sizeof(MassReq);
-  p.held = min((231000 - fixed) / S::kTileBytes, p.Hkv * (((int)min((long long)p.x.T * p.G, 1ll << 20) + 7) / 8));
+  p.held = min((230000 - fixed) / S::kTileBytes, p.Hkv * (((int)min((long long)p.x.T * p.G, 1ll << 20) + 7) / 8));
   mass_kernel_mma<D, F8><<<sms, kMassWarps * 32, (size_t)fixed + p.held * S::kTileBytes, s>>>(p);
   FLIDE_LAUNCH_CHECK();
   return FLIDE_OK;

@@ -94,6 +94,26 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *m, 
       "l"((uint64_t)m), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
       : "memory");
 }
+// Cache policy of data that is read once: first to leave L2.
+__device__ __forceinline__ uint64_t policy_evict_first() {
+  uint64_t h;
+  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(h));
+  return h;
+}
+__device__ __forceinline__ uint64_t policy_evict_normal() {
+  uint64_t h;
+  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(h));
+  return h;
+}
+// 3-D tiled load with a cache policy.
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *m, uint32_t bar,
+                                            int c0, int c1, int c2, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
+      "l"((uint64_t)m), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "l"(policy)
+      : "memory");
+}
 // 2-D tiled load into this CTA's shared memory, completing on `bar`.
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *m, uint32_t bar,
                                             int c0, int c1) {
