@@ -141,6 +141,7 @@ __global__ void __launch_bounds__(kMThreads) mass_kernel_portable(const MassPara
 // groups of 16 rows evenly: a warp has about three.
 constexpr int kMassWarps = 16;
 constexpr int kRing = 8192;  // bytes of a warp's ring
+constexpr int kMassExtra = 5;  // groups that a block's start on a request costs beside its own (3 us of 0.7)
 
 template <int D, bool F8>
 struct MassShape {
@@ -163,6 +164,10 @@ __device__ __forceinline__ void copy_async16(uint32_t dst, const void *src, bool
                : "memory");
 }
 
+__device__ __forceinline__ void copy_async4(uint32_t dst, const void *src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+
 template <int D, bool F8>
 __global__ void __launch_bounds__(kMassWarps * 32, 1) mass_kernel_mma(const MassParams p) {
   using S = MassShape<D, F8>;
@@ -179,7 +184,8 @@ __global__ void __launch_bounds__(kMassWarps * 32, 1) mass_kernel_mma(const Mass
     long long *group0 = &list[0].group0;  // every fourth 8-byte word of the list
     request_prefix(R, [&](int r) -> long long {
       MassReq &q = list[r];
-      const long long n = mass_units(p, r, 16, blockIdx.x == 0);
+      long long n = mass_units(p, r, 16, blockIdx.x == 0);
+      if (n > 0) n += kMassExtra;
       q.root = root_tokens(x, r, &q.t0);
       int base;
       q.hist = history_rows(x, p.hist, r, false, &base);
@@ -200,8 +206,10 @@ __global__ void __launch_bounds__(kMassWarps * 32, 1) mass_kernel_mma(const Mass
       if (list[mid + 1].group0 > u) hi = mid; else r = mid + 1;
     }
     const MassReq q = list[r];
-    const int ga = (int)(u - q.group0), gb = (int)min(list[r + 1].group0 - q.group0, ga + (u_end - u));
-    u += gb - ga;
+    const int ua = (int)(u - q.group0), ub = (int)min(list[r + 1].group0 - q.group0, ua + (u_end - u));
+    u += ub - ua;
+    const int ga = max(ua - kMassExtra, 0), gb = ub - kMassExtra;
+    if (gb <= ga) continue;
     const int past_groups = (q.hist + 15) / 16;
     const int rows = q.root * p.G, per = (rows + 7) / 8, tiles = p.Hkv * per;  // tile = head * per + row tile
     const uint64_t policy = tiles > p.held ? again : once;
@@ -261,37 +269,53 @@ __global__ void __launch_bounds__(kMassWarps * 32, 1) mass_kernel_mma(const Mass
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
       };
-#pragma unroll 1
-      for (int k = 0; k < S::kStages - 1; ++k) copy();  // on their way while the queries come
-      __syncthreads();  // the tiles held before are done with
-      for (int e = tid; e < (b1 - b0) * S::kCj * 32; e += kMassWarps * 32) {
-        const int t = e / (S::kCj * 32), j = e / 32 % S::kCj, l = e & 31;
-        const int h = (b0 + t) / per, qr = (b0 + t) % per * 8 + (l >> 2);
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        const size_t at = (size_t)(q.t0 + qr / p.G) * p.Hq + h * p.G + qr % p.G;
-        if (qr < rows)
-          v = *reinterpret_cast<const uint4 *>(static_cast<const char *>(p.q) + at * S::kRow + 64 * j + 16 * (l & 3));
-        uint4 *to = qs + t * S::kWords * 32 + l;
-        if (F8) {
-          to[2 * j * 32] = make_uint4(e4m3x2_to_half2(v.x), e4m3x2_to_half2(v.x >> 16), e4m3x2_to_half2(v.y),
-                                      e4m3x2_to_half2(v.y >> 16));
-          to[(2 * j + 1) * 32] = make_uint4(e4m3x2_to_half2(v.z), e4m3x2_to_half2(v.z >> 16), e4m3x2_to_half2(v.w),
-                                            e4m3x2_to_half2(v.w >> 16));
-        } else {
-          to[j * 32] = v;
+      // the query tiles before the ring's first copies, which would keep them waiting
+      // (the tiles held before are done with: the last pass ended in a barrier)
+      auto tiles_words = [&](auto &&f) {
+        for (int e = tid; e < (b1 - b0) * S::kCj * 32; e += kMassWarps * 32) {
+          const int t = e / (S::kCj * 32), j = e / 32 % S::kCj, l = e & 31;
+          const int h = (b0 + t) / per, qr = (b0 + t) % per * 8 + (l >> 2);
+          const size_t at = (size_t)(q.t0 + qr / p.G) * p.Hq + h * p.G + qr % p.G;
+          f(qs + (t * S::kWords + (F8 ? 2 : 1) * j) * 32 + l, j, l, qr < rows, qr < rows ? at : 0, ls + t * 8 + (l >> 2));
         }
-        if (j == 0 && (l & 3) == 0) ls[t * 8 + (l >> 2)] = qr < rows ? p.lse[at] * kLog2eM : INFINITY;
-      }
+      };
+      tiles_words([&](uint4 *to, int j, int l, bool row, size_t at, float *lse_to) {
+        copy_async16(smem_u32(to), static_cast<const char *>(p.q) + at * S::kRow + 64 * j + 16 * (l & 3), row, again);
+        if (j == 0 && (l & 3) == 0) copy_async4(smem_u32(lse_to), p.lse + at);
+      });
+      asm volatile("cp.async.commit_group;" ::: "memory");
+#pragma unroll 1
+      for (int k = 0; k < S::kStages - 1; ++k) copy();
+      asm volatile("cp.async.wait_group %0;" ::"n"(S::kStages - 1) : "memory");
+      // what this thread copied, in its final form
+      tiles_words([&](uint4 *to, int j, int l, bool row, size_t, float *lse_to) {
+        if (F8) {
+          const uint4 v = *to;
+          to[0] = make_uint4(e4m3x2_to_half2(v.x), e4m3x2_to_half2(v.x >> 16), e4m3x2_to_half2(v.y),
+                             e4m3x2_to_half2(v.y >> 16));
+          to[32] = make_uint4(e4m3x2_to_half2(v.z), e4m3x2_to_half2(v.z >> 16), e4m3x2_to_half2(v.w),
+                              e4m3x2_to_half2(v.w >> 16));
+        }
+        if (j == 0 && (l & 3) == 0) *lse_to = row ? *lse_to * kLog2eM : INFINITY;
+      });
       __syncthreads();
-      // row i of a group's 16 gets `sum` from this pass's heads
-      auto store = [&](int grp, int i, float sum) {
+      // place of row i of a group's 16 in the weights, -1: no such row
+      auto place = [&](int grp, int i) -> int {
         const bool fresh = grp >= past_groups;
         i += 16 * (fresh ? grp - past_groups : grp);
-        if (i >= (fresh ? q.root : q.hist)) return;
-        const int at = (fresh ? q.hist : 0) + i;
-        // (a later batch of query tiles adds to the first one's sum)
-        out[at] = b0 > 0 ? out[at] + sum : fresh ? sum : in[at] + sum;
+        return i >= (fresh ? q.root : q.hist) ? -1 : (fresh ? q.hist : 0) + i;
       };
+      // what this pass's sum is added to (a later batch of query tiles adds to the first
+      // one's sum); loaded well before it is needed
+      auto prior = [&](int grp, int at) -> float {
+        return at < 0 ? 0.f : b0 > 0 ? out[at] : grp < past_groups ? in[at] : 0.f;
+      };
+      // the warp's last group, where other warps have parts of it and this one its first head
+      const int cut = ga + (int)((s1 - 1) / heads);
+      const long long end = (long long)(cut + 1 - ga) * heads;
+      const bool owner = s1 > s0 && end > s1 && end - heads >= s0;
+      const int cut_at = owner && lane < 16 ? place(cut, lane) : -1;
+      const float cut_prior = prior(cut, cut_at);
       int st = 0, grp = grp0, first = hh0;
       for (long long s = s0; s < s1; ++grp, first = 0) {
         const bool fresh = grp >= past_groups;
@@ -299,6 +323,14 @@ __global__ void __launch_bounds__(kMassWarps * 32, 1) mass_kernel_mma(const Mass
         const int last = (int)min((long long)heads, first + (s1 - s));
         s += last - first;
         float acc[2] = {0.f, 0.f};  // rows i0 + g, i0 + g + 8
+        const bool whole = last - first == heads;
+        int at[2];
+        float was[2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          at[t] = whole && c == 0 ? place(grp, g + 8 * t) : -1;
+          was[t] = prior(grp, at[t]);
+        }
         for (int hh = first; hh < last; ++hh) {
           asm volatile("cp.async.wait_group %0;" ::"n"(S::kStages - 2) : "memory");
           uint4 kr[2][S::kCj];
@@ -353,23 +385,19 @@ __global__ void __launch_bounds__(kMassWarps * 32, 1) mass_kernel_mma(const Mass
         for (int t = 0; t < 2; ++t) {
           acc[t] += __shfl_xor_sync(0xffffffffu, acc[t], 1);
           acc[t] += __shfl_xor_sync(0xffffffffu, acc[t], 2);
-          if (c == 0) {
-            if (last - first == heads) store(grp, g + 8 * t, acc[t]);
-            else edge[warp][first == 0][g + 8 * t] = acc[t];
-          }
+          if (at[t] >= 0) out[at[t]] = was[t] + acc[t];
+          if (!whole && c == 0) edge[warp][first == 0][g + 8 * t] = acc[t];
         }
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
       // a group that several warps share: the warp with its first head adds their
       // sums, in order
       __syncthreads();
-      const int cut = ga + (int)((s1 - 1) / heads);  // the warp's last group
-      const long long end = (long long)(cut + 1 - ga) * heads;
-      if (s1 > s0 && end > s1 && end - heads >= s0 && lane < 16) {
+      if (cut_at >= 0) {
         float sum = edge[warp][1][lane];
         for (int w = warp + 1; w < kMassWarps && step0(w) < end; ++w)
           if (step0(w + 1) > step0(w)) sum += edge[w][0][lane];
-        store(cut, lane, sum);
+        out[cut_at] = cut_prior + sum;
       }
     }
   }
