@@ -124,6 +124,24 @@ def test_greedy_rows_and_edges():
     assert status == 0 and nxt.tolist() == [-1, -1]
 
 
+@pytest.mark.parametrize("sampled", [False, True])
+@pytest.mark.parametrize("V", [300, 1021, 40000])
+def test_subnormal_and_negative_zero_entries(V, sampled):
+    """-0 counts as 0 and a subnormal probability as its value: a row that holds nothing else is drawn from."""
+    tree = inputs._tree([(0, [(-1, 1), (0, 1)])], 1)
+    tiny = [11, 140, V - 3]
+    target = torch.full((2, V), -0.0)
+    target[0, tiny] = torch.tensor([1e-42, 3e-42, 2e-42])
+    draft = torch.full((2, V), -0.0)
+    draft[0, 5] = 1.0
+    tok = torch.tensor([0, 5], dtype=torch.int32)
+    for un, want in ((0.0, tiny[0]), (0.16, tiny[0]), (0.17, tiny[1]), (0.66, tiny[1]), (0.67, tiny[2]),
+                     (1 - 2.0 ** -24, tiny[2])):
+        status, n, nxt, path = _run(tree, tok, target, draft if sampled else None, torch.full((2,), 0.5),
+                                    torch.tensor([un]))
+        assert status == 0 and n.tolist() == [0] and nxt.tolist() == [want]
+
+
 def test_bad_tokens_and_spare_rows():
     tree = TREES["mixed"]()
     tok, target, draft, u, un = _draw(tree, 64, 1, True, torch.float32)

@@ -20,8 +20,10 @@
 // A cluster of 8 (or 16) blocks walks one request: every block takes its part of
 // the vocabulary in each pass and repeats the walk's decisions from the same
 // numbers (sums are exchanged through distributed shared memory in a fixed
-// order).  Bound by the latency of the walk's dependent loads for one tree,
-// by the rows' bytes for a batch.
+// order).  Bound by latency: of the walk's dependent loads for one tree (8192
+// point masses: 9 us), of the passes of the tree that rejects most for a batch
+// (64 sampled trees, 131072 entries: 43 us; every tree's first pass ends after 11 to
+// 18 us, the last trees take 6 to 7 for each further one).
 #include <cooperative_groups.h>
 
 #include "common.cuh"
@@ -55,6 +57,19 @@ __device__ __forceinline__ double warp_sum_d(double v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
+}
+
+// prob_of(v) 2^-896: the float's bits moved to where a double has them, subnormal
+// numbers too.  A pass converts two entries of every kind of token, and the
+// conversion instruction has a sixteenth of the shifts' rate.
+__device__ __forceinline__ double small_prob(float v) {
+  const uint32_t b = __float_as_uint(fmaxf(v, 0.f));  // (of NaN and 0: 0; of -0 and 0: 0)
+  return __hiloint2double((int)(b >> 3), (int)(b << 29));
+}
+// x where it is positive, else 0; x is a number
+__device__ __forceinline__ double positive_part(double x) {
+  const int keep = ~(__double2hiint(x) >> 31);
+  return __hiloint2double(__double2hiint(x) & keep, __double2loint(x) & keep);
 }
 
 template <int k>
@@ -200,18 +215,28 @@ verify_kernel(const VerifyParams p) {
           double w[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            if (kKind == 1) w[i] = fmax(fma(-c, (double)fmaxf(qv[i], 0.f), (double)fmaxf(pv[i], 0.f)), 0.);
-            else if (kKind == 0) w[i] = (double)fmaxf(pv[i], 0.f);
+            if (kKind == 1) w[i] = positive_part(fma(-c, small_prob(qv[i]), small_prob(pv[i])));
+            else if (kKind == 0) w[i] = small_prob(pv[i]);
             else w[i] = weight(v_lo + (s0 + k * kVWarps) * seg_len + o + i, pv[i], 0.f);
           }
           acc[k] += (w[0] + w[1]) + (w[2] + w[3]);
         }
       }
+      // the four segments' sums over the lanes: halves of the warp take two of them
+      // each, quarters one, so six exchanges stand for twenty
+      static_assert(kAhead == 4, "a segment to a quarter of the warp");
+      const bool up = lane & 16, right = lane & 8;
+      double x = up ? acc[2] : acc[0], y = up ? acc[3] : acc[1];
+      x += __shfl_xor_sync(0xffffffffu, up ? acc[0] : acc[2], 16);
+      y += __shfl_xor_sync(0xffffffffu, up ? acc[1] : acc[3], 16);
+      double t = right ? y : x;
+      t += __shfl_xor_sync(0xffffffffu, right ? x : y, 8);
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        const double t = warp_sum_d(acc[k]);
-        if (lane == 0 && s0 + k * kVWarps < n_seg) sh.seg[s0 + k * kVWarps] = t;
-      }
+      for (int o = 4; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+      if (kKind != 2) t *= 0x1p896;
+      if (kKind != 2 && t >= 0x1p128) t = INFINITY;  // an infinite entry
+      const int k = lane >> 3;
+      if ((lane & 7) == 0 && s0 + k * kVWarps < n_seg) sh.seg[s0 + k * kVWarps] = t;
     }
   };
   // sum of the weights over the vocabulary, the same bits in every block;
@@ -367,23 +392,34 @@ verify_kernel(const VerifyParams p) {
   const int s = to_end ? s_last : s_hit;
   const int a = v_lo + s * seg_len, b = min(v_hi, a + seg_len);
   int pick = -1, positive = -1;
-  for (int v0 = a; v0 < b; v0 += 32) {
-    const int v = v0 + lane;
-    const double w = v < b ? weight(v, load_f(prow + v), load_f(qrow + v)) : 0.;
-    double incl = w;
+  for (int v0 = a; v0 < b; v0 += 128) {  // four entries to a lane
+    const int v = v0 + 4 * lane;
+    const float4 pv = load4<T, kVec>(prow, v, b), qv = load4<T, kVec>(qrow, v, b);
+    const double w[4] = {weight(v, pv.x, qv.x), weight(v + 1, pv.y, qv.y), weight(v + 2, pv.z, qv.z),
+                         weight(v + 3, pv.w, qv.w)};
+    double upto4 = (w[0] + w[1]) + (w[2] + w[3]);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const double y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += y;
+      const double y = __shfl_up_sync(0xffffffffu, upto4, o);
+      if (lane >= o) upto4 += y;
     }
-    const unsigned pos = __ballot_sync(0xffffffffu, w > 0.);
-    if (pos) positive = v0 + 31 - __clz(pos);
-    const unsigned hit = __ballot_sync(0xffffffffu, !to_end && w > 0. && acc + incl > aim);
+    // the sums before each of the lane's entries
+    double at = __shfl_up_sync(0xffffffffu, upto4, 1);
+    at = acc + (lane ? at : 0.);
+    int mine = -1, some = -1;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      at += w[i];
+      if (w[i] > 0.) some = v + i;
+      if (!to_end && mine < 0 && w[i] > 0. && at > aim) mine = v + i;
+    }
+    positive = max(positive, __reduce_max_sync(0xffffffffu, some));
+    const unsigned hit = __ballot_sync(0xffffffffu, mine >= 0);
     if (hit) {
-      pick = v0 + __ffs(hit) - 1;
+      pick = __shfl_sync(0xffffffffu, mine, __ffs(hit) - 1);
       break;
     }
-    acc += __shfl_sync(0xffffffffu, incl, 31);
+    acc += __shfl_sync(0xffffffffu, upto4, 31);
   }
   if (lane == 0) p.next_token[r] = pick >= 0 ? pick : positive;
 }
@@ -431,8 +467,8 @@ extern "C" int flide_verify_draft(const flide_tree_index *idx, const int32_t *to
     // rows of whole 16-byte (bf16: 8-byte) words are read as such
   const bool vec = V % 4 == 0 && ((uintptr_t)target | (uintptr_t)draft) % 16 == 0;
   // 16 blocks to a cluster where every tree has its 16 at once and its rows are
-  // long: a pass over 131072 entries takes 4 us instead of 6, the wider exchange
-  // costs 2 us a call (8192 entries: 11 instead of 9 us)
+  // long: a pass over 131072 entries takes 3.5 us instead of 6, the wider
+  // exchange costs 2 us a call (8192 entries: 11 instead of 9 us)
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
