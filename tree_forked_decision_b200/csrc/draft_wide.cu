@@ -62,7 +62,7 @@ enum {
   bVFree = bV + kMaxStages,   // [stages]
   bS = bVFree + kMaxStages,   // [2 S buffers]
   bP = bS + 2,                // [2], 4 warps
-  bOFree = bP + 2,            // [2], 4 warps
+  bOFree = bP + 2,            // [2], the 4 warps of an S buffer, or (copies) all 8
   bO = bOFree + 2,
   bMerge = bO + 1,            // 8 warps
   bDrain = bMerge + 1,
@@ -120,7 +120,8 @@ draft_part_wide(const __grid_constant__ WideMaps maps, const DraftParams p, int 
   asm volatile("griddepcontrol.launch_dependents;");
   if (tid == 0) {
     for (int i = 0; i < kBars; ++i)
-      mbar_init(bar(i), (i >= bP && i < bP + 2) || (i >= bOFree && i < bOFree + 2) ? 4u : i == bMerge ? 8u : 1u);
+      mbar_init(bar(i), i >= bP && i < bP + 2 ? 4u
+                        : i >= bOFree && i < bOFree + 2 ? (kRep > 1 ? 8u : 4u) : i == bMerge ? 8u : 1u);
     fence_mbar_init();
     ms.abort = 0;
   }
@@ -457,11 +458,12 @@ draft_part_wide(const __grid_constant__ WideMaps maps, const DraftParams p, int 
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(bOFree + h));
       } else {
-        // The copies' results become one.  A row's sharers are kRep warps of each S
-        // buffer; they add a chunk of columns each to the buffer in shared memory
-        // and move on to the next, so every sum has one order.
-        constexpr int kShare = 2 * kRep, kChunk = 128 / kShare;
-        const int mine = h * kRep + row / kCopy, r = row % kCopy, wid = warp;
+        // The copies' results become one.  A warp adds the two S buffers' (both are its
+        // TMEM lanes), in one half of the columns; the kRep warps that share a row
+        // there then add a chunk of columns each to the buffer in shared memory and
+        // move on to the next, so every sum has one order.
+        constexpr int kChunk = 64 / kRep;
+        const int mine = row / kCopy, r = row % kCopy, wid = warp;
         float *buf = reinterpret_cast<float *>(smem + s_m), *st_m = buf + kCopy * 132, *st_l = st_m + 256;
         if (h >= steps) m = -INFINITY;
         st_m[wid * 32 + lane] = m - kShift;
@@ -469,46 +471,56 @@ draft_part_wide(const __grid_constant__ WideMaps maps, const DraftParams p, int 
         if (!(ok = meet())) break;
         float top = -INFINITY, all = 0.f;
 #pragma unroll
-        for (int k = 0; k < kShare; ++k) {  // sharer k's warp: S buffer k / kRep, this row's quadrant of copy k % kRep
+        for (int k = 0; k < 2 * kRep; ++k) {  // S buffer k / kRep, this row's quadrant of copy k % kRep
           const int wk = (k / kRep) * 4 + (k % kRep) * (4 / kRep) + (warp & 3) % (4 / kRep);
           top = fmaxf(top, st_m[wk * 32 + lane]);
         }
 #pragma unroll
-        for (int k = 0; k < kShare; ++k) {
+        for (int k = 0; k < 2 * kRep; ++k) {
           const int wk = (k / kRep) * 4 + (k % kRep) * (4 / kRep) + (warp & 3) % (4 / kRep);
           all += st_l[wk * 32 + lane] * (top == -INFINITY ? 0.f : ex2_approx(st_m[wk * 32 + lane] - top));
         }
-        const float f = m == -INFINITY ? 0.f : ex2_approx(m - kShift - top);
+        float f[2];  // of this copy's O in each S buffer
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float mk = st_m[((warp & 3) + 4 * k) * 32 + lane];
+          f[k] = mk == -INFINITY ? 0.f : ex2_approx(mk - top);
+        }
 #pragma unroll 1
-        for (int k = 0; k < kShare && ok; ++k) {
-          const int c0 = (mine + k) % kShare * kChunk;
-          uint32_t v[kChunk];
-          if constexpr (kChunk == 16) tmem_ld16(t_o + c0, v);
-          else tmem_ld32(t_o + c0, v);
+        for (int k = 0; k < kRep && ok; ++k) {
+          const int c0 = 64 * h + (mine + k) % kRep * kChunk;
+          uint32_t v[2][kChunk];
+          if constexpr (kChunk == 16) {
+            tmem_ld16(tl + 128 + c0, v[0]);
+            tmem_ld16(tl + 384 + c0, v[1]);
+          } else {
+            tmem_ld32(tl + 128 + c0, v[0]);
+            tmem_ld32(tl + 384 + c0, v[1]);
+          }
           float4 *to = reinterpret_cast<float4 *>(buf + r * 132 + c0);
 #pragma unroll
           for (int j = 0; j < kChunk / 4; ++j) {
-            float4 o = k > 0 ? to[j] : make_float4(0.f, 0.f, 0.f, 0.f);
-            if (h < steps) {
-              o.x = fmaf(f, __uint_as_float(v[4 * j]), o.x);
-              o.y = fmaf(f, __uint_as_float(v[4 * j + 1]), o.y);
-              o.z = fmaf(f, __uint_as_float(v[4 * j + 2]), o.z);
-              o.w = fmaf(f, __uint_as_float(v[4 * j + 3]), o.w);
+            float o[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              o[i] = f[0] * __uint_as_float(v[0][4 * j + i]);
+              if (steps > 1) o[i] = fmaf(f[1], __uint_as_float(v[1][4 * j + i]), o[i]);  // (else never written)
             }
-            to[j] = o;
+            const float4 was = k > 0 ? to[j] : make_float4(0.f, 0.f, 0.f, 0.f);
+            to[j] = make_float4(was.x + o[0], was.y + o[1], was.z + o[2], was.w + o[3]);
           }
           ok = meet();
         }
         if (!ok) break;
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(bOFree + h));
+        if (lane < 2) mbar_arrive(bar(bOFree + lane));
         const size_t at = (size_t)run.slot * kCopy;
         for (int e = tid; e < kCopy * 32; e += 256)
           if (e / 32 < limit)
             *reinterpret_cast<float4 *>(p.part_o + (at + e / 32) * 128 + 4 * (e & 31)) =
                 *reinterpret_cast<const float4 *>(buf + e / 32 * 132 + 4 * (e & 31));
-        if (mine == 0 && r < limit) *reinterpret_cast<float2 *>(p.part_ml + 2 * (at + r)) = make_float2(top, all);
+        if (h == 0 && mine == 0 && r < limit) *reinterpret_cast<float2 *>(p.part_ml + 2 * (at + r)) = make_float2(top, all);
       }
       kt0 += tiles;
     }
