@@ -564,27 +564,31 @@ struct Row8 {
   static __device__ __forceinline__ int at(int e, int l) { return (8 * (e / kW) + l) * kW + e % kW; }
 };
 
-// bf16 and e4m3, d of 64 or 128: one warp per (token, query head) as four groups
-// of eight lanes, each with its own running (max, sum, O) over every fourth key
-// of the token's path and every fourth partial of its history; joined by shuffles
-// at the end.  Bound by latency: five dependent loads stand before the path's
-// first product and two before the first partial, so rows are kept apart (a warp
-// for all heads of a group took 5 us a head) and few registers let 32 warps share
-// an SM.  Starts beside the part kernel (programmatic launch) and waits for its
-// results only where it needs them.
+// bf16 and e4m3, d of 64 or 128: a warp is four groups of eight lanes, each with
+// its own running (max, sum, O).  Few rows: a warp to a (token, query head), each
+// group takes every fourth key of the token's path and every fourth partial of its
+// history, joined by shuffles at the end.  Many rows: two or four heads of a
+// group's K/V head to a warp, which list the path once and load its keys once.
+// Bound by latency: five dependent loads stand before the path's first product and
+// two before the first partial.  Starts beside the part kernel (programmatic
+// launch) and waits for its results only where it needs them, so what counts is
+// that all warps run at once.  1, 2, 4 heads to a warp, whole call: 80 rows of 16
+// partials 14, 16, 18 us; 10240 rows 72, 64, 61; 16384 rows 312, 297, 291.  Half the
+// registers and 32 warps to an SM spill (10240 rows: 68 us with four heads).
 constexpr int kJoinWarps = 8;
 constexpr int kPath = 64;  // keys of a path listed at a time
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kJoinWarps * 32, 4) draft_join_kernel(const DraftParams p) {
+template <typename T, int D, int kHeads>
+__global__ void __launch_bounds__(kJoinWarps * 32, 2) draft_join_kernel(const DraftParams p) {
+  constexpr int kKeys = 4 / kHeads;  // groups that share a head's keys and partials
   using Row = Row8<T, D>;
   constexpr int kE = Row::kE;
   __shared__ int path_rows[kJoinWarps][kPath];
   const flide_tree_index &x = p.x;
-  const int lane = threadIdx.x & 31, grp = lane >> 3, l8 = lane & 7;
+  const int lane = threadIdx.x & 31, grp = (lane >> 3) / kHeads, l8 = lane & 7;
   int *path = path_rows[threadIdx.x >> 5];
-  const long long job = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-  const int t = (int)(job / p.Hq), h = (int)(job - (long long)t * p.Hq), hk = h / p.G;
+  const unsigned job = blockIdx.x * kJoinWarps + (threadIdx.x >> 5), sets = (unsigned)p.Hq / kHeads;
+  const int t = (int)(job / sets), h = (int)(job - t * sets) * kHeads + (lane >> 3) % kHeads, hk = h / p.G;
   const size_t head = (size_t)t * p.Hq + h;
   // what t alone addresses is loaded at once (the last block's rows past the capacity
   // take its last token's); a token past the stream's has no node
@@ -616,13 +620,19 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) draft_join_kernel(const Dr
         for (int i = max(b0, end - len); i < min(b0 + kPath, end); ++i) path[i - b0] = first + i - (end - len);
         __syncwarp();
         const int cnt = min(kPath, total - b0);
-        for (int k0 = 0; k0 < cnt; k0 += 4) {
-          const bool on = k0 + grp < cnt;
-          const int key = (int)checked(x.status, x.counts, path[on ? k0 + grp : 0], x.counts[FLIDE_CNT_T], 805);
+        uint4 kw[Row::kWords], vw[Row::kWords];
+        auto key_at = [&](int i, uint4 (&kn)[Row::kWords], uint4 (&vn)[Row::kWords]) {
+          const int key = (int)checked(x.status, x.counts, path[i < cnt ? i : 0], x.counts[FLIDE_CNT_T], 805);
           const size_t at = ((size_t)key * p.Hkv + hk) * D;
-          uint4 kw[Row::kWords], vw[Row::kWords];
-          Row::load(K + at, l8, kw);
-          Row::load(Vs + at, l8, vw);
+          Row::load(K + at, l8, kn);
+          Row::load(Vs + at, l8, vn);
+        };
+        if (kHeads > 1) key_at(grp, kw, vw);
+        for (int k0 = 0; k0 < cnt; k0 += kKeys) {
+          const bool on = k0 + grp < cnt;
+          uint4 kn[Row::kWords], vn[Row::kWords];  // several heads: the next key's, a step ahead
+          if (kHeads == 1) key_at(k0 + grp, kw, vw);
+          else if (k0 + kKeys < cnt) key_at(k0 + kKeys + grp, kn, vn);
           float f[kE], s = 0.f;
           {
             float qv[kE];
@@ -634,15 +644,23 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) draft_join_kernel(const Dr
           s += __shfl_xor_sync(0xffffffffu, s, 1);
           s += __shfl_xor_sync(0xffffffffu, s, 2);
           s += __shfl_xor_sync(0xffffffffu, s, 4);
-          if (!on) continue;
-          s *= qk_scale;
-          const float mn = fmaxf(m, s), ref = mn == -INFINITY ? 0.f : mn;
-          const float o = ex2_approx(m - ref), w = ex2_approx(s - ref);
-          l = l * o + w;
-          m = mn;
-          Row::unpack(vw, f);
+          if (on) {
+            s *= qk_scale;
+            const float mn = fmaxf(m, s), ref = mn == -INFINITY ? 0.f : mn;
+            const float o = ex2_approx(m - ref), w = ex2_approx(s - ref);
+            l = l * o + w;
+            m = mn;
+            Row::unpack(vw, f);
 #pragma unroll
-          for (int e = 0; e < kE; ++e) acc[e] = fmaf(w, f[e], acc[e] * o);
+            for (int e = 0; e < kE; ++e) acc[e] = fmaf(w, f[e], acc[e] * o);
+          }
+          if (kHeads > 1) {
+#pragma unroll
+            for (int i = 0; i < Row::kWords; ++i) {
+              kw[i] = kn[i];
+              vw[i] = vn[i];
+            }
+          }
         }
       }
     }
@@ -670,12 +688,12 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) draft_join_kernel(const Dr
     float2 ml;
     float4 v[kE / 4];
     if (grp < parts) partial(grp, ml, v);
-    for (int i = grp; i < parts; i += 4) {
+    for (int i = grp; i < parts; i += kKeys) {
       const float2 ml0 = ml;
       float4 v0[kE / 4];
 #pragma unroll
       for (int e = 0; e < kE / 4; ++e) v0[e] = v[e];
-      if (i + 4 < parts) partial(i + 4, ml, v);
+      if (i + kKeys < parts) partial(i + kKeys, ml, v);
       if (ml0.x == -INFINITY) continue;  // an empty partial
       const float mn = fmaxf(m, ml0.x);
       const float f = ex2_approx(m - mn), g = ex2_approx(ml0.x - mn);
@@ -690,29 +708,30 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) draft_join_kernel(const Dr
       }
     }
   }
-  // the four groups' results
-  float mt = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
-  mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 16));
+  // the results of a head's groups
+  float mt = m;
+#pragma unroll
+  for (int o = 8 * kHeads; o < 32; o *= 2) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
   const float f = m == -INFINITY ? 0.f : ex2_approx(m - mt);
   l *= f;
-  l += __shfl_xor_sync(0xffffffffu, l, 8);
-  l += __shfl_xor_sync(0xffffffffu, l, 16);
+#pragma unroll
+  for (int o = 8 * kHeads; o < 32; o *= 2) l += __shfl_xor_sync(0xffffffffu, l, o);
   const float inv = (p.descale ? p.descale[2] : 1.f) / l;
 #pragma unroll
   for (int e = 0; e < kE; ++e) {
     acc[e] *= f;
-    acc[e] += __shfl_xor_sync(0xffffffffu, acc[e], 8);
-    acc[e] += __shfl_xor_sync(0xffffffffu, acc[e], 16);
+#pragma unroll
+    for (int o = 8 * kHeads; o < 32; o *= 2) acc[e] += __shfl_xor_sync(0xffffffffu, acc[e], o);
     acc[e] *= inv;
   }
-  // a group stores a quarter of its lanes' elements (64: the first two groups a half)
+  // a group stores its share of its lanes' elements, four at a time
   __nv_bfloat16 *O = static_cast<__nv_bfloat16 *>(p.out) + head * D;
 #pragma unroll
   for (int e = 0; e < kE; e += 4)
-    if (e / 4 == grp)
+    if (e / 4 % kKeys == grp)
       *reinterpret_cast<uint2 *>(O + Row::at(e, l8)) =
           make_uint2(pack_bf16x2(acc[e], acc[e + 1]), pack_bf16x2(acc[e + 2], acc[e + 3]));
-  if (p.lse && lane == 0) p.lse[head] = (mt + log2f(l)) * kLn2D;
+  if (p.lse && grp == 0 && l8 == 0) p.lse[head] = (mt + log2f(l)) * kLn2D;
 }
 
 // ---- host ----------------------------------------------------------------------
@@ -796,9 +815,9 @@ int join_portable_launch(const DraftParams &p, cudaStream_t s) {
   return FLIDE_OK;
 }
 
-template <typename T, int D>
-int join_launch(const DraftParams &p, cudaStream_t s) {
-  const long long warps = (long long)p.x.T * p.Hq;
+template <typename T, int D, int kHeads>
+int join_of(const DraftParams &p, cudaStream_t s) {
+  const long long warps = (long long)p.x.T * (p.Hq / kHeads);
   cudaLaunchAttribute at;
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
@@ -808,7 +827,17 @@ int join_launch(const DraftParams &p, cudaStream_t s) {
   cfg.stream = s;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return launched(cudaLaunchKernelEx(&cfg, draft_join_kernel<T, D>, p));
+  return launched(cudaLaunchKernelEx(&cfg, draft_join_kernel<T, D, kHeads>, p));
+}
+
+template <typename T, int D>
+int join_launch(const DraftParams &p, int sms, cudaStream_t s) {
+  const long long rows = (long long)p.x.T * p.Hq, at_once = 2ll * kJoinWarps * sms;
+  // as many heads to a warp as it takes for all warps to run at once (16 to an SM); a
+  // wave of them that starts after the part kernel repeats the path's loads behind it
+  if (rows <= at_once || p.G % 2) return join_of<T, D, 1>(p, s);
+  if (rows <= 2 * at_once || p.G % 4) return join_of<T, D, 2>(p, s);
+  return join_of<T, D, 4>(p, s);
 }
 
 int draft_attn(const void *q, const void *k, const void *v, const void *past_k, const void *past_v,
@@ -876,8 +905,8 @@ int draft_attn(const void *q, const void *k, const void *v, const void *past_k, 
                              : mma_launch<64, false, 2>(p, dev, sms, s);
   }
   if (rc != FLIDE_OK) return rc;
-  if (dtype == FLIDE_E4M3) return join_launch<uint8_t, 128>(p, s);
-  return d == 128 ? join_launch<__nv_bfloat16, 128>(p, s) : join_launch<__nv_bfloat16, 64>(p, s);
+  if (dtype == FLIDE_E4M3) return join_launch<uint8_t, 128>(p, sms, s);
+  return d == 128 ? join_launch<__nv_bfloat16, 128>(p, sms, s) : join_launch<__nv_bfloat16, 64>(p, sms, s);
 }
 
 }  // namespace
