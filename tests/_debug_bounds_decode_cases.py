@@ -49,7 +49,7 @@ def _calls(tree, idx, d, dtype):
 def run(out_dir):
     res, arrays = {"debug_bounds": int(flide._lib().flide_debug_bounds())}, {}
     chain = [(0, 1), (0, 1), (1, 2), (1, 1)]
-    for tag, nodes, d, dtype in (("mma16", [(0, 1)], 128, torch.bfloat16), ("tile32", chain, 128, torch.bfloat16),
+    for tag, nodes, d, dtype in (("mma16", [(0, 1)], 64, torch.bfloat16), ("tile32", chain, 128, torch.bfloat16),
                                  ("tile128", chain * 5, 128, torch.bfloat16), ("portable", chain, 96, torch.float32)):
         tree, idx = _setup(nodes)
         for name, x in _calls(tree, idx, d, dtype).items():

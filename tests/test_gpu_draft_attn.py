@@ -109,17 +109,20 @@ def test_packed(case, kind):
 def test_paged_with_nan_behind_the_rows(case, block_rows, kind):
     """Rows of a block past a history's end hold NaN, and belong to nobody."""
     tree = TREES[case]()
-    Hq, Hkv, d = 16, 4, 128
-    x, hist, ds = _inputs(tree, Hq, Hkv, d, kind, 9)
-    pools, table, slots, width = dh.scatter(hist, block_rows, np.random.default_rng(block_rows), fill=math.nan)
-    _, idx = build(tree)
-    q, k, v = _dev(x)
-    scale = 1 / math.sqrt(d)
-    out, lse = flide.draft_attn_paged(q, k, v, idx, scale, pools[0].cuda(), pools[1].cuda(), table.cuda(),
-                                      slots.cuda(), block_rows, width, descale=None if ds is None else ds.cuda())
-    torch.cuda.synchronize()
-    assert idx.status() == 0
-    _check(tree, x, hist, ds, scale, out, lse, kind)
+    shapes = [(16, 4, 128)]
+    if case in ("edges", "many"):  # head layouts and sizes without a tcgen05 tile
+        shapes += [(5, 1, 128), (20, 1, 128)] + ([] if kind == "e4m3" else [(8, 2, 64), (16, 1, 64)])
+    for Hq, Hkv, d in shapes:
+        x, hist, ds = _inputs(tree, Hq, Hkv, d, kind, 9)
+        pools, table, slots, width = dh.scatter(hist, block_rows, np.random.default_rng(block_rows), fill=math.nan)
+        _, idx = build(tree)
+        q, k, v = _dev(x)
+        scale = 1 / math.sqrt(d)
+        out, lse = flide.draft_attn_paged(q, k, v, idx, scale, pools[0].cuda(), pools[1].cuda(), table.cuda(),
+                                          slots.cuda(), block_rows, width, descale=None if ds is None else ds.cuda())
+        torch.cuda.synchronize()
+        assert idx.status() == 0
+        _check(tree, x, hist, ds, scale, out, lse, kind)
 
 
 @pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf, torch.finfo(torch.bfloat16).min])

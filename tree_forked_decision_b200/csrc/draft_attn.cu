@@ -736,11 +736,17 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 2) draft_join_kernel(const Dr
 
 // ---- host ----------------------------------------------------------------------
 
-// Which part kernel, by the query rows of a request on average (the capacities:
-// the host sees no more): up to 16 rows a 16-row tile, and above that, where the
-// tcgen05 kernel takes the type and head layout, its smallest tile that holds
-// them (bf16 up to 256 rows, e4m3 128); elsewhere 32-row tiles, each a pass over
-// the keys.
+// Which part kernel.  The tcgen05 kernel, where it takes the type and head layout,
+// with its smallest tile that holds a request's query rows on average (the
+// capacities: the host sees no more; bf16 up to 256 rows, e4m3 128); elsewhere
+// 16-row tiles or 32-row tiles, each a pass over the keys, on mma.sync.  One
+// request's decoding, 4 rows a K/V head: 65536 rows of history 55 us in a 32-row
+// tile, 74 in the 16-row kernel; 64 requests of 4096 rows 111 and 167; 512 rows 13
+// and 11 (e4m3 65536: 44 and 49; 16 requests of 512: 18 and 15).  8 requests over
+// 32768 rows, 64 rows to a head: 167 us in a 64-row tile, 187 in a 128-row tile, 272
+// in a 256-row tile, 407 in 32-row tiles on mma.sync; 128 rows: 190 in a 128-row
+// tile, 277 in a 256-row tile; 64 requests of 512 rows, 4 rows: 39 us in a 32-row
+// tile, 42 in a 64-row tile.
 enum Kernel { kPortable, kMma, kWide };
 struct Variant {
   Kernel kernel;
@@ -750,8 +756,8 @@ struct Variant {
 Variant variant_of(long long R, long long T, int G, int d, int dtype) {
   if (dtype == FLIDE_F32 || (d != 64 && d != 128)) return {kPortable, 16, 0};
   const long long rows = (T * G + R - 1) / (R > 0 ? R : 1);
-  if (rows <= 16) return {kMma, 16, 0};
-  if (d != 128 || 128 % G || R > 1024) return {kMma, 32, 0};  // (the tiles leave room for 1024 list entries)
+  // (the tiles leave room for 1024 list entries)
+  if (d != 128 || 128 % G || R > 1024) return {kMma, rows <= 16 ? 16 : 32, 0};
   if (rows <= 32 && G <= 32) return {kWide, 32, 0};
   if (rows <= 64 && G <= 64) return {kWide, 64, 0};
   if (rows <= 128 || dtype == FLIDE_E4M3) return {kWide, 128, 1};

@@ -135,10 +135,13 @@ __global__ void __launch_bounds__(kMThreads) mass_kernel_portable(const MassPara
 // Bound by K's bytes, and so by what is on its way: each lane copies the very
 // words it will need to its own places in shared memory (8 KB a warp), a head or
 // more ahead and past the end of a group of rows; no lane reads another's words,
-// so nothing but the copies is waited for.  After that by the latency of a head's
-// 260 instructions: 16 histories of 1024 to 16384 rows, 4 root tokens of 32 heads
-// took 73 us with 8 warps an SM, 63 with 12, 59 with 16.  Blocks share the batch's
-// groups of 16 rows evenly: a warp has about three.
+// so nothing but the copies is waited for.  K leaves L2 before other lines: it is
+// read once.  Blocks share the batch's groups of 16 rows evenly, a block's warps
+// the (group, head) steps of its share; parts of a group are added in order at the
+// end.  16 histories of 1024 to 16384 rows, 4 root tokens of 32 heads (238 MB):
+// 48 us, 5.0 TB/s, of which 6 before the first product and 34 in the loop at 7
+// TB/s.  8 warps an SM instead of 16: 14 us more; whole groups to a warp (four
+// rounds where 3.1 would do) 5 more; the queries behind the ring's copies 5 more.
 constexpr int kMassWarps = 16;
 constexpr int kRing = 8192;  // bytes of a warp's ring
 constexpr int kMassExtra = 5;  // groups that a block's start on a request costs beside its own (3 us of 0.7)
