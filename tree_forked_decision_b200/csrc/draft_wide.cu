@@ -348,7 +348,7 @@ draft_part_wide(const __grid_constant__ WideMaps maps, const DraftParams p, int 
         const float mt = c * fmaxf(fmax3f(mx[0], mx[1], mx[2]), fmax3f(fmax3f(mx[3], mx[4], mx[5]), mx[6], mx[7]));
         if (i < 2) {
           m = mt;
-        } else if (__any_sync(0xffffffffu, mt > m + (F8 ? 2.f : 8.f))) {
+        } else if (__any_sync(0xffffffffu, mt > m + (F8 ? 2.75f : 8.f))) {
           // this buffer's last PV is complete: it was issued before this S
           const float mn = fmaxf(m, mt), f = mn == -INFINITY ? 1.f : exp2f(m - mn);
 #pragma unroll 1
