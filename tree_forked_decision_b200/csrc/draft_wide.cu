@@ -22,19 +22,20 @@
 //
 // e4m3: S and O come from the codes (kind::f8f6f4, exact products).  A weight in
 // e4m3 would be 2^-4 off, so it goes in as two codes, its own and its remainder's:
-// two products at twice the rate.  Scaled by 2^6 (its reference is at most 4 below
-// the row's maximum), a weight is off by 2^-8 of itself or 2^-16 of the row's
-// largest.  (Widening V to half in the softmax warps instead: 13 us more of 110.)
+// two products at twice the rate.  Scaled by 2^6, a weight is off by 2^-8 of
+// itself or 2^-16 of the row's largest; a row's reference is raised once a score
+// passes it by 2.75 (2^8.75 < 448, the format's largest; raised at 2, some warp of
+// a tile had to rescale O in most of a history's first tiles: 82 us instead of 78).  (Widening V to half in the softmax warps instead: 13 us more of 110.)
 //
 // 256 rows are bound by the two warpgroups' softmax and the MMA issue (see
 // attn_tc.cu): 2.35 us a key tile where its bytes would take 1.5; 8 requests of 64
-// tokens over 32768 rows, 32 + 8 heads, 287 us a call, 960 TFLOP/s.  128 rows and
+// tokens over 32768 rows, 32 + 8 heads, 290 us a call, 950 TFLOP/s.  128 rows and
 // fewer by the history's bytes and the ends of runs: a tile takes 1.25 us (bytes
 // 1.5, part of them from L2), a block's first scores come after 8 us, a run's
 // end takes 4 to 5; 16 histories of 512 to 8192 rows, 20 tokens each, 61 us a call,
 // 4.2 TB/s.  e4m3, 32 rows: 0.93 us a tile (bytes 0.75), bound by its twelve
 // products (1.75K cycles); a run's end 3 us; 16 histories of 1024 to 16391 rows, 8
-// tokens each, 80 us a call, 3.8 TB/s.  Histories that one tile reads leave L2
+// tokens each, 78 us a call, 3.9 TB/s.  Histories that one tile reads leave L2
 // before other lines (16 x 8192 rows: 75 -> 68 us).  Every wait is bounded (2 s);
 // on expiry the block records FLIDE_ERR_TIMEOUT, waits for its own copies and
 // MMAs, frees TMEM and ends.
