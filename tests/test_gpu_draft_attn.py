@@ -36,7 +36,7 @@ TREES = {
     "many": lambda: inputs._tree([(int(n), [(-1, 1 + i % 3), (0, 1), (0, 2), (1, 1)]) for i, n in
                                   enumerate(np.random.default_rng(1).integers(0, 400, 37))], 2),
 }
-HEADS = [(4, 4), (16, 4), (8, 1), (12, 3), (5, 1), (40, 2)]
+HEADS = [(4, 4), (16, 4), (8, 1), (12, 3), (5, 1), (40, 2), (14, 2), (129, 1), (100, 1)]
 
 
 def _inputs(tree, Hq, Hkv, d, kind, seed):
@@ -110,8 +110,8 @@ def test_paged_with_nan_behind_the_rows(case, block_rows, kind):
     """Rows of a block past a history's end hold NaN, and belong to nobody."""
     tree = TREES[case]()
     shapes = [(16, 4, 128)]
-    if case in ("edges", "many"):  # head layouts and sizes without a tcgen05 tile
-        shapes += [(5, 1, 128), (20, 1, 128)] + ([] if kind == "e4m3" else [(8, 2, 64), (16, 1, 64)])
+    if case in ("edges", "many"):  # tiles with rows to spare; heads without a tcgen05 tile
+        shapes += [(5, 1, 128), (21, 3, 128), (20, 1, 128), (130, 1, 128)] + ([] if kind == "e4m3" else [(8, 2, 64), (16, 1, 64)])
     for Hq, Hkv, d in shapes:
         x, hist, ds = _inputs(tree, Hq, Hkv, d, kind, 9)
         pools, table, slots, width = dh.scatter(hist, block_rows, np.random.default_rng(block_rows), fill=math.nan)
@@ -123,6 +123,24 @@ def test_paged_with_nan_behind_the_rows(case, block_rows, kind):
         torch.cuda.synchronize()
         assert idx.status() == 0
         _check(tree, x, hist, ds, scale, out, lse, kind)
+
+
+@pytest.mark.parametrize("kind,d", [("bf16", 128), ("bf16", 64), ("e4m3", 128), ("f32", 64)])
+@pytest.mark.parametrize("R", [1024, 1025, 2048])
+def test_many_requests(R, kind, d):
+    """One or two tokens a request, up to the most requests of a call."""
+    rng = np.random.default_rng(R)
+    tree = inputs._tree([(int(n), [(-1, 1 + i % 2)]) for i, n in enumerate(rng.integers(0, 40, R))], 0)
+    x, hist, ds = _inputs(tree, 8, 2, d, kind, 4)
+    pools, table, slots, width = dh.scatter(hist, 16, rng)
+    _, idx = build(tree)
+    q, k, v = _dev(x)
+    scale = 1 / math.sqrt(d)
+    out, lse = flide.draft_attn_paged(q, k, v, idx, scale, pools[0].cuda(), pools[1].cuda(), table.cuda(), slots.cuda(),
+                                      16, width, descale=None if ds is None else ds.cuda())
+    torch.cuda.synchronize()
+    assert idx.status() == 0
+    _check(tree, x, hist, ds, scale, out, lse, kind)
 
 
 @pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf, torch.finfo(torch.bfloat16).min])

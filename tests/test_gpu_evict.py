@@ -91,6 +91,37 @@ def test_mass_sums_to_the_tokens_and_heads():
     assert np.allclose(got.numpy(), [3 * 16, 16], rtol=1e-5)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_mass_of_many_requests(kind):
+    """The most requests of a call, each with one group of rows or two."""
+    R, Hq, Hkv, d = 2048, 8, 2, 128
+    rng = np.random.default_rng(2)
+    tree = inputs._tree([(int(n), [(-1, 1 + i % 2)]) for i, n in enumerate(rng.integers(0, 20, R))], 0)
+    x, hist, ds = _inputs(tree, Hq, Hkv, d, kind, 8)
+    s = [None] * 3 if ds is None else ds
+    scale = 1 / math.sqrt(d)
+    pk = [_wide(h, s[1]) for h in hist[0]]
+    _, lse, _, _, size = dh.attention(tree, *[_wide(y, z) for y, z in zip(x, s)], pk,
+                                      [_wide(h, s[2]) for h in hist[1]], scale)
+    lse = lse.float()
+    pools, table, slots, width = dh.scatter(hist[:1], 16, rng, extra=2)
+    _, idx = build(tree)
+    q, k, _ = _dev(x)
+    mass = torch.zeros((table.numel() // width, width * 16), device="cuda")
+    flide.history_mass(q, k, lse.cuda(), idx, scale, pools[0].cuda(), table.cuda(), slots.cuda(), 16, width, mass,
+                       descale=None if ds is None else ds.cuda())
+    torch.cuda.synchronize()
+    assert idx.status() == 0
+    want = dh.mass_of(tree, _wide(x[0], s[0]), _wide(x[1], s[1]), pk, lse, scale)
+    rel = (d + 4) * 2.0 ** -24 * size + 2.0 ** -20 + 2.0 ** -23 * float(lse.abs().max()) + 2.0 ** -24 * Hq * 64
+    got = mass.cpu().double()
+    for r in range(R):
+        n = want[r].shape[0]
+        err = (got[int(slots[r]), :n] - want[r]).abs()
+        assert bool((err <= rel * want[r] + 2.0 ** -24 * want[r] + 1e-12).all())
+        assert not bool(got[int(slots[r]), n:].any())
+
+
 def test_mass_errors():
     tree = inputs._tree([(200, [(-1, 1)]), (90, [(-1, 60)])], 0)
     x, hist, _ = _inputs(tree, 8, 2, 128, "bf16", 6)

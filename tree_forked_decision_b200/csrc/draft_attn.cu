@@ -746,22 +746,26 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 2) draft_join_kernel(const Dr
 // 32768 rows, 64 rows to a head: 167 us in a 64-row tile, 187 in a 128-row tile, 272
 // in a 256-row tile, 407 in 32-row tiles on mma.sync; 128 rows: 190 in a 128-row
 // tile, 277 in a 256-row tile; 64 requests of 512 rows, 4 rows: 39 us in a 32-row
-// tile, 42 in a 64-row tile.
+// tile, 42 in a 64-row tile.  Groups that do not divide the tile leave rows of it
+// empty: 5 heads to a group, 24 tokens, 8 requests over 32768 rows 199 us, 804 in
+// 32-row tiles on mma.sync.
 enum Kernel { kPortable, kMma, kWide };
 struct Variant {
   Kernel kernel;
   int tile_rows, parts_log;
+  int operand = 0;  // kWide: rows of the operand, whole tokens of which are the tile's
 };
 
 Variant variant_of(long long R, long long T, int G, int d, int dtype) {
   if (dtype == FLIDE_F32 || (d != 64 && d != 128)) return {kPortable, 16, 0};
   const long long rows = (T * G + R - 1) / (R > 0 ? R : 1);
   // (the tiles leave room for 1024 list entries)
-  if (d != 128 || 128 % G || R > 1024) return {kMma, rows <= 16 ? 16 : 32, 0};
-  if (rows <= 32 && G <= 32) return {kWide, 32, 0};
-  if (rows <= 64 && G <= 64) return {kWide, 64, 0};
-  if (rows <= 128 || dtype == FLIDE_E4M3) return {kWide, 128, 1};
-  return {kWide, 256, 0};
+  if (d != 128 || G > 128 || R > 1024) return {kMma, rows <= 16 ? 16 : 32, 0};
+  auto tile_of = [&](int operand) { return operand / G * G; };
+  for (int operand : {32, 64, 128})
+    if (G <= operand && (rows <= tile_of(operand) || (operand == 128 && dtype == FLIDE_E4M3)))
+      return {kWide, tile_of(operand), operand == 128, operand};
+  return {kWide, 2 * tile_of(128), 0, 256};
 }
 
 constexpr int kMaxWorkers = 640;  // of any variant: what the workspace allows for
@@ -900,7 +904,7 @@ int draft_attn(const void *q, const void *k, const void *v, const void *past_k, 
   }
   if (var.kernel == kWide) {
     p.workers = min(kWideWorkers, sms);
-    rc = draft_wide_launch(p, past_rows, dtype == FLIDE_E4M3, dev, s);
+    rc = draft_wide_launch(p, var.operand, past_rows, dtype == FLIDE_E4M3, dev, s);
   } else if (var.tile_rows == 16) {
     rc = dtype == FLIDE_E4M3 ? mma_launch<128, true, 1>(p, dev, sms, s)
          : d == 128          ? mma_launch<128, false, 1>(p, dev, sms, s)

@@ -1,7 +1,7 @@
 // draft_wide.cu -- draft attention's part kernel for wide trees, on tcgen05.
 //
-// A tile of query rows (tokens x heads of the group) is one or two 128-row
-// operands.  Keys come in tiles of 128 by TMA, K and V each through a ring of
+// A tile of query rows (whole tokens x heads of the group, as many as fit) is one or
+// two 128-row operands.  Keys come in tiles of 128 by TMA, K and V each through a ring of
 // stages; S = Q K^T and O += P V accumulate in TMEM, the softmax reads S and
 // writes P there, one row a thread.  Two softmax warpgroups work on two S
 // buffers, so the tensor core always has the other one's products to do:
@@ -133,6 +133,14 @@ draft_part_wide(const __grid_constant__ WideMaps maps, const DraftParams p, int 
     fence_mbar_init();
     ms.abort = 0;
   }
+  // rows of an operand, or of a copy, that hold queries: whole tokens.  The rows behind
+  // them stay 0 (no copy writes them), so their softmax is quiet.
+  const int real = mtok * p.G;
+  if (real != kCopy) {
+    for (int e = tid; e < kHalves * kTile / 16; e += kWThreads)
+      reinterpret_cast<uint4 *>(smem)[e] = make_uint4(0u, 0u, 0u, 0u);
+    fence_proxy_async_smem();
+  }
   if (!draft_list(p, list, ms.part)) return;
   const long long U = list[x.R].unit0;
   const int w = blockIdx.x, W = workers_of(U, p.workers);
@@ -185,7 +193,7 @@ draft_part_wide(const __grid_constant__ WideMaps maps, const DraftParams p, int 
       if (!is_v) {
         if (rc > 0 && !(ok = wait(bQFree, (rc - 1) & 1))) break;
         if (lane == 0) {
-          mbar_arrive_expect_tx(bar(bQ), kHalves * kTile);
+          mbar_arrive_expect_tx(bar(bQ), kHalves * kSlabs * kRep * real * 128);
           for (int h = 0; h < kHalves; ++h)
             for (int s = 0; s < kSlabs; ++s)
               for (int c = 0; c < kRep; ++c)
@@ -428,12 +436,13 @@ draft_part_wide(const __grid_constant__ WideMaps maps, const DraftParams p, int 
       }
       if (!ok || !(ok = wait(bO, rc & 1))) break;
       tc_fence_after();
-      const int limit = run.tokens * p.G - run.tile * p.tile_rows - (kHalves == 2 ? h * kBM : 0);  // real rows
+      // the rows with tokens of the request
+      const int limit = min(real, run.tokens * p.G - run.tile * p.tile_rows - (kHalves == 2 ? h * real : 0));
       if constexpr (kRep == 1) {
         // the partial's rows, 128 bytes of four rows a store: eight lanes exchange
         // their rows' 16-byte words (lane j takes word j of each), because a lane
         // writing its own row touches 32 lines a store (6.4K cycles a run)
-        const size_t at = (size_t)run.slot * 256 + h * 128;
+        const size_t at = (size_t)(2 * run.slot + h) * real;
         const int l8 = lane & 7;
 #pragma unroll 1
         for (int c4 = 0; c4 < 4 && h < steps; ++c4) {
@@ -523,7 +532,7 @@ draft_part_wide(const __grid_constant__ WideMaps maps, const DraftParams p, int 
         tc_fence_before();
         __syncwarp();
         if (lane < 2) mbar_arrive(bar(bOFree + lane));
-        const size_t at = (size_t)run.slot * kCopy;
+        const size_t at = (size_t)run.slot * real;
         for (int e = tid; e < kCopy * 32; e += 256)
           if (e / 32 < limit)
             *reinterpret_cast<float4 *>(p.part_o + (at + e / 32) * 128 + 4 * (e & 31)) =
@@ -591,12 +600,12 @@ int wide_launch(const DraftParams &p, const WideMaps &maps, int mtok, int box_ro
 
 }  // namespace
 
-int draft_wide_launch(DraftParams &p, int past_rows, bool f8, int dev, cudaStream_t s) {
+int draft_wide_launch(DraftParams &p, int operand, int past_rows, bool f8, int dev, cudaStream_t s) {
   p.unit = kBN;
   // key tiles that a run costs beside its own: about 11K cycles of 1.5K (codes),
   // 2.2K and (256 rows) 3.9K a tile
-  p.extra = f8 ? 6 : p.tile_rows == 2 * kBM ? 3 : 5;
-  const int rep = p.tile_rows < kBM ? kBM / p.tile_rows : 1;
+  p.extra = f8 ? 6 : operand == 2 * kBM ? 3 : 5;
+  const int rep = operand < kBM ? kBM / operand : 1;
   const int mtok = kBM / rep / p.G, esz = f8 ? 1 : 2;
   // rows of a box: a tile's, or the most that divides both it and a block
   int box_rows = kBN;
@@ -608,7 +617,7 @@ int draft_wide_launch(DraftParams &p, int past_rows, bool f8, int dev, cudaStrea
       !wide_map(&maps.k, past ? p.past_k : p.k, esz, p.Hkv, past ? past_rows : p.x.T, 1, box_rows) ||
       !wide_map(&maps.v, past ? p.past_v : p.v, esz, p.Hkv, past ? past_rows : p.x.T, 1, box_rows))
     return FLIDE_ERR_CUDA;
-  if (p.tile_rows == 2 * kBM) return wide_launch<2, 1, false>(p, maps, mtok, box_rows, dev, s);
+  if (operand == 2 * kBM) return wide_launch<2, 1, false>(p, maps, mtok, box_rows, dev, s);
   switch (rep) {
     case 4:
       return f8 ? wide_launch<1, 4, true>(p, maps, mtok, box_rows, dev, s)
