@@ -167,7 +167,7 @@ __device__ __forceinline__ bool draft_run(const DraftParams &p, const DraftReq *
 }
 
 // draft_wide.cu (sets p's unit and extra): operands of 32, 64, 128 (bf16, e4m3) or 256 rows (bf16) on tcgen05,
-// of which whole tokens fill p.tile_rows; d == 128
+// of which whole tokens fill p.tile_rows; d of 128, or 64 (bf16, no 32-row operand)
 int draft_wide_launch(DraftParams &p, int operand, int past_rows, bool f8, int dev, cudaStream_t s);
 
 }  // namespace flide

@@ -84,9 +84,9 @@ struct __align__(16) Misc {
 };
 // Where copies' results are joined: their rows (132 floats: eight lanes' words in
 // 32 banks), and a warp's (max, sum) for each of its rows.
-constexpr int merge_bytes(int rep) { return rep > 1 ? kBM / rep * 132 * 4 + 2 * 8 * 32 * 4 : 0; }
-constexpr size_t wide_smem(bool f8, int halves, int rep, int tiles, int R) {
-  return (size_t)(halves + tiles) * (f8 ? 16384 : 32768) + merge_bytes(rep) + kBarBytes + sizeof(Misc) +
+constexpr int merge_bytes(int d, int rep) { return rep > 1 ? kBM / rep * (d + 4) * 4 + 2 * 8 * 32 * 4 : 0; }
+constexpr size_t wide_smem(int tile_bytes, int d, int halves, int rep, int tiles, int R) {
+  return (size_t)(halves + tiles) * tile_bytes + merge_bytes(d, rep) + kBarBytes + sizeof(Misc) +
          (size_t)(R + 1) * sizeof(DraftReq) + 1024;
 }
 
@@ -107,7 +107,7 @@ struct WideMaps {
   CUtensorMap q, k, v;
 };
 
-template <int kHalves, int kRep, bool F8>
+template <int kD, int kHalves, int kRep, bool F8>
 __global__ void __launch_bounds__(kWThreads, 1)
 draft_part_wide(const __grid_constant__ WideMaps maps, const DraftParams p, int mtok, int box_rows,
                 int stages_k, int stages_v) {
@@ -116,9 +116,9 @@ draft_part_wide(const __grid_constant__ WideMaps maps, const DraftParams p, int 
   const uint32_t sb = smem_u32(smem);
   static_assert(kHalves == 1 || kRep == 1, "copies are of a tile of one operand");
   constexpr int kCopy = kBM / kRep, kCols = kBN / kRep;  // rows of a copy, keys of its threads
-  constexpr int kTile = F8 ? 16384 : 32768, kSlabs = F8 ? 1 : 2;  // bytes; 128-byte slabs of a row
+  constexpr int kSlabs = kD * (F8 ? 1 : 2) / 128, kTile = kSlabs * 16384;  // 128-byte slabs of a row; bytes
   const int s_k = kHalves * kTile, s_v = s_k + stages_k * kTile, s_m = s_v + stages_v * kTile;
-  const int s_bar = s_m + merge_bytes(kRep);
+  const int s_bar = s_m + merge_bytes(kD, kRep);
   Misc &ms = *reinterpret_cast<Misc *>(smem + s_bar + kBarBytes);
   volatile int *abort_flag = &ms.abort;
   DraftReq *list = reinterpret_cast<DraftReq *>(&ms + 1);
@@ -224,7 +224,7 @@ draft_part_wide(const __grid_constant__ WideMaps maps, const DraftParams p, int 
     // -------------------------------------------------------------- MMA
     if (lane == 0) {
       constexpr uint32_t id_s = F8 ? idesc_e4m3(kBM, kBN, false) : idesc_bf16(kBM, kBN, false);
-      constexpr uint32_t id_pv = F8 ? idesc_e4m3(kBM, 128, true) : idesc_bf16(kBM, 128, true);
+      constexpr uint32_t id_pv = F8 ? idesc_e4m3(kBM, kD, true) : idesc_bf16(kBM, kD, true);
       auto wait = [&](int b, uint32_t parity) { return mbar_wait(bar(b), parity, abort_flag, kWaitNs); };
       bool ok = true;
       int rc = 0;
@@ -337,7 +337,7 @@ draft_part_wide(const __grid_constant__ WideMaps maps, const DraftParams p, int 
             for (int e = left * 8 + (tid & 127); e < kBN * 8; e += 128) {
               uint4 *z = reinterpret_cast<uint4 *>(smem + s_v + st * kTile) + e;
               z[0] = make_uint4(0u, 0u, 0u, 0u);
-              if (!F8) z[1024] = make_uint4(0u, 0u, 0u, 0u);  // the upper 64 elements
+              if (kSlabs == 2) z[1024] = make_uint4(0u, 0u, 0u, 0u);  // the upper 64 elements
             }
             fence_proxy_async_smem();
           }
@@ -361,7 +361,7 @@ draft_part_wide(const __grid_constant__ WideMaps maps, const DraftParams p, int 
           // this buffer's last PV is complete: it was issued before this S
           const float mn = fmaxf(m, mt), f = mn == -INFINITY ? 1.f : exp2f(m - mn);
 #pragma unroll 1
-          for (int c4 = 0; c4 < 4; ++c4) {
+          for (int c4 = 0; c4 < kD / 32; ++c4) {
             uint32_t r32[32];
             tmem_ld32(t_o + 32 * c4, r32);
 #pragma unroll
@@ -445,7 +445,7 @@ draft_part_wide(const __grid_constant__ WideMaps maps, const DraftParams p, int 
         const size_t at = (size_t)(2 * run.slot + h) * real;
         const int l8 = lane & 7;
 #pragma unroll 1
-        for (int c4 = 0; c4 < 4 && h < steps; ++c4) {
+        for (int c4 = 0; c4 < kD / 32 && h < steps; ++c4) {
           uint32_t r32[32];
           tmem_ld32(t_o + 32 * c4, r32);
 #pragma unroll
@@ -466,7 +466,7 @@ draft_part_wide(const __grid_constant__ WideMaps maps, const DraftParams p, int 
           for (int a = 0; a < 8; ++a) {
             const int r = row - l8 + a;
             if (r % kCopy < limit)
-              *reinterpret_cast<uint4 *>(p.part_o + (at + r) * 128 + 32 * c4 + 4 * l8) =
+              *reinterpret_cast<uint4 *>(p.part_o + (at + r) * kD + 32 * c4 + 4 * l8) =
                   make_uint4(r32[4 * a], r32[4 * a + 1], r32[4 * a + 2], r32[4 * a + 3]);
           }
         }
@@ -479,9 +479,10 @@ draft_part_wide(const __grid_constant__ WideMaps maps, const DraftParams p, int 
         // TMEM lanes), in one half of the columns; the kRep warps that share a row
         // there then add a chunk of columns each to the buffer in shared memory and
         // move on to the next, so every sum has one order.
-        constexpr int kChunk = 64 / kRep;
+        constexpr int kChunk = kD / 2 / kRep, kLine = kD + 4;
+        static_assert(kChunk == 16 || kChunk == 32, "columns of a TMEM load");
         const int mine = row / kCopy, r = row % kCopy, wid = warp;
-        float *buf = reinterpret_cast<float *>(smem + s_m), *st_m = buf + kCopy * 132, *st_l = st_m + 256;
+        float *buf = reinterpret_cast<float *>(smem + s_m), *st_m = buf + kCopy * kLine, *st_l = st_m + 256;
         if (h >= steps) m = -INFINITY;
         st_m[wid * 32 + lane] = m - kShift;
         st_l[wid * 32 + lane] = l;
@@ -505,7 +506,7 @@ draft_part_wide(const __grid_constant__ WideMaps maps, const DraftParams p, int 
         }
 #pragma unroll 1
         for (int k = 0; k < kRep && ok; ++k) {
-          const int c0 = 64 * h + (mine + k) % kRep * kChunk;
+          const int c0 = kD / 2 * h + (mine + k) % kRep * kChunk;
           uint32_t v[2][kChunk];
           if constexpr (kChunk == 16) {
             tmem_ld16(tl + 128 + c0, v[0]);
@@ -514,7 +515,7 @@ draft_part_wide(const __grid_constant__ WideMaps maps, const DraftParams p, int 
             tmem_ld32(tl + 128 + c0, v[0]);
             tmem_ld32(tl + 384 + c0, v[1]);
           }
-          float4 *to = reinterpret_cast<float4 *>(buf + r * 132 + c0);
+          float4 *to = reinterpret_cast<float4 *>(buf + r * kLine + c0);
 #pragma unroll
           for (int j = 0; j < kChunk / 4; ++j) {
             float o[4];
@@ -533,10 +534,11 @@ draft_part_wide(const __grid_constant__ WideMaps maps, const DraftParams p, int 
         __syncwarp();
         if (lane < 2) mbar_arrive(bar(bOFree + lane));
         const size_t at = (size_t)run.slot * real;
-        for (int e = tid; e < kCopy * 32; e += 256)
-          if (e / 32 < limit)
-            *reinterpret_cast<float4 *>(p.part_o + (at + e / 32) * 128 + 4 * (e & 31)) =
-                *reinterpret_cast<const float4 *>(buf + e / 32 * 132 + 4 * (e & 31));
+        constexpr int kQuads = kD / 4;
+        for (int e = tid; e < kCopy * kQuads; e += 256)
+          if (e / kQuads < limit)
+            *reinterpret_cast<float4 *>(p.part_o + (at + e / kQuads) * kD + 4 * (e % kQuads)) =
+                *reinterpret_cast<const float4 *>(buf + e / kQuads * kLine + 4 * (e % kQuads));
         if (h == 0 && mine == 0 && r < limit) *reinterpret_cast<float2 *>(p.part_ml + 2 * (at + r)) = make_float2(top, all);
       }
       kt0 += tiles;
@@ -571,13 +573,13 @@ EncodeFn encode_tiled() {
   return fn;
 }
 
-// [rows, heads, 128] bf16 or codes as (element, head, row); box of 128 swizzled
+// [rows, heads, d] bf16 or codes as (element, head, row); box of 128 swizzled
 // bytes x box_heads x box_rows
-bool wide_map(CUtensorMap *m, const void *base, int esz, int heads, long rows, int box_heads, int box_rows) {
+bool wide_map(CUtensorMap *m, const void *base, int d, int esz, int heads, long rows, int box_heads, int box_rows) {
   EncodeFn enc = encode_tiled();
   if (!enc || rows <= 0) return false;
-  const cuuint64_t dims[3] = {128, (cuuint64_t)heads, (cuuint64_t)rows};
-  const cuuint64_t strides[2] = {(cuuint64_t)128 * esz, (cuuint64_t)heads * 128 * esz};
+  const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)rows};
+  const cuuint64_t strides[2] = {(cuuint64_t)d * esz, (cuuint64_t)heads * d * esz};
   const cuuint32_t box[3] = {(cuuint32_t)(128 / esz), (cuuint32_t)box_heads, (cuuint32_t)box_rows};
   const cuuint32_t step[3] = {1, 1, 1};
   return enc(m, esz == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
@@ -586,14 +588,15 @@ bool wide_map(CUtensorMap *m, const void *base, int esz, int heads, long rows, i
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int kHalves, int kRep, bool F8>
+template <int kD, int kHalves, int kRep, bool F8>
 int wide_launch(const DraftParams &p, const WideMaps &maps, int mtok, int box_rows, int dev, cudaStream_t s) {
+  constexpr int kTileBytes = kBN * kD * (F8 ? 1 : 2);
   int k = kMaxStages, v = kMaxStages;  // as many as fit, K's first
-  while (k > 1 && wide_smem(F8, kHalves, kRep, k + v, p.x.R) > kSmemMax) (k > v ? k : v)--;
+  while (k > 1 && wide_smem(kTileBytes, kD, kHalves, kRep, k + v, p.x.R) > kSmemMax) (k > v ? k : v)--;
   if (k < 2 || v < 2) return FLIDE_ERR_CAPACITY;
-  const size_t smem = wide_smem(F8, kHalves, kRep, k + v, p.x.R);
-  if (!allow_smem<draft_part_wide<kHalves, kRep, F8>>(dev)) return FLIDE_ERR_CUDA;
-  draft_part_wide<kHalves, kRep, F8><<<p.workers, kWThreads, smem, s>>>(maps, p, mtok, box_rows, k, v);
+  const size_t smem = wide_smem(kTileBytes, kD, kHalves, kRep, k + v, p.x.R);
+  if (!allow_smem<draft_part_wide<kD, kHalves, kRep, F8>>(dev)) return FLIDE_ERR_CUDA;
+  draft_part_wide<kD, kHalves, kRep, F8><<<p.workers, kWThreads, smem, s>>>(maps, p, mtok, box_rows, k, v);
   FLIDE_LAUNCH_CHECK();
   return FLIDE_OK;
 }
@@ -606,28 +609,33 @@ int draft_wide_launch(DraftParams &p, int operand, int past_rows, bool f8, int d
   // 2.2K and (256 rows) 3.9K a tile
   p.extra = f8 ? 6 : operand == 2 * kBM ? 3 : 5;
   const int rep = operand < kBM ? kBM / operand : 1;
-  const int mtok = kBM / rep / p.G, esz = f8 ? 1 : 2;
+  const int mtok = kBM / rep / p.G, esz = f8 ? 1 : 2, d = p.d;
   // rows of a box: a tile's, or the most that divides both it and a block
   int box_rows = kBN;
   if (p.hist.block_table)
     while (p.hist.block_rows % box_rows) box_rows /= 2;
   WideMaps maps;
   const bool past = p.past_k != nullptr && past_rows > 0;  // without: no unit, no load
-  if (!wide_map(&maps.q, p.q, esz, p.Hq, p.x.T, p.G, mtok) ||
-      !wide_map(&maps.k, past ? p.past_k : p.k, esz, p.Hkv, past ? past_rows : p.x.T, 1, box_rows) ||
-      !wide_map(&maps.v, past ? p.past_v : p.v, esz, p.Hkv, past ? past_rows : p.x.T, 1, box_rows))
+  if (!wide_map(&maps.q, p.q, d, esz, p.Hq, p.x.T, p.G, mtok) ||
+      !wide_map(&maps.k, past ? p.past_k : p.k, d, esz, p.Hkv, past ? past_rows : p.x.T, 1, box_rows) ||
+      !wide_map(&maps.v, past ? p.past_v : p.v, d, esz, p.Hkv, past ? past_rows : p.x.T, 1, box_rows))
     return FLIDE_ERR_CUDA;
-  if (operand == 2 * kBM) return wide_launch<2, 1, false>(p, maps, mtok, box_rows, dev, s);
+  if (d == 64) {
+    if (operand == 2 * kBM) return wide_launch<64, 2, 1, false>(p, maps, mtok, box_rows, dev, s);
+    return rep == 2 ? wide_launch<64, 1, 2, false>(p, maps, mtok, box_rows, dev, s)
+                    : wide_launch<64, 1, 1, false>(p, maps, mtok, box_rows, dev, s);
+  }
+  if (operand == 2 * kBM) return wide_launch<128, 2, 1, false>(p, maps, mtok, box_rows, dev, s);
   switch (rep) {
     case 4:
-      return f8 ? wide_launch<1, 4, true>(p, maps, mtok, box_rows, dev, s)
-                : wide_launch<1, 4, false>(p, maps, mtok, box_rows, dev, s);
+      return f8 ? wide_launch<128, 1, 4, true>(p, maps, mtok, box_rows, dev, s)
+                : wide_launch<128, 1, 4, false>(p, maps, mtok, box_rows, dev, s);
     case 2:
-      return f8 ? wide_launch<1, 2, true>(p, maps, mtok, box_rows, dev, s)
-                : wide_launch<1, 2, false>(p, maps, mtok, box_rows, dev, s);
+      return f8 ? wide_launch<128, 1, 2, true>(p, maps, mtok, box_rows, dev, s)
+                : wide_launch<128, 1, 2, false>(p, maps, mtok, box_rows, dev, s);
     default:
-      return f8 ? wide_launch<1, 1, true>(p, maps, mtok, box_rows, dev, s)
-                : wide_launch<1, 1, false>(p, maps, mtok, box_rows, dev, s);
+      return f8 ? wide_launch<128, 1, 1, true>(p, maps, mtok, box_rows, dev, s)
+                : wide_launch<128, 1, 1, false>(p, maps, mtok, box_rows, dev, s);
   }
 }
 
