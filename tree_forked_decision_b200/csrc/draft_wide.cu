@@ -36,7 +36,10 @@
 // 4.2 TB/s.  e4m3, 32 rows: 0.93 us a tile (bytes 0.75), bound by its twelve
 // products (1.75K cycles); a run's end 3 us; 16 histories of 1024 to 16391 rows, 8
 // tokens each, 78 us a call, 3.9 TB/s.  Histories that one tile reads leave L2
-// before other lines (16 x 8192 rows: 75 -> 68 us).  Every wait is bounded (2 s);
+// before other lines (16 x 8192 rows: 75 -> 68 us; blocks that many requests share
+// through their tables pay for it: 64 requests over the same 16384 rows 476 -> 499).
+// Loading the next run's Q in a warp of its own, or as soon as the last scores are
+// out, changed nothing.  Every wait is bounded (2 s);
 // on expiry the block records FLIDE_ERR_TIMEOUT, waits for its own copies and
 // MMAs, frees TMEM and ends.
 #include <cstddef>
