@@ -1,0 +1,52 @@
+"""Draft attention at the edges of its contract: every tile size at the most requests that a tile
+takes, scales of zero, values that are not finite, one key that outweighs all others."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from tree_forked_decision_b200 import flide, inputs
+
+import decode_helpers as dh
+from gpu_helpers import build
+from test_gpu_draft_attn import _cat, _check, _dev, _inputs, _wide
+
+pytestmark = pytest.mark.gpu
+
+KINDS = [("bf16", 128), ("bf16", 64), ("e4m3", 128), ("f32", 64)]
+# tokens of a request: with 4 heads to a group 4, 40, 100 and 200 query rows, a tile of each size
+TOKENS = [1, 10, 25, 50]
+
+
+def _draft(tree, x, hist, ds, scale):
+    _, idx = build(tree)
+    q, k, v = _dev(x)
+    pk, pv = (_cat(h).cuda() for h in hist)
+    out, lse = flide.draft_attn(q, k, v, idx, scale, past_k=pk, past_v=pv, descale=None if ds is None else ds.cuda())
+    torch.cuda.synchronize()
+    assert idx.status() == 0
+    return out, lse
+
+
+@pytest.mark.parametrize("kind,d", KINDS)
+@pytest.mark.parametrize("tokens", TOKENS)
+@pytest.mark.parametrize("R", [967, 968, 1024])
+def test_every_tile_with_many_requests(R, tokens, kind, d):
+    """A call takes up to 2048 requests, whatever tile its rows ask for; every 41st request is checked."""
+    rng = np.random.default_rng(R)
+    past = rng.integers(0, 40, R).tolist()
+    tree = inputs._tree([(n, [(-1, tokens)]) for n in past], 0)
+    x, hist, ds = _inputs(tree, 4, 1, d, kind, 4)
+    pools, table, slots, width = dh.scatter(hist, 16, rng)
+    _, idx = build(tree)
+    q, k, v = _dev(x)
+    scale = 1 / math.sqrt(d)
+    out, lse = flide.draft_attn_paged(q, k, v, idx, scale, pools[0].cuda(), pools[1].cuda(), table.cuda(), slots.cuda(),
+                                      16, width, descale=None if ds is None else ds.cuda())
+    torch.cuda.synchronize()
+    assert idx.status() == 0
+    some = list(range(0, R, 41)) + [R - 1]
+    rows = torch.cat([torch.arange(r * tokens, (r + 1) * tokens) for r in some])
+    _check(inputs._tree([(past[r], [(-1, tokens)]) for r in some], 0), [y[rows] for y in x],
+           [[h[r] for r in some] for h in hist], ds, scale, out.cpu()[rows], lse.cpu()[rows], kind)

@@ -168,6 +168,8 @@ __device__ __forceinline__ bool draft_run(const DraftParams &p, const DraftReq *
 
 // draft_wide.cu (sets p's unit and extra): operands of 32, 64, 128 (bf16, e4m3) or 256 rows (bf16) on tcgen05,
 // of which whole tokens fill p.tile_rows; d of 128, or 64 (bf16, no 32-row operand)
+// whether a call of R requests leaves such a tile its shared memory
+bool draft_wide_fits(int operand, int d, bool f8, long long R);
 int draft_wide_launch(DraftParams &p, int operand, int past_rows, bool f8, int dev, cudaStream_t s);
 
 }  // namespace flide

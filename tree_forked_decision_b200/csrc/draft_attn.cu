@@ -751,7 +751,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 2) draft_join_kernel(const Dr
 // 32-row tiles on mma.sync.  Heads of 64: half the bytes of a key row, so up to 32
 // rows the loads in registers win (8 requests over 32768 rows: 16 rows 105 us, 134 in
 // a 64-row tile; 32 rows 117 and 134), beyond them the tile (64 rows 214 and 134, 256
-// rows 820 and 251).
+// rows 820 and 251).  The tiles leave room for 1024 list entries, but for the 64-row
+// one of 128-wide bf16 heads, whose merge buffer takes 34 KB of it: from 968 requests
+// on the 128-row tile takes its rows.
 enum Kernel { kPortable, kMma, kWide };
 struct Variant {
   Kernel kernel;
@@ -762,11 +764,11 @@ struct Variant {
 Variant variant_of(long long R, long long T, int G, int d, int dtype) {
   if (dtype == FLIDE_F32 || (d != 64 && d != 128)) return {kPortable, 16, 0};
   const long long rows = (T * G + R - 1) / (R > 0 ? R : 1);
-  // (the tiles leave room for 1024 list entries)
   if (G > 128 || R > 1024 || (d == 64 && rows <= 32)) return {kMma, rows <= 16 ? 16 : 32, 0};
   auto tile_of = [&](int operand) { return operand / G * G; };
   for (int operand : {32, 64, 128})
-    if (G <= operand && (operand > 32 || d == 128) && (rows <= tile_of(operand) || (operand == 128 && dtype == FLIDE_E4M3)))
+    if (G <= operand && (operand > 32 || d == 128) && (rows <= tile_of(operand) || (operand == 128 && dtype == FLIDE_E4M3)) &&
+        draft_wide_fits(operand, d, dtype == FLIDE_E4M3, R))
       return {kWide, tile_of(operand), operand == 128, operand};
   return {kWide, 2 * tile_of(128), 0, 256};
 }

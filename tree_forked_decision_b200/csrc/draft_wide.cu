@@ -63,6 +63,7 @@ constexpr uint64_t kWaitNs = 2000000000ull;
 // codes), then the barriers and the block's work list (32 bytes a request).  As many
 // stages as fit.
 constexpr int kMaxStages = 4;
+constexpr int kMinStages = 4;  // of K and V together: two each
 constexpr int kSmemMax = 232448;
 enum {
   bQ = 0,
@@ -88,7 +89,7 @@ struct __align__(16) Misc {
 // Where copies' results are joined: their rows (132 floats: eight lanes' words in
 // 32 banks), and a warp's (max, sum) for each of its rows.
 constexpr int merge_bytes(int d, int rep) { return rep > 1 ? kBM / rep * (d + 4) * 4 + 2 * 8 * 32 * 4 : 0; }
-constexpr size_t wide_smem(int tile_bytes, int d, int halves, int rep, int tiles, int R) {
+constexpr size_t wide_smem(int tile_bytes, int d, int halves, int rep, int tiles, long long R) {
   return (size_t)(halves + tiles) * tile_bytes + merge_bytes(d, rep) + kBarBytes + sizeof(Misc) +
          (size_t)(R + 1) * sizeof(DraftReq) + 1024;
 }
@@ -595,8 +596,7 @@ template <int kD, int kHalves, int kRep, bool F8>
 int wide_launch(const DraftParams &p, const WideMaps &maps, int mtok, int box_rows, int dev, cudaStream_t s) {
   constexpr int kTileBytes = kBN * kD * (F8 ? 1 : 2);
   int k = kMaxStages, v = kMaxStages;  // as many as fit, K's first
-  while (k > 1 && wide_smem(kTileBytes, kD, kHalves, kRep, k + v, p.x.R) > kSmemMax) (k > v ? k : v)--;
-  if (k < 2 || v < 2) return FLIDE_ERR_CAPACITY;
+  while (k + v > kMinStages && wide_smem(kTileBytes, kD, kHalves, kRep, k + v, p.x.R) > kSmemMax) (k > v ? k : v)--;
   const size_t smem = wide_smem(kTileBytes, kD, kHalves, kRep, k + v, p.x.R);
   if (!allow_smem<draft_part_wide<kD, kHalves, kRep, F8>>(dev)) return FLIDE_ERR_CUDA;
   draft_part_wide<kD, kHalves, kRep, F8><<<p.workers, kWThreads, smem, s>>>(maps, p, mtok, box_rows, k, v);
@@ -605,6 +605,11 @@ int wide_launch(const DraftParams &p, const WideMaps &maps, int mtok, int box_ro
 }
 
 }  // namespace
+
+bool draft_wide_fits(int operand, int d, bool f8, long long R) {
+  return wide_smem(kBN * d * (f8 ? 1 : 2), d, operand == 2 * kBM ? 2 : 1, operand < kBM ? kBM / operand : 1, kMinStages,
+                   R) <= kSmemMax;
+}
 
 int draft_wide_launch(DraftParams &p, int operand, int past_rows, bool f8, int dev, cudaStream_t s) {
   p.unit = kBN;
