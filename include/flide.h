@@ -566,7 +566,8 @@ size_t flide_draft_attn_workspace_bytes(int32_t R, int32_t T, int32_t Hq, int32_
  *          idx->T, Hq, Hkv, d) bytes; one call at a time
  * Rows past the stream's last token are left as they were.  A key that a row
  * does not see takes no part in its result, whatever its value.  q, k, v, the
- * past and out 16-byte aligned; scale finite and >= 0 (FLIDE_ERR_INVALID).
+ * past and out 16-byte aligned; scale finite and >= 0 (FLIDE_ERR_INVALID), descale's
+ * factors not negative; with a scale of 0 every key weighs the same.
  * The softmax weights are rounded to bf16 before they multiply v (not for
  * FLIDE_F32; e4m3: to half, or to the sum of two e4m3 values: relative error
  * <= 2^-8, absolute <= 2^-16 of the row's largest weight); their sum is not.

@@ -50,3 +50,24 @@ def test_every_tile_with_many_requests(R, tokens, kind, d):
     rows = torch.cat([torch.arange(r * tokens, (r + 1) * tokens) for r in some])
     _check(inputs._tree([(past[r], [(-1, tokens)]) for r in some], 0), [y[rows] for y in x],
            [[h[r] for r in some] for h in hist], ds, scale, out.cpu()[rows], lse.cpu()[rows], kind)
+
+
+@pytest.mark.parametrize("kind,d", KINDS)
+@pytest.mark.parametrize("tokens", TOKENS)
+@pytest.mark.parametrize("scale", [0.0, 1e-45])
+def test_scale_of_zero(scale, tokens, kind, d):
+    """All scores are (nearly) equal: the mean of the values, whatever stands behind the history's end."""
+    tree = inputs._tree([(n, [(-1, tokens)]) for n in (0, 1, 31, 33, 127, 128, 129, 300, 1025)], 0)
+    x, hist, ds = _inputs(tree, 4, 1, d, kind, 5)
+    out, lse = _draft(tree, x, hist, ds, scale)
+    _check(tree, x, hist, ds, scale, out, lse, kind)
+
+
+@pytest.mark.parametrize("tokens", TOKENS)
+def test_factors_whose_product_vanishes(tokens):
+    """descale[0] descale[1] below the least 32-bit number: as a scale of zero."""
+    tree = inputs._tree([(n, [(-1, tokens)]) for n in (0, 1, 33, 129, 300)], 0)
+    x, hist, _ = _inputs(tree, 4, 1, 128, "e4m3", 5)
+    ds = torch.tensor([1e-30, 1e-30, 0.01])
+    out, lse = _draft(tree, x, hist, ds, 0.1)
+    _check(tree, x, hist, ds, 0.1, out, lse, "e4m3")

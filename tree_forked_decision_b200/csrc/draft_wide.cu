@@ -301,7 +301,10 @@ draft_part_wide(const __grid_constant__ WideMaps maps, const DraftParams p, int 
     const int col0 = (warp & 3) * 32 / kCopy * kCols;       // the first key of this warp's copy
     const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t t_s = tl + h * 256, t_o = tl + h * 256 + 128;
-    const float c = p.scale * kLog2eD * (F8 ? p.descale[0] * p.descale[1] : 1.f);
+    // keys behind the history are -inf before they are scaled, and -inf times 0 would be
+    // NaN: a factor of 0 becomes 2^-140, which moves a score below 2^100 by less than 2^-40
+    const float factor = p.scale * kLog2eD * (F8 ? p.descale[0] * p.descale[1] : 1.f);
+    const float c = factor == 0.f ? 0x1p-140f : factor;
     auto wait = [&](int b, uint32_t parity) {
       return __all_sync(0xffffffffu, mbar_wait(bar(b), parity, abort_flag, kWaitNs));
     };
