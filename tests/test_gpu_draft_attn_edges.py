@@ -71,3 +71,35 @@ def test_factors_whose_product_vanishes(tokens):
     ds = torch.tensor([1e-30, 1e-30, 0.01])
     out, lse = _draft(tree, x, hist, ds, 0.1)
     _check(tree, x, hist, ds, 0.1, out, lse, "e4m3")
+
+
+@pytest.mark.parametrize("kind,d", [("bf16", 128), ("bf16", 64), ("f32", 64)])
+@pytest.mark.parametrize("tokens", TOKENS)
+def test_infinite_values_that_a_row_sees(tokens, kind, d):
+    """An infinity among the values that a row sees, every weight above 0: infinite there, NaN where both
+    signs meet or a NaN stands, and no other element is touched."""
+    past = [1, 40, 129, 1000, 3001]
+    tree = inputs._tree([(n, [(-1, tokens)]) for n in past], 0)
+    x, hist, _ = _inputs(tree, 8, 2, d, kind, 6)
+    for r, n in enumerate(past):
+        v = hist[1][r]
+        at = lambda share: min(n - 1, int(share * n))  # noqa: E731
+        v[at(0.3), 0, 1] = math.inf
+        v[at(0.99), 0, 2] = -math.inf
+        v[at(0.6), 0, d - 1] = v[0, 0, d - 1] = math.inf   # twice, in different places
+        if n > 1:
+            v[at(0.2), 0, 5], v[n - 1, 0, 5] = math.inf, -math.inf
+        if r % 2:
+            v[at(0.5), 0, 7] = math.nan
+    scale = 1 / math.sqrt(d)
+    out, lse = _draft(tree, x, hist, None, scale)
+    o, want, wv, peak, size = dh.attention(tree, *[y.double() for y in x], [h.double() for h in hist[0]],
+                                           [h.double() for h in hist[1]], scale)
+    got = out.double().cpu()
+    assert torch.equal(got.isnan(), o.isnan())
+    inf = o.isinf()
+    assert bool(inf.any()) and torch.equal(got.isinf(), inf) and torch.equal(got[inf], o[inf])
+    fine = o.isfinite()
+    tol = dh.attention_tolerance(o, wv, peak, size, d, max(past) + tokens, out.dtype, 0.0 if kind == "f32" else 2.0 ** -8)
+    assert bool(((got - o).abs()[fine] <= tol[fine]).all())
+    assert bool(((lse.double().cpu() - want).abs() <= dh.lse_tolerance(want, size, d, max(past) + tokens)).all())

@@ -542,10 +542,45 @@ draft_part_wide(const __grid_constant__ WideMaps maps, const DraftParams p, int 
         if (lane < 2) mbar_arrive(bar(bOFree + lane));
         const size_t at = (size_t)run.slot * real;
         constexpr int kQuads = kD / 4;
+        bool nan = false;
         for (int e = tid; e < kCopy * kQuads; e += 256)
-          if (e / kQuads < limit)
-            *reinterpret_cast<float4 *>(p.part_o + (at + e / kQuads) * kD + 4 * (e % kQuads)) =
-                *reinterpret_cast<const float4 *>(buf + e / kQuads * kLine + 4 * (e % kQuads));
+          if (e / kQuads < limit) {
+            const float4 o = *reinterpret_cast<const float4 *>(buf + e / kQuads * kLine + 4 * (e % kQuads));
+            *reinterpret_cast<float4 *>(p.part_o + (at + e / kQuads) * kD + 4 * (e % kQuads)) = o;
+            nan |= isnan(o.x) | isnan(o.y) | isnan(o.z) | isnan(o.w);
+          }
+        if (!F8 && __any_sync(0xffffffffu, nan)) {  // (codes have no infinity)
+          // An infinite value times the weight 0 that other copies have for its key is NaN.
+          // Where a column of the run's values holds infinities of one sign and no NaN,
+          // that infinity is its sum.
+          uint32_t seen = 0;  // the thread's columns: +inf bits 0 to 3, -inf 4 to 7, NaN 8 to 11
+          const __nv_bfloat16 *col = static_cast<const __nv_bfloat16 *>(p.past_v) + run.hk * kD + 4 * (tid % kQuads);
+#pragma unroll 1
+          for (int key = run.k0; key < run.k1; key += 16) {  // (rows of a block come in sixteens)
+            const long long from = history_row(x, p.hist, run.base, key);
+            if (from < 0) continue;
+            uint2 w[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              w[j] = key + j < run.k1 ? *reinterpret_cast<const uint2 *>(col + (size_t)(from + j) * p.Hkv * kD)
+                                      : make_uint2(0u, 0u);
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const uint32_t v = (i < 2 ? w[j].x : w[j].y) >> 16 * (i & 1) & 0xffffu;
+                if ((v & 0x7fffu) >= 0x7f80u) seen |= (v == 0x7f80u ? 1u : v == 0xff80u ? 16u : 256u) << i;
+              }
+          }
+          for (int e = tid; e < kCopy * kQuads; e += 256)
+            if (e / kQuads < limit)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const uint32_t kind = seen >> i & 0x111u;
+                if ((kind == 1u || kind == 16u) && isnan(buf[e / kQuads * kLine + 4 * (e % kQuads) + i]))
+                  p.part_o[(at + e / kQuads) * kD + 4 * (e % kQuads) + i] = kind == 1u ? INFINITY : -INFINITY;
+              }
+        }
         if (h == 0 && mine == 0 && r < limit) *reinterpret_cast<float2 *>(p.part_ml + 2 * (at + r)) = make_float2(top, all);
       }
       kt0 += tiles;
