@@ -524,18 +524,14 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
               if ((uint32_t)(i - lo) >= w) sr[i] = 0xff800000u;  // -inf
           }
         }
-        // row max: 8 chains of three-input max
-        float mx[8];
+        // row max: 3 chains of three-input max (2, 4, 8 or 16 chains: within 1%)
+        float mx[3];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) mx[k] = __uint_as_float(sr[k]);
+        for (int k = 0; k < 3; ++k) mx[k] = fmaxf(__uint_as_float(sr[2 * k]), __uint_as_float(sr[2 * k + 1]));
 #pragma unroll
-        for (int i = 8; i < BN; i += 16) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            mx[k] = fmax3f(mx[k], __uint_as_float(sr[i + 2 * k]), __uint_as_float(sr[i + 2 * k + 1]));
-        }
-        const float smax = fmaxf(fmax3f(mx[0], mx[1], mx[2]),
-                                 fmax3f(fmax3f(mx[3], mx[4], mx[5]), mx[6], mx[7]));
+        for (int i = 6; i < BN; i += 2)
+          mx[i / 2 % 3] = fmax3f(mx[i / 2 % 3], __uint_as_float(sr[i]), __uint_as_float(sr[i + 1]));
+        const float smax = fmax3f(mx[0], mx[1], mx[2]);
         const float mt = smax * c;
         if (j == 0) {
           m_used = mt;
