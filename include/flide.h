@@ -569,8 +569,9 @@ size_t flide_draft_attn_workspace_bytes(int32_t R, int32_t T, int32_t Hq, int32_
  * past and out 16-byte aligned; scale finite and >= 0 (FLIDE_ERR_INVALID), descale's
  * factors not negative; with a scale of 0 every key weighs the same.
  * The softmax weights are rounded to bf16 before they multiply v (not for
- * FLIDE_F32; e4m3: to half, or to the sum of two e4m3 values: relative error
- * <= 2^-8, absolute <= 2^-16 of the row's largest weight); their sum is not.
+ * FLIDE_F32; e4m3: to half, or to the sum of an e4m3 and an e5m2 value: off by at
+ * most 2^-8 of the weight, or 2^-20 of the row's largest one and then at most an
+ * eighth of the weight, or 2^-23 of the largest); their sum is not.
  * Host errors: FLIDE_ERR_SHAPE, FLIDE_ERR_CAPACITY (workspace too small, more
  * than 2048 requests, T * Hq past 2^30), FLIDE_ERR_CUDA; device errors as
  * flide_fork_attn, and FLIDE_ERR_CAPACITY for a past of more than 2^30 rows. */

@@ -103,3 +103,53 @@ def test_infinite_values_that_a_row_sees(tokens, kind, d):
     tol = dh.attention_tolerance(o, wv, peak, size, d, max(past) + tokens, out.dtype, 0.0 if kind == "f32" else 2.0 ** -8)
     assert bool(((got - o).abs()[fine] <= tol[fine]).all())
     assert bool(((lse.double().cpu() - want).abs() <= dh.lse_tolerance(want, size, d, max(past) + tokens)).all())
+
+
+@pytest.mark.parametrize("spread", [0.0, 0.6])
+@pytest.mark.parametrize("tokens", TOKENS)
+def test_one_key_outweighs_each_other(tokens, spread):
+    """e4m3: one key of weight 2^17 times each of 16384 others, which hold a ninth of the sum together (a
+    first token that draws the attention).  A weight w of a row whose largest is L is off by at most
+    max(2^-8 w, 2^-20 L), and by 2^-3 w from 2^-20 L on (two codes, e4m3 and e5m2, of w 2^6 / L)."""
+    R, n, Hkv, d = 20, 16384, 8, 128
+    g = torch.Generator().manual_seed(tokens)
+    tree = inputs._tree([(n, [(-1, tokens)])] * R, 0)
+    T = tree.T
+    ds = torch.tensor([0.01, 0.01, 0.01])
+    code = lambda y: (y / 0.01).clamp(-448, 448).to(torch.float8_e4m3fn)  # noqa: E731
+    one = torch.ones(d)
+    q = code(one.expand(T, 4 * Hkv, d) * (1 + 0.05 * torch.rand(T, 4 * Hkv, 1, generator=g)))
+    hk = spread * torch.randn(n, Hkv, d, generator=g)
+    hk[0] = 1.0
+    hv = 1 + 0.25 * torch.rand(n, Hkv, d, generator=g)
+    hv[0] = 0.0
+    hk, hv = code(hk), code(hv)
+    scale = 17 * math.log(2) / d
+    k = code(-one.expand(T, Hkv, d))  # the stream's own keys: hardly any weight
+    v = code(torch.ones(T, Hkv, d))
+    bl, width = 128, n // 128
+    table = torch.arange(width, dtype=torch.int32).repeat(R)  # every request reads the same blocks
+    _, idx = build(tree)
+    b = lambda y: y.contiguous().view(torch.uint8).cuda()  # noqa: E731
+    out, lse = flide.draft_attn_paged(b(q), b(k), b(v), idx, scale, b(hk), b(hv), table.cuda(),
+                                      torch.arange(R, dtype=torch.int32, device="cuda"), bl, width, descale=ds.cuda())
+    torch.cuda.synchronize()
+    assert idx.status() == 0
+    f = lambda y: y.double().cuda() * float(ds[0])  # noqa: E731
+    rows = torch.arange(0, T, max(1, T // 40))  # some tokens of all requests
+    for h in range(0, 4 * Hkv, 5):
+        kk, vv = f(hk[:, h // 4]), f(hv[:, h // 4])
+        s = f(q[rows, h]) @ kk.T * scale
+        w = torch.exp(s - s.amax(1, keepdim=True))
+        own = torch.exp(-scale * d - s.amax(1)) * tokens * 1.2   # the stream's keys, at most
+        total = w.sum(1, keepdim=True)
+        o = (w / total) @ vv
+        err = torch.where(w >= 2.0 ** -20, torch.minimum(w * 2.0 ** -3, torch.clamp(w * 2.0 ** -8, min=2.0 ** -20)), w)
+        # 32-bit sums of as many terms; sizes of a score's products as in decode_helpers
+        ds32 = (d + 4) * 2.0 ** -24 * float((f(q[rows, h]).abs() @ kk.abs().T * scale).max())
+        rel = 2 * ds32 + 2.0 ** -20 + 2 * (n + tokens + 8) * 2.0 ** -24
+        tol = 2.0 ** -8 * o + (err / total) @ vv + rel * o + 3 * (own / total[:, 0])[:, None] + 1e-9
+        diff = (out[rows.cuda(), h].double() - o).abs()
+        assert bool((diff <= tol).all()), float((diff / tol).max())
+        if spread:  # weights that differ are rounded either way: the sum of 16384 is far closer
+            assert float((diff / o).max()) < 2.0 ** -6

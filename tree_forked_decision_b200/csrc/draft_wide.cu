@@ -22,10 +22,16 @@
 //
 // e4m3: S and O come from the codes (kind::f8f6f4, exact products).  A weight in
 // e4m3 would be 2^-4 off, so it goes in as two codes, its own and its remainder's:
-// two products at twice the rate.  Scaled by 2^6, a weight is off by 2^-8 of
-// itself or 2^-16 of the row's largest; a row's reference is raised once a score
-// passes it by 2.75 (2^8.75 < 448, the format's largest; raised at 2, some warp of
-// a tile had to rescale O in most of a history's first tiles: 82 us instead of 78).  (Widening V to half in the softmax warps instead: 13 us more of 110.)
+// two products at twice the rate.  The remainder is in e5m2: half a step of either
+// type is 2^-8 of the weight (3 + 1 + 3 bits and a sign), but e5m2 reaches from 2^-16
+// up, where e4m3's least step, 2^-9, would lose every key below 2^-16 of a row's
+// dominant one, however many there are (16384 keys of 2^-17 of a first one, a ninth of
+// the sum together: results up to half short).  Scaled by 2^6, a weight is off by 2^-8
+// of itself or 2^-20 of the row's largest, and below 2^-16 of it by an eighth of itself.
+// A row's reference is raised once a score passes it by 2.75 (2^8.75 < 448, the
+// format's largest; raised at 2, some warp of a tile had to rescale O in most of a
+// history's first tiles: 82 us instead of 78).  (Widening V to half in the softmax
+// warps instead: 13 us more of 110.)
 //
 // 256 rows are bound by the two warpgroups' softmax and the MMA issue (see
 // attn_tc.cu): 2.35 us a key tile where its bytes would take 1.5; 8 requests of 64
@@ -229,6 +235,7 @@ draft_part_wide(const __grid_constant__ WideMaps maps, const DraftParams p, int 
     if (lane == 0) {
       constexpr uint32_t id_s = F8 ? idesc_e4m3(kBM, kBN, false) : idesc_bf16(kBM, kBN, false);
       constexpr uint32_t id_pv = F8 ? idesc_e4m3(kBM, kD, true) : idesc_bf16(kBM, kD, true);
+      constexpr uint32_t id_rem = idesc_e5m2_e4m3(kBM, kD, true);
       auto wait = [&](int b, uint32_t parity) { return mbar_wait(bar(b), parity, abort_flag, kWaitNs); };
       bool ok = true;
       int rc = 0;
@@ -270,7 +277,7 @@ draft_part_wide(const __grid_constant__ WideMaps maps, const DraftParams p, int 
             // bf16: 16 keys each; codes: 32 keys each, the weights and then their remainders
             const uint32_t acc = (i >= 2 || kk > 0) ? 1u : 0u;
             const uint64_t b = sdesc_sw128(v_at + (F8 ? (kk & 3) * 4096 : kk * 2048), 16384, 1024);
-            if (F8) mma_f8_ts(tmem + h * 256 + 128, tmem + h * 256 + kk * 8, b, id_pv, acc);
+            if (F8) mma_f8_ts(tmem + h * 256 + 128, tmem + h * 256 + kk * 8, b, kk < 4 ? id_pv : id_rem, acc);
             else mma_bf16_ts(tmem + h * 256 + 128, tmem + h * 256 + kk * 8, b, id_pv, acc);
           }
           if (kHalves == 1 || h == 1) {
@@ -404,7 +411,7 @@ draft_part_wide(const __grid_constant__ WideMaps maps, const DraftParams p, int 
               e[k + 1] -= f.y;
             }
             // words of codes take the places of scores that were read: j / 4 < j
-            const uint32_t rest = pack_e4m3x4(e[0], e[1], e[2], e[3]);
+            const uint32_t rest = pack_e5m2x4(e[0], e[1], e[2], e[3]);
             sr[j / 4] = code;
             rem[j / 4] = rest;
           }

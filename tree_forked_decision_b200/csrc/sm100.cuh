@@ -318,6 +318,18 @@ __device__ __forceinline__ uint32_t pack_e4m3x4(float a0, float a1, float a2, fl
   return r;
 }
 
+// The same to e5m2 codes (saturating to +-57344).
+__device__ __forceinline__ uint32_t pack_e5m2x4(float a0, float a1, float a2, float a3) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo, hi;\n\t"
+      "cvt.rn.satfinite.e5m2x2.f32 lo, %2, %1;\n\t"
+      "cvt.rn.satfinite.e5m2x2.f32 hi, %4, %3;\n\t"
+      "mov.b32 %0, {lo, hi};\n}"
+      : "=r"(r)
+      : "f"(a0), "f"(a1), "f"(a2), "f"(a3));
+  return r;
+}
+
 // ---- MMA -----------------------------------------------------------------
 // D[tmem] (+)= A[smem] * B[smem]^T, kind::f16 (bf16 inputs, fp32 accumulate),
 // issued by one thread.
@@ -384,6 +396,10 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool b_mn_major)
 __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool b_mn_major) {
   return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) |
          ((uint32_t)(M >> 4) << 24);
+}
+// The same with A in e5m2 (a type for each operand is kind::f8f6f4's own).
+__host__ __device__ constexpr uint32_t idesc_e5m2_e4m3(int M, int N, bool b_mn_major) {
+  return idesc_e4m3(M, N, b_mn_major) | (1u << 7);
 }
 
 // Instruction descriptor for kind::f16 with every option: fp32 accumulator,
