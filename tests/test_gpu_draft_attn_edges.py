@@ -105,6 +105,22 @@ def test_infinite_values_that_a_row_sees(tokens, kind, d):
     assert bool(((lse.double().cpu() - want).abs() <= dh.lse_tolerance(want, size, d, max(past) + tokens)).all())
 
 
+@pytest.mark.parametrize("kind,d", [("bf16", 128), ("bf16", 64), ("f32", 64)])
+@pytest.mark.parametrize("tokens", TOKENS)
+def test_keys_that_are_all_nan(tokens, kind, d):
+    """A history whose every key is NaN leaves no number in its rows, and the other requests alone."""
+    tree = inputs._tree([(n, [(-1, tokens)]) for n in (50, 500, 60)], 0)
+    x, hist, _ = _inputs(tree, 4, 1, d, kind, 7)
+    scale = 1 / math.sqrt(d)
+    was = _draft(tree, x, hist, None, scale)
+    hist[0][1][:] = math.nan
+    out, lse = _draft(tree, x, hist, None, scale)
+    mid = slice(tokens, 2 * tokens)
+    assert bool(out[mid].isnan().all()) and bool(lse[mid].isnan().all())
+    for rows in (slice(0, tokens), slice(2 * tokens, 3 * tokens)):
+        assert torch.equal(out[rows], was[0][rows]) and torch.equal(lse[rows], was[1][rows])
+
+
 @pytest.mark.parametrize("spread", [0.0, 0.6])
 @pytest.mark.parametrize("tokens", TOKENS)
 def test_one_key_outweighs_each_other(tokens, spread):

@@ -694,7 +694,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 2) draft_join_kernel(const Dr
 #pragma unroll
       for (int e = 0; e < kE / 4; ++e) v0[e] = v[e];
       if (i + kKeys < parts) partial(i + kKeys, ml, v);
-      if (ml0.x == -INFINITY) continue;  // an empty partial
+      if (ml0.x == -INFINITY && ml0.y == 0.f) continue;  // an empty partial (of NaN scores: not 0)
       const float mn = fmaxf(m, ml0.x);
       const float f = ex2_approx(m - mn), g = ex2_approx(ml0.x - mn);
       l = l * f + ml0.y * g;
