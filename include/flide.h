@@ -643,7 +643,8 @@ int flide_verify_draft(const flide_tree_index *idx, const int32_t *tokens, const
  * Each slot at most once per call (two requests would race for its sums).
  * Device errors: FLIDE_ERR_INVALID for a bad slot or block,
  * FLIDE_ERR_CAPACITY where P + n passes max_blocks * block_rows or P 2^30 (that
- * request is skipped).  Host errors as flide_draft_attn_paged. */
+ * request is skipped).  A request without root tokens is skipped too: none of its
+ * entries is written, in mass_out neither.  Host errors as flide_draft_attn_paged. */
 int flide_history_mass(const void *q, const void *k, const float *lse, const void *pool_k,
                        int32_t n_blocks, int32_t block_rows, const int32_t *block_table,
                        int32_t max_blocks, const int32_t *req_slot, int32_t n_slots,

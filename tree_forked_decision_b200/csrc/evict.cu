@@ -14,6 +14,8 @@
 // `sinks`, the last `recent`, and the rows of largest mass between them (of
 // equal ones the lowest index).  The kept rows stay in order and move to the
 // front of the destination's blocks, in place if they are the source's.
+#include <cmath>
+
 #include "common.cuh"
 #include "launch.cuh"
 #include "sm100.cuh"
@@ -749,7 +751,10 @@ int flide_history_mass(const void *q, const void *k, const float *lse, const voi
   if (dtype == FLIDE_E4M3 && (!descale || d != 128)) return FLIDE_ERR_SHAPE;
   if (idx->R < 0 || idx->T < 0) return FLIDE_ERR_SHAPE;
   if (((uintptr_t)q | (uintptr_t)k | (uintptr_t)pool_k) % 16) return FLIDE_ERR_SHAPE;
-  if (idx->R > kMaxListR) return FLIDE_ERR_CAPACITY;
+  // (in place, a weight of NaN would stay)
+  if (!(scale >= 0.f) || std::isinf(scale)) return FLIDE_ERR_INVALID;
+  if (idx->R > kMaxListR || (long long)idx->T * Hq > 0x3fffffffLL || (long long)n_blocks * block_rows > 0x7fffffffLL)
+    return FLIDE_ERR_CAPACITY;
   if (idx->R == 0 || idx->T == 0) return FLIDE_OK;
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
