@@ -70,6 +70,7 @@ class HistoryStore:
         self.status = torch.zeros(1, dtype=torch.int32, device=device)
         self.mass = None  # attention weight per history row, from accumulate_mass on
         self.evicted_h = np.zeros(max_requests, np.int32)  # rows evicted per slot
+        self._weighed = {}  # slot -> its rows' weights before a step that is not committed yet
 
     def __del__(self):
         pool = getattr(self, "_pool", None)
@@ -87,6 +88,7 @@ class HistoryStore:
     def release(self, slot: int):
         flide._check(self._lib.flide_pool_release(self._pool, slot), "flide_pool_release")
         self.evicted_h[slot] = 0
+        self._weighed.pop(slot, None)
         if self.mass is not None:
             self.mass[slot].zero_()
         self._sync_table()
@@ -164,14 +166,19 @@ class HistoryStore:
 
     def accumulate_mass(self, q, k, lse, index: flide.TreeIndex, scale: float, slots):
         """Adds the attention weight that this step's root tokens gave each history row,
-        and starts that of the root's own rows: after draft_attn, before commit."""
+        and starts that of the root's own rows: after draft_attn, before commit.  A commit
+        that is refused takes it back (a step's retry weighs its rows again)."""
         slots = self._once(slots)
         if self.mass is None:
             self.mass = torch.zeros((self.max_requests, self.max_blocks * self.block_rows),
                                     dtype=torch.float32, device=self.device)
         req = torch.tensor(slots, dtype=torch.int32, device=self.device)
+        live = [s for s in slots if s >= 0]
+        rows = max((self.length(s) for s in live), default=0)
+        before = dict(zip(live, self.mass[:, :rows][live]))
         flide.history_mass(q, k, lse, index, scale, self.pool_k, self.table, req, self.block_rows,
                            self.max_blocks, self.mass)
+        self._weighed.update(before)
 
     def evict(self, slots, budget: int, sinks: int = 0, recent: int = 0):
         """Cuts the histories of `slots` that are longer than `budget` rows down to their
@@ -185,6 +192,7 @@ class HistoryStore:
                                    self.pool_k, self.pool_v, self.mass, int(budget), self.status,
                                    sinks=int(sinks), recent=int(recent))
         for s in slots:
+            self._weighed.pop(s, None)  # its rows have moved
             if s >= 0 and self.length(s) > budget:
                 self.evicted_h[s] += self.length(s) - budget
                 self.mass[s, budget:].zero_()  # rows to come start without weight
@@ -204,7 +212,8 @@ class HistoryStore:
 
     def reserve(self, slots, tree):
         """Host half of commit: reserves each request's root rows in its slot
-        (all requests or none: on FlideError no slot changes), refreshes the
+        (all requests or none: on FlideError no slot changes, and the weights that
+        accumulate_mass gave them for this step are taken back), refreshes the
         device block table and lengths, and returns the start rows (-1 where
         slots[r] is -1).  Each slot at most once per step (ValueError)."""
         slots = [int(s) for s in slots]
@@ -218,8 +227,14 @@ class HistoryStore:
         sl = np.array(slots, np.int32)
         start = np.zeros(len(slots), np.int32)
         p = lambda a: a.ctypes.data_as(ctypes.c_void_p)
-        flide._check(self._lib.flide_pool_append_batch(self._pool, len(slots), p(sl), p(counts),
-                                                       p(start)), "flide_pool_append_batch")
+        code = self._lib.flide_pool_append_batch(self._pool, len(slots), p(sl), p(counts), p(start))
+        for s in kept:
+            before = self._weighed.pop(s, None)
+            if code != flide.OK and before is not None:
+                n = self.length(s)
+                self.mass[s, :n] = before[:n]
+                self.mass[s, n:].zero_()
+        flide._check(code, "flide_pool_append_batch")
         self._sync_table()
         return start
 
