@@ -80,3 +80,18 @@ def test_released_and_evicted_slots_are_not_brought_back():
     with pytest.raises(flide.FlideError):
         store.commit([0, 2], inputs._tree([(0, [(-1, 90)]), (0, [(-1, 1)])], 0), idx, k, v)
     assert torch.equal(store.mass, after) and not bool(store.mass[2].any())
+
+
+@pytest.mark.parametrize("bad", [3, 100])
+def test_slots_that_are_none_of_the_store(bad):
+    store, slots = _store()
+    before = (store.mass.clone(), store.pool_k.clone(), store.lengths.clone())
+    with pytest.raises(flide.FlideError) as e:
+        store.evict([0, bad], 8)
+    assert e.value.code == flide.ERR_INVALID
+    with pytest.raises(flide.FlideError) as e:
+        store.accumulate_mass(None, None, None, None, 0.1, [bad, 0])
+    assert e.value.code == flide.ERR_INVALID
+    torch.cuda.synchronize()
+    assert torch.equal(store.mass, before[0]) and torch.equal(store.pool_k, before[1])
+    assert torch.equal(store.lengths, before[2]) and int(store.status) == 0

@@ -168,7 +168,7 @@ class HistoryStore:
         """Adds the attention weight that this step's root tokens gave each history row,
         and starts that of the root's own rows: after draft_attn, before commit.  A commit
         that is refused takes it back (a step's retry weighs its rows again)."""
-        slots = self._once(slots)
+        slots = self._once(slots, "accumulate_mass")
         if self.mass is None:
             self.mass = torch.zeros((self.max_requests, self.max_blocks * self.block_rows),
                                     dtype=torch.float32, device=self.device)
@@ -184,13 +184,14 @@ class HistoryStore:
         """Cuts the histories of `slots` that are longer than `budget` rows down to their
         first `sinks`, last `recent` and heaviest rows, in place, and frees the blocks
         past them.  Returns the rows kept, int32 [len(slots), budget], -1 past the end."""
-        slots = self._once(slots)
+        slots = self._once(slots, "evict")
         if self.mass is None:
             raise ValueError("evict needs the rows' attention weight (accumulate_mass)")
         req = torch.tensor(slots, dtype=torch.int32, device=self.device)
         kept = flide.history_evict(req, self.lengths, self.table, self.block_rows, self.max_blocks,
                                    self.pool_k, self.pool_v, self.mass, int(budget), self.status,
                                    sinks=int(sinks), recent=int(recent))
+        # (slots, lengths and blocks are the pool's own: nothing is left for the device to refuse)
         for s in slots:
             self._weighed.pop(s, None)  # its rows have moved
             if s >= 0 and self.length(s) > budget:
@@ -201,13 +202,14 @@ class HistoryStore:
         self._sync_table()
         return kept
 
-    @staticmethod
-    def _once(slots):
-        """The slots as ints, each at most once (-1: none)."""
+    def _once(self, slots, where):
+        """The slots as ints, each one of the store's and at most once (-1: none)."""
         slots = [int(s) for s in slots]
         live = [s for s in slots if s >= 0]
         if len(set(live)) != len(live):
             raise ValueError("a slot may stand for one request of a call")
+        if any(s >= self.max_requests for s in live):
+            raise flide.FlideError(flide.ERR_INVALID, where)
         return slots
 
     def reserve(self, slots, tree):
