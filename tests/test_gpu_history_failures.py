@@ -73,12 +73,13 @@ def test_only_the_refused_slots_are_taken_back():
 
 def test_released_and_evicted_slots_are_not_brought_back():
     store, slots = _store()
-    _, idx, k, v = _step(store, slots, [10, 30], 7)
+    _, idx, k, _ = _step(store, slots, [10, 30], 7)
     store.release(2)
     store.evict([0], 8, sinks=1, recent=2)
     after = store.mass.clone()
+    rows = k.new_zeros(91, Hkv, d)
     with pytest.raises(flide.FlideError):
-        store.commit([0, 2], inputs._tree([(0, [(-1, 90)]), (0, [(-1, 1)])], 0), idx, k, v)
+        store.commit([0, 2], inputs._tree([(0, [(-1, 90)]), (0, [(-1, 1)])], 0), idx, rows, rows)
     assert torch.equal(store.mass, after) and not bool(store.mass[2].any())
 
 

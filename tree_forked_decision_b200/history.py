@@ -244,6 +244,13 @@ class HistoryStore:
         """Appends request r's root tokens (this step's observation) and its
         root's end GDN state to slot slots[r] (-1: nothing kept)."""
         slots = [int(s) for s in slots]
+        # (rows of another type would be written past the pool's end)
+        flide._rows_like("commit", self.pool_k, k=k, v=v)
+        tokens = int(tree.arrays()[2].sum())
+        if min(k.shape[0], v.shape[0]) < tokens:
+            raise ValueError(f"commit: k and v need {tokens} rows, got {k.shape[0]} and {v.shape[0]}")
+        if self.H:
+            flide._states_like("commit", self.H, self.dv, self.dk, node_state=node_state)
         start = self.reserve(slots, tree)
         req = torch.tensor(slots, dtype=torch.int32, device=self.device)
         st_d = torch.from_numpy(start).to(self.device)
