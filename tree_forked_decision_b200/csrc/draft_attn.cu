@@ -18,7 +18,6 @@
 //     a sibling branch cannot reach a row, NaN and infinity included.
 // History rows need no mask but their number, and rows past it are not read.
 #include <cuda_fp16.h>
-#include <cuda_fp8.h>
 #include <math.h>
 
 #include <algorithm>
@@ -35,16 +34,7 @@ using namespace sm100;
 
 constexpr float kLn2D = 0.6931471805599453f;
 
-template <typename T>
-__device__ __forceinline__ float value_of(const T *p) { return load_f(p); }
-template <>
-__device__ __forceinline__ float value_of<uint8_t>(const uint8_t *p) {
-  __nv_fp8_e4m3 c;
-  c.__x = *p;
-  return (float)c;
-}
-
-// Any element type and head size: CUDA cores, 32 keys a step.
+// float32, and bf16 head sizes of no tensor-core kernel: CUDA cores, 32 keys a step.
 constexpr int kPT = 128;   // threads
 constexpr int kPRows = 16; // rows of a tile
 constexpr int kPKeys = 32; // keys of a unit
@@ -67,7 +57,7 @@ __global__ void __launch_bounds__(kPT) draft_part_portable(const DraftParams p) 
   const long long u_end = worker_start(U, W, w + 1);
   const T *Q = static_cast<const T *>(p.q), *K = static_cast<const T *>(p.past_k),
           *Vp = static_cast<const T *>(p.past_v);
-  const float qk_scale = p.scale * kLog2eD * (p.descale ? p.descale[0] * p.descale[1] : 1.f);
+  const float qk_scale = p.scale * kLog2eD;
   const int nd = d / 32;
   Run run;
   while (draft_run(p, list, u, u_end, w, run)) {
@@ -75,7 +65,7 @@ __global__ void __launch_bounds__(kPT) draft_part_portable(const DraftParams p) 
     for (int e = tid; e < kPRows * d; e += kPT) {
       const int row = e / d, i = e - row * d, g = run.tile * kPRows + row;
       sq[row * ld + i] = g < run.tokens * p.G
-          ? value_of(Q + ((size_t)(run.t0 + g / p.G) * p.Hq + run.hk * p.G + g % p.G) * d + i) : 0.f;
+          ? load_f(Q + ((size_t)(run.t0 + g / p.G) * p.Hq + run.hk * p.G + g % p.G) * d + i) : 0.f;
     }
     float m[4], l[4], acc[4][8];
 #pragma unroll
@@ -92,8 +82,8 @@ __global__ void __launch_bounds__(kPT) draft_part_portable(const DraftParams p) 
         const long long row = kr < left ? history_row(x, p.hist, run.base, k0 + kr) : -1;
         for (int i = lane; i < d; i += 32) {
           const size_t at = ((size_t)max(row, 0ll) * p.Hkv + run.hk) * d + i;
-          sk[kr * ld + i] = row >= 0 ? value_of(K + at) : 0.f;
-          sv[kr * ld + i] = row >= 0 ? value_of(Vp + at) : 0.f;
+          sk[kr * ld + i] = row >= 0 ? load_f(K + at) : 0.f;
+          sv[kr * ld + i] = row >= 0 ? load_f(Vp + at) : 0.f;
         }
       }
       __syncthreads();
@@ -458,10 +448,10 @@ draft_part_mma(const DraftParams p) {
   }
 }
 
-// Any element type and head size: one warp per (token, query head): the tokens on
-// its path, then the partial results of its history, then the output row and its
-// log-sum-exp.
-template <typename T, typename TOut>
+// float32, and bf16 head sizes of no tensor-core kernel: one warp per (token, query
+// head): the tokens on its path, then the partial results of its history, then the
+// output row and its log-sum-exp.
+template <typename T>
 __global__ void __launch_bounds__(256) draft_join_portable(const DraftParams p) {
   const flide_tree_index &x = p.x;
   if (failed(x.status)) return;
@@ -472,12 +462,11 @@ __global__ void __launch_bounds__(256) draft_join_portable(const DraftParams p) 
   const int hk = h / p.G, d = p.d, nd = d / 32;
   const int n = (int)checked(x.status, x.counts, x.token_node[t], x.counts[FLIDE_CNT_N], 801);
   const T *Q = static_cast<const T *>(p.q), *K = static_cast<const T *>(p.k), *Vs = static_cast<const T *>(p.v);
-  const float sv = p.descale ? p.descale[2] : 1.f;
-  const float qk_scale = p.scale * kLog2eD * (p.descale ? p.descale[0] * p.descale[1] : 1.f);
+  const float qk_scale = p.scale * kLog2eD;
   float qv[8], acc[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    qv[i] = i < nd ? value_of(Q + ((size_t)t * p.Hq + h) * d + lane + 32 * i) * qk_scale : 0.f;
+    qv[i] = i < nd ? load_f(Q + ((size_t)t * p.Hq + h) * d + lane + 32 * i) * qk_scale : 0.f;
     acc[i] = 0.f;
   }
   float m = -INFINITY, l = 0.f;
@@ -489,7 +478,7 @@ __global__ void __launch_bounds__(256) draft_join_portable(const DraftParams p) 
       float s = 0.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (i < nd) s = fmaf(qv[i], value_of(K + at + 32 * i), s);
+        if (i < nd) s = fmaf(qv[i], load_f(K + at + 32 * i), s);
       s = warp_sum(s);
       const float mn = fmaxf(m, s), ref = mn == -INFINITY ? 0.f : mn;
       const float f = exp2f(m - ref), w = exp2f(s - ref);
@@ -497,7 +486,7 @@ __global__ void __launch_bounds__(256) draft_join_portable(const DraftParams p) 
       m = mn;
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (i < nd) acc[i] = fmaf(w, value_of(Vs + at + 32 * i), acc[i] * f);
+        if (i < nd) acc[i] = fmaf(w, load_f(Vs + at + 32 * i), acc[i] * f);
     }
   }
   const DraftReq q = p.list[x.node_req[n]];
@@ -520,8 +509,8 @@ __global__ void __launch_bounds__(256) draft_join_portable(const DraftParams p) 
         if (i < nd) acc[i] = fmaf(g, p.part_o[pr * d + lane + 32 * i], acc[i] * f);
     }
   }
-  const float inv = sv / l;
-  TOut *O = static_cast<TOut *>(p.out) + ((size_t)t * p.Hq + h) * d + lane;
+  const float inv = 1.f / l;
+  T *O = static_cast<T *>(p.out) + ((size_t)t * p.Hq + h) * d + lane;
 #pragma unroll
   for (int i = 0; i < 8; ++i)
     if (i < nd) store_f(O + 32 * i, acc[i] * inv);
@@ -822,10 +811,10 @@ int mma_launch(DraftParams &p, int dev, int sms, cudaStream_t s) {
   return part_launch<draft_part_mma<D, F8, kMT>>(p, dev, S::kMW * 32, S::kSmem + (size_t)(p.x.R + 1) * sizeof(DraftReq), s);
 }
 
-template <typename T, typename TOut>
+template <typename T>
 int join_portable_launch(const DraftParams &p, cudaStream_t s) {
   const long long warps = (long long)p.x.T * p.Hq;
-  draft_join_portable<T, TOut><<<(unsigned)((warps + 7) / 8), 256, 0, s>>>(p);
+  draft_join_portable<T><<<(unsigned)((warps + 7) / 8), 256, 0, s>>>(p);
   FLIDE_LAUNCH_CHECK();
   return FLIDE_OK;
 }
@@ -904,8 +893,7 @@ int draft_attn(const void *q, const void *k, const void *v, const void *past_k, 
   if (var.kernel == kPortable) {
     rc = dtype == FLIDE_F32 ? portable_launch<float>(p, dev, sms, s) : portable_launch<__nv_bfloat16>(p, dev, sms, s);
     if (rc != FLIDE_OK) return rc;
-    return dtype == FLIDE_F32 ? join_portable_launch<float, float>(p, s)
-                              : join_portable_launch<__nv_bfloat16, __nv_bfloat16>(p, s);
+    return dtype == FLIDE_F32 ? join_portable_launch<float>(p, s) : join_portable_launch<__nv_bfloat16>(p, s);
   }
   if (var.kernel == kWide) {
     p.workers = min(kWideWorkers, sms);
