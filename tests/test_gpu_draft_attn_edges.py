@@ -169,3 +169,14 @@ def test_one_key_outweighs_each_other(tokens, spread):
         assert bool((diff <= tol).all()), float((diff / tol).max())
         if spread:  # weights that differ are rounded either way: the sum of 16384 is far closer
             assert float((diff / o).max()) < 2.0 ** -6
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(4, 4), (8, 2), (16, 4)])
+@pytest.mark.parametrize("kind", ["bf16", "e4m3", "f32"])
+def test_long_paths(kind, Hq, Hkv):
+    """Paths of more than 64 keys and more than 32 ancestors, with one, two and four heads to a warp of the join."""
+    tree = inputs._tree([(n, [(-1, 150)] + [(i, 1 + i % 2) for i in range(45)]) for n in (0, 200)], 45)
+    x, hist, ds = _inputs(tree, Hq, Hkv, 128, kind, 8)
+    scale = 1 / math.sqrt(128)
+    out, lse = _draft(tree, x, hist, ds, scale)
+    _check(tree, x, hist, ds, scale, out, lse, kind)
