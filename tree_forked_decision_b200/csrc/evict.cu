@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(kMThreads) mass_kernel_portable(const MassPara
 // tokens stays in one lane quad's registers: S^T = K Q^T with the 16 rows as the
 // m16 operand and 8 query rows (tokens x heads of the group) as the n8 one, kept
 // in shared memory as the raw 16-byte words that the lanes' k order asks for (see
-// draft_attn.cu).  exp(score - lse) of a padding row is exp(-inf) = 0.
+// draft_attn.cu).
 //
 // Bound by K's bytes, and so by what is on its way: each lane copies the very
 // words it will need to its own places in shared memory (8 KB a warp), a head or
@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(kMassWarps * 32, 1) mass_kernel_mma(const Mass
           to[32] = make_uint4(e4m3x2_to_half2(v.z), e4m3x2_to_half2(v.z >> 16), e4m3x2_to_half2(v.w),
                               e4m3x2_to_half2(v.w >> 16));
         }
-        if (j == 0 && (l & 3) == 0) *lse_to = row ? *lse_to * kLog2eM : INFINITY;
+        if (j == 0 && (l & 3) == 0) *lse_to *= kLog2eM;  // (a padding row's is not used)
       });
       __syncthreads();
       // place of row i of a group's 16 in the weights, -1: no such row
@@ -379,8 +379,9 @@ __global__ void __launch_bounds__(kMassWarps * 32, 1) mass_kernel_mma(const Mass
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 float e = ex2_approx(fmaf(s[k][i], qk_scale, -(i & 1 ? l2.y : l2.x)));
-                // a root row is seen by its own token and later ones
-                if (fresh && (r0 + (i & 1)) / p.G < i0 + g + 8 * (i >> 1)) e = 0.f;
+                // a root row is seen by its own token and later ones; a padding row's score
+                // is 0, or NaN with an infinite key
+                if (r0 + (i & 1) >= rows || (fresh && (r0 + (i & 1)) / p.G < i0 + g + 8 * (i >> 1))) e = 0.f;
                 acc[i >> 1] += e;
               }
             }
