@@ -516,7 +516,10 @@ int flide_history_gather(int32_t R, const int32_t *req_slot, int32_t max_request
  *   FLIDE_ROPE_YARN    by parts (Peng et al., "YaRN"): a pair that makes at
  *                      least `fast` turns over orig_len positions is kept, one
  *                      of at most `slow` turns divided by factor, linearly in
- *                      between; *mscale = 0.1 ln(factor) + 1
+ *                      its number of turns in between, as the paper states it;
+ *                      *mscale = 0.1 ln(factor) + 1.  (Checkpoints whose code
+ *                      has the ramp linear in the pair's index, between two
+ *                      rounded indices, need that table: flide_rope takes any.)
  * *mscale (host) is 1 otherwise.  2 <= rot_dim <= 1024, even, else
  * FLIDE_ERR_SHAPE (also for an unknown scaling or a NULL argument); base <= 0,
  * factor < 1, for YARN orig_len <= 0, slow < 0 or fast <= slow, or a value that
@@ -563,7 +566,9 @@ size_t flide_draft_attn_workspace_bytes(int32_t R, int32_t T, int32_t Hq, int32_
  *   lse    float [T, Hq], may be NULL: natural logarithm of the sum of
  *          exp(scale * score) over the token's keys
  *   workspace  device, 256-byte aligned, flide_draft_attn_workspace_bytes(idx->R,
- *          idx->T, Hq, Hkv, d) bytes; one call at a time
+ *          idx->T, Hq, Hkv, d) bytes; one call at a time.  32-bit partial rows, a
+ *          tile of them for every worker and item: megabytes for a few requests,
+ *          2.2 GB for 1024 requests of 64 tokens with 32 + 8 heads of 128
  * Rows past the stream's last token are left as they were.  A key that a row
  * does not see takes no part in its result, whatever its value.  q, k, v, the
  * past and out 16-byte aligned; scale finite and >= 0 (FLIDE_ERR_INVALID), descale's

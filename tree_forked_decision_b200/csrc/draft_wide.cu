@@ -35,13 +35,16 @@
 //
 // 256 rows are bound by the two warpgroups' softmax and the MMA issue (see
 // attn_tc.cu): 2.35 us a key tile where its bytes would take 1.5; 8 requests of 64
-// tokens over 32768 rows, 32 + 8 heads, 290 us a call, 950 TFLOP/s.  128 rows and
-// fewer by the history's bytes and the ends of runs: a tile takes 1.25 us (bytes
+// tokens over 32768 rows, 32 + 8 heads, 296 us a call, 930 TFLOP/s, while the clock
+// holds; back to back the power limit makes it 353 (1.49 GHz, 780 TFLOP/s).  128 rows
+// and fewer by the history's bytes and the ends of runs: a tile takes 1.25 us (bytes
 // 1.5, part of them from L2), a block's first scores come after 8 us, a run's
 // end takes 4 to 5; 16 histories of 512 to 8192 rows, 20 tokens each, 61 us a call,
-// 4.2 TB/s.  e4m3, 32 rows: 0.93 us a tile (bytes 0.75), bound by its twelve
-// products (1.75K cycles); a run's end 3 us; 16 histories of 1024 to 16391 rows, 8
-// tokens each, 78 us a call, 3.9 TB/s.  Histories that one tile reads leave L2
+// 4.2 TB/s (back to back 67 to 71).  e4m3, 32 rows: 0.93 us a tile (bytes 0.75), bound
+// by its twelve products (1.75K cycles); a run's end 3 us; 16 histories of 1024 to
+// 16391 rows, 8 tokens each, 79 us a call, 3.9 TB/s (back to back 92 to 97).  The tiles
+// of 128 and 256 rows spill 170 to 200 bytes a thread at the 168 registers that 352
+// threads leave.  Histories that one tile reads leave L2
 // before other lines (16 x 8192 rows: 75 -> 68 us; blocks that many requests share
 // through their tables pay for it: 64 requests over the same 16384 rows 476 -> 499).
 // Loading the next run's Q in a warp of its own, or as soon as the last scores are

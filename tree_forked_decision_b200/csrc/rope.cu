@@ -83,7 +83,8 @@ struct Unit<T, false> {
 // copied word; else one pair or one copied element.  A thread keeps its unit and
 // goes over the block's (token, head) rows, some of them loaded ahead (as raw
 // words: unpacking at the load waits for each in turn, 199 us).  8 requests of
-// 4096 + 64 x 16 tokens, 32 + 8 heads of 128, bf16: 137 us, 6.1 TB/s.
+// 4096 + 64 x 16 tokens, 32 + 8 heads of 128, bf16: 138 us replayed from a graph, 6.1
+// TB/s; 144 called back to back.
 template <typename T, bool kVec, bool kInter>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p, int tok) {
   extern __shared__ __align__(16) float cs[];  // cos [tok][half], sin [tok][half]

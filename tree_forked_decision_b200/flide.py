@@ -679,7 +679,8 @@ def _shaped(where, shape, **named):
 def rope_freqs(rot_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
                orig_len: float = 0.0, fast: float = 32.0, slow: float = 1.0, device="cuda"):
     """Rotation frequencies (float64 tensor [rot_dim / 2], radians a position) and
-    the factor mscale for `rope`; scaling "none", "linear", "ntk" or "yarn"."""
+    the factor mscale for `rope`; scaling "none", "linear", "ntk" or "yarn" (its ramp
+    linear in a pair's turns, as the paper has it)."""
     if scaling not in ROPE_SCALING:
         raise ValueError(f"rope_freqs: scaling is one of {sorted(ROPE_SCALING)}, got {scaling!r}")
     freqs = np.empty(max(int(rot_dim) // 2, 1), np.float64)

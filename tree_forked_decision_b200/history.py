@@ -35,6 +35,11 @@ it), with the history bounded to `budget` rows:
     store.accumulate_mass(q, k, lse, index, scale, slots)     # before commit
     store.commit(slots, tree, index, k, v, node_state)
     store.evict(slots, budget, sinks=4, recent=64)
+
+The store's calls take the slots from the host and copy them to the device each time;
+a step that is captured into a CUDA graph calls ``flide.draft_attn_paged`` and
+``flide.history_mass`` with the store's ``pool_k``, ``pool_v``, ``table`` and ``mass`` (there
+from the first ``accumulate_mass`` on), and slots and a workspace of its own.
 """
 from __future__ import annotations
 
