@@ -217,6 +217,13 @@ class HistoryStore:
             raise flide.FlideError(flide.ERR_INVALID, where)
         return slots
 
+    def _take_back(self, weighed):
+        """Puts back rows' weights from before a step (slot -> weights)."""
+        for s, before in weighed.items():
+            n = self.length(s)
+            self.mass[s, :n] = before[:n]
+            self.mass[s, n:].zero_()
+
     def reserve(self, slots, tree):
         """Host half of commit: reserves each request's root rows in its slot
         (all requests or none: on FlideError no slot changes, and the weights that
@@ -234,34 +241,45 @@ class HistoryStore:
         sl = np.array(slots, np.int32)
         start = np.zeros(len(slots), np.int32)
         p = lambda a: a.ctypes.data_as(ctypes.c_void_p)
+        weighed = {s: self._weighed.pop(s) for s in kept if s in self._weighed}
         code = self._lib.flide_pool_append_batch(self._pool, len(slots), p(sl), p(counts), p(start))
-        for s in kept:
-            before = self._weighed.pop(s, None)
-            if code != flide.OK and before is not None:
-                n = self.length(s)
-                self.mass[s, :n] = before[:n]
-                self.mass[s, n:].zero_()
+        if code != flide.OK:
+            self._take_back(weighed)
         flide._check(code, "flide_pool_append_batch")
         self._sync_table()
         return start
 
     def commit(self, slots, tree, index: flide.TreeIndex, k, v, node_state=None):
         """Appends request r's root tokens (this step's observation) and its
-        root's end GDN state to slot slots[r] (-1: nothing kept)."""
+        root's end GDN state to slot slots[r] (-1: nothing kept).  Where it raises, the
+        store is as it was before the step."""
         slots = [int(s) for s in slots]
-        # (rows of another type would be written past the pool's end)
-        flide._rows_like("commit", self.pool_k, k=k, v=v)
-        tokens = int(tree.arrays()[2].sum())
-        if min(k.shape[0], v.shape[0]) < tokens:
-            raise ValueError(f"commit: k and v need {tokens} rows, got {k.shape[0]} and {v.shape[0]}")
-        if self.H:
-            flide._states_like("commit", self.H, self.dv, self.dk, node_state=node_state)
-        start = self.reserve(slots, tree)
-        req = torch.tensor(slots, dtype=torch.int32, device=self.device)
-        st_d = torch.from_numpy(start).to(self.device)
-        flide._check(self._lib.flide_history_append(
-            ctypes.byref(index.c), flide._ptr(req), flide._ptr(st_d), flide._ptr(self.table),
-            self.max_blocks, self.block_rows, flide._ptr(k), flide._ptr(v), flide._ptr(self.pool_k),
-            flide._ptr(self.pool_v), self.Hkv, self.d, flide._dtype_code(k),
-            flide._ptr(node_state if self.H else None), self.H, self.dk, self.dv,
-            flide._ptr(self.pool_S), flide._stream()), "flide_history_append")
+        weighed = {s: self._weighed[s] for s in slots if s in self._weighed}
+        start = None
+        try:
+            # (rows of another type would be written past the pool's end)
+            flide._rows_like("commit", self.pool_k, k=k, v=v)
+            tokens = int(tree.arrays()[2].sum())
+            if min(k.shape[0], v.shape[0]) < tokens:
+                raise ValueError(f"commit: k and v need {tokens} rows, got {k.shape[0]} and {v.shape[0]}")
+            if self.H:
+                flide._states_like("commit", self.H, self.dv, self.dk, node_state=node_state)
+            pk, pv, ps = flide._ptr(k), flide._ptr(v), flide._ptr(node_state if self.H else None)
+            start = self.reserve(slots, tree)
+            req = torch.tensor(slots, dtype=torch.int32, device=self.device)
+            st_d = torch.from_numpy(start).to(self.device)
+            flide._check(self._lib.flide_history_append(
+                ctypes.byref(index.c), flide._ptr(req), flide._ptr(st_d), flide._ptr(self.table),
+                self.max_blocks, self.block_rows, pk, pv, flide._ptr(self.pool_k),
+                flide._ptr(self.pool_v), self.Hkv, self.d, flide._dtype_code(k), ps, self.H, self.dk,
+                self.dv, flide._ptr(self.pool_S), flide._stream()), "flide_history_append")
+        except Exception:
+            if start is not None:  # the rows are reserved, but nothing stands in them
+                for s, n in zip(slots, start):
+                    if s >= 0:
+                        self._lib.flide_pool_truncate(self._pool, s, int(n))
+                self._sync_table()
+            for s in weighed:
+                self._weighed.pop(s, None)
+            self._take_back(weighed)
+            raise
