@@ -731,7 +731,9 @@ int fork_attn_tc(const void *q, const void *k, const void *v, const void *pk, co
   prm.mtok = mtok;
   prm.has_past = has_past ? 1 : 0;
   prm.past_rows = has_past ? past_rows : 0;
-  prm.qk_log2 = scale * kLog2e;
+  // masked scores are -inf before they are scaled, and -inf times 0 would be NaN: a scale
+  // of 0 becomes 2^-100, which moves a score below 2^60 by less than 2^-40
+  prm.qk_log2 = scale == 0.f ? 0x1p-100f : scale * kLog2e;
   const long grid = (long)Hkv * ((x->T + 2 * mtok - 1) / (2 * mtok) + 2L * x->R);
   if (grid <= 0) return FLIDE_OK;
   if (grid > 0x7fffffffL) return FLIDE_ERR_CAPACITY;
